@@ -102,7 +102,8 @@ class HipEvents:
 # single-step and gated-activation kernels, the host-side discretisation
 # entry point, the C ABI layer's validation): edits there leave the traffic
 # record valid
-DIGEST_EXCLUDE = {"s5_step.hip", "s5_glu.hip", "s5_discretize.hip", "s5_api.cpp"}
+DIGEST_EXCLUDE = {"s5_step.hip", "s5_glu.hip", "s5_discretize.hip", "s5_api.cpp", "s5_qk.hip", "s5_delta.h",
+                  "s5_delta_api.cpp", "s5_delta_step.hip"}
 
 
 def kernel_source_digest() -> str:

@@ -30,6 +30,12 @@ __all__ = [
     "forward_timevarying_stateful",
     "set_profiling_events",
     "status_string",
+    "gated_delta",
+    "gated_delta_backward",
+    "gated_delta_step",
+    "qk_norm_rope",
+    "qk_norm_rope_backward",
+    "rope_frequencies",
 ]
 
 S5_F32 = 0
@@ -43,7 +49,8 @@ _lib = None
 
 EXPORTS = ("s5_discretize", "s5_forward", "s5_forward_noalloc", "s5_forward_timevarying", "s5_forward_stateful",
            "s5_forward_timevarying_stateful", "s5_forward_ex", "s5_step", "s5_glu", "s5_status_string",
-           "s5_set_profiling_events")
+           "s5_set_profiling_events", "s5_gated_delta_workspace", "s5_gated_delta", "s5_gated_delta_backward",
+           "s5_gated_delta_step", "s5_qk_workspace", "s5_qk_norm_rope", "s5_qk_norm_rope_backward")
 
 # option bits of s5_forward_ex (include/s5.h)
 FLAG_HALF_SPECTRUM = 1 << 0
@@ -52,6 +59,10 @@ FLAG_GELU = 1 << 2
 FLAG_BIDIRECTIONAL = 1 << 3
 FLAG_GELU_TANH = 1 << 4
 FLAG_GLU = 1 << 5
+# option bits of s5_qk_norm_rope
+QK_RMS = 1 << 0
+QK_L2 = 1 << 1
+QK_INTERLEAVED = 1 << 2
 
 
 class ForwardDesc(ctypes.Structure):
@@ -63,6 +74,26 @@ class ForwardDesc(ctypes.Structure):
                 ("delta", ctypes.c_void_p), ("x0", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("x_last", ctypes.c_void_p),
                 ("glu_w", ctypes.c_void_p), ("glu_bias", ctypes.c_void_p), ("glu_variant", ctypes.c_int32)]
+
+
+class DeltaDesc(ctypes.Structure):
+    """s5_delta_desc of include/s5.h."""
+    _fields_ = ([("size", ctypes.c_uint32), ("io", ctypes.c_int)] +
+                [(n, ctypes.c_int64) for n in ("B", "L", "Hk", "Hv", "Dk", "Dv", "q_stride", "k_stride", "v_stride")] +
+                [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta", "s0", "lengths", "y", "s_last", "dy",
+                                                "ds_last", "dq", "dk", "dv", "dg", "dbeta", "ds0", "workspace")] +
+                [("workspace_bytes", ctypes.c_int64)])
+
+
+class QkDesc(ctypes.Structure):
+    """s5_qk_desc of include/s5.h."""
+    _fields_ = ([("size", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("io", ctypes.c_int)] +
+                [(n, ctypes.c_int64) for n in ("T", "L", "Hq", "Hk", "D", "R", "q_stride", "k_stride")] +
+                [("eps", ctypes.c_float), ("rope_scale", ctypes.c_float)] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "q_weight", "k_weight", "freqs", "positions", "q_out", "k_out",
+                                                "dq_out", "dk_out", "dq_weight", "dk_weight", "workspace")] +
+                [("workspace_bytes", ctypes.c_int64)])
 
 
 class S5Error(RuntimeError):
@@ -105,6 +136,18 @@ def lib() -> ctypes.CDLL:
         L.s5_step.restype = st
         L.s5_glu.argtypes = [i64, i64, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp]
         L.s5_glu.restype = st
+        for name in ("s5_gated_delta", "s5_gated_delta_backward"):
+            getattr(L, name).argtypes = [ctypes.POINTER(DeltaDesc), vp]
+            getattr(L, name).restype = st
+        L.s5_gated_delta_workspace.argtypes = [ctypes.POINTER(DeltaDesc), ctypes.c_int, ctypes.POINTER(i64)]
+        L.s5_gated_delta_workspace.restype = st
+        L.s5_gated_delta_step.argtypes = [i64] * 5 + [ctypes.c_int] + [i64] * 3 + [ctypes.c_float] + [vp] * 8
+        L.s5_gated_delta_step.restype = st
+        for name in ("s5_qk_norm_rope", "s5_qk_norm_rope_backward"):
+            getattr(L, name).argtypes = [ctypes.POINTER(QkDesc), vp]
+            getattr(L, name).restype = st
+        L.s5_qk_workspace.argtypes = [ctypes.POINTER(QkDesc), ctypes.POINTER(i64)]
+        L.s5_qk_workspace.restype = st
         L.s5_status_string.argtypes = [st]
         L.s5_status_string.restype = ctypes.c_char_p
         L.s5_set_profiling_events.argtypes = [vp, ctypes.c_int]
@@ -386,3 +429,334 @@ def set_profiling_events(events) -> None:
     events = list(events or [])
     arr = (ctypes.c_void_p * max(1, len(events)))(*events) if events else None
     _check(lib().s5_set_profiling_events(arr, len(events)), "s5_set_profiling_events")
+
+
+# ---- gated delta rule, and the norm and rotation of its queries and keys ------
+
+
+class _On:
+    """The device of `t` as the current one and, if a stream is given, that
+    stream as torch's: outputs and workspaces are then allocated for the
+    stream that the kernels run on. Costs nothing where both already are."""
+
+    def __init__(self, t, stream):
+        import torch
+        self.contexts = []
+        if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(t.device))
+        if stream is not None:
+            if t.device.type == "cuda" and stream.device != t.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+
+    def __exit__(self, *e):
+        for c in reversed(self.contexts):
+            c.__exit__(*e)
+
+
+def _same_device(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+
+
+def _given(t, name, dtype, shape, device):
+    """Pointer of a checked contiguous tensor, None for None."""
+    if t is None:
+        return None
+    _dev_tensor(t, name, dtype, shape)
+    _same_device(t, name, device)
+    return t.data_ptr()
+
+
+def _made(t, name, dtype, shape, device, zero=False):
+    """A given output, checked, or a new one (filled with zeros if not every
+    row of it will be written)."""
+    import torch
+    if t is None:
+        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+    _given(t, name, dtype, shape, device)
+    return t
+
+
+def _heads(t, name, dtype, lead, device):
+    """Elements between the tokens of t [*lead, heads, features]: heads and
+    features contiguous, one distance between all tokens."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+    _same_device(t, name, device)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    n = len(lead)
+    if t.dim() != n + 2 or tuple(t.shape[:n]) != tuple(lead):
+        raise ValueError(f"{name} must have shape {tuple(lead)} + (heads, features), got {tuple(t.shape)}")
+    H, D = t.shape[n:]
+    if H < 1 or D < 1:
+        raise ValueError(f"{name} must have heads and features, got {tuple(t.shape)}")
+    st = t.stride()
+    row = H * D
+    if t.numel() == 0 or t.is_contiguous():
+        return row
+    if (D > 1 and st[n + 1] != 1) or (H > 1 and st[n] != D):
+        raise ValueError(f"{name}: the heads and features of a token must be contiguous, got strides {st}")
+    ld, rows = None, 1   # from the innermost leading dimension outwards
+    for size, stride in zip(reversed(lead), reversed(st[:n])):
+        if size > 1:
+            if ld is None:
+                ld = stride // rows if stride % rows == 0 else -1
+            elif stride != ld * rows:
+                raise ValueError(f"{name}: tokens must lie at one distance, got strides {st}")
+        rows *= size
+    if ld is None:
+        ld = row
+    if ld < row:
+        raise ValueError(f"{name}: tokens overlap, got strides {st}")
+    return ld
+
+
+def _workspace(nbytes, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _delta_desc(q, k, v, g, beta, s0, scale, lengths):
+    import torch
+    if v.dim() != 4:
+        raise ValueError("v must be [B, L, Hv, Dv]")
+    B, L, Hv, Dv = v.shape
+    dev, io = v.device, _io_code(v.dtype)
+    ldv = _heads(v, "v", v.dtype, (B, L), dev)
+    ldk = _heads(k, "k", v.dtype, (B, L), dev)
+    ldq = _heads(q, "q", v.dtype, (B, L), dev)
+    Hk, Dk = k.shape[2:]
+    if q.shape != k.shape:
+        raise ValueError(f"q and k must have one shape, got {tuple(q.shape)} and {tuple(k.shape)}")
+    if Hv % Hk:
+        raise ValueError(f"the value heads ({Hv}) must be a multiple of the key heads ({Hk})")
+    f32 = torch.float32
+    d = DeltaDesc(ctypes.sizeof(DeltaDesc), io, B, L, Hk, Hv, Dk, Dv, ldq, ldk, ldv,
+                  Dk ** -0.5 if scale is None else float(scale), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                  _given(g, "g", f32, (B, L, Hv), dev), _given(beta, "beta", f32, (B, L, Hv), dev),
+                  _given(s0, "s0", f32, (B, Hv, Dk, Dv), dev), _given(lengths, "lengths", torch.int32, (B,), dev))
+    return d, dev
+
+
+def _run_delta(desc, backward, stream, device):
+    L = lib()
+    need = ctypes.c_int64()
+    name = "s5_gated_delta_backward" if backward else "s5_gated_delta"
+    _check(L.s5_gated_delta_workspace(ctypes.byref(desc), int(backward), ctypes.byref(need)), name)
+    ws = _workspace(need.value, device)
+    if ws is not None:
+        desc.workspace, desc.workspace_bytes = ws.data_ptr(), need.value
+    _check(getattr(L, name)(ctypes.byref(desc), _stream_handle(stream)), name)
+
+
+def gated_delta(q, k, v, g, beta, s0=None, *, scale=None, lengths=None, final_state=False, y=None, s_last=None,
+                stream=None):
+    """The gated delta rule (s5_gated_delta) over whole sequences:
+    S_t = a_t S_{t-1} + k_t u_t^T, u_t = beta_t (v_t - a_t S_{t-1}^T k_t),
+    y_t = scale S_t^T q_t, a_t = exp(g_t).
+
+    q, k [B, L, Hk, Dk] and v [B, L, Hv, Dv], float32 or bfloat16, may be slices
+    of one projection (the heads of a token contiguous, one distance between
+    tokens); value head h reads key head h // (Hv // Hk). g, beta [B, L, Hv]
+    float32; s0 [B, Hv, Dk, Dv] float32 or None (zero); scale None is
+    Dk ** -0.5. lengths [B] int32: the valid steps of each sequence; rows of y
+    behind them are zero in a y made here and left as they were in a given one.
+    Returns (y, s_last), s_last None unless final_state is set or a buffer is
+    given (which may be s0)."""
+    import torch
+    with _On(v, stream):
+        d, dev = _delta_desc(q, k, v, g, beta, s0, scale, lengths)
+        B, L, Hv, Dv = v.shape
+        y = _made(y, "y", v.dtype, (B, L, Hv, Dv), dev, zero=lengths is not None)
+        if final_state or s_last is not None:
+            s_last = _made(s_last, "s_last", torch.float32, (B, Hv, d.Dk, Dv), dev)
+            d.s_last = s_last.data_ptr()
+        d.y = y.data_ptr()
+        _run_delta(d, False, stream, dev)
+    return y, s_last
+
+
+def gated_delta_backward(dy, q, k, v, g, beta, s0=None, ds_last=None, *, scale=None, lengths=None, dq=None, dk=None,
+                         dv=None, dg=None, dbeta=None, ds0=None, stream=None):
+    """Gradients of gated_delta (s5_gated_delta_backward) from dy, the gradient
+    of y, and ds_last, that of the last state (None: zero); the forward pass is
+    computed again, nothing is kept from it. Returns (dq, dk, dv, dg, dbeta,
+    ds0), ds0 None unless s0 or a buffer for it is given. With lengths the
+    rows behind are zero in gradients made here and left in given ones."""
+    import torch
+    with _On(v, stream):
+        d, dev = _delta_desc(q, k, v, g, beta, s0, scale, lengths)
+        B, L, Hv, Dv = v.shape
+        f32, zero = torch.float32, lengths is not None
+        d.dy = _given(dy, "dy", v.dtype, (B, L, Hv, Dv), dev)
+        d.ds_last = _given(ds_last, "ds_last", f32, (B, Hv, d.Dk, Dv), dev)
+        dq = _made(dq, "dq", v.dtype, tuple(q.shape), dev, zero)
+        dk = _made(dk, "dk", v.dtype, tuple(k.shape), dev, zero)
+        dv = _made(dv, "dv", v.dtype, (B, L, Hv, Dv), dev, zero)
+        dg = _made(dg, "dg", f32, (B, L, Hv), dev, zero)
+        dbeta = _made(dbeta, "dbeta", f32, (B, L, Hv), dev, zero)
+        if s0 is not None or ds0 is not None:
+            ds0 = _made(ds0, "ds0", f32, (B, Hv, d.Dk, Dv), dev)
+            d.ds0 = ds0.data_ptr()
+        d.dq, d.dk, d.dv, d.dg, d.dbeta = (t.data_ptr() for t in (dq, dk, dv, dg, dbeta))
+        _run_delta(d, True, stream, dev)
+    return dq, dk, dv, dg, dbeta, ds0
+
+
+def gated_delta_step(q, k, v, g, beta, s, *, scale=None, y=None, stream=None):
+    """One token of gated_delta for each of B sequences (s5_gated_delta_step):
+    q, k [B, Hk, Dk], v [B, Hv, Dv], g, beta [B, Hv]; s [B, Hv, Dk, Dv] float32
+    is updated in place. Returns y [B, Hv, Dv]."""
+    import torch
+    if v.dim() != 3:
+        raise ValueError("v must be [B, Hv, Dv]")
+    B, Hv, Dv = v.shape
+    dev, io = v.device, _io_code(v.dtype)
+    with _On(v, stream):
+        ldv = _heads(v, "v", v.dtype, (B,), dev)
+        ldk = _heads(k, "k", v.dtype, (B,), dev)
+        ldq = _heads(q, "q", v.dtype, (B,), dev)
+        Hk, Dk = k.shape[1:]
+        if q.shape != k.shape:
+            raise ValueError(f"q and k must have one shape, got {tuple(q.shape)} and {tuple(k.shape)}")
+        if Hv % Hk:
+            raise ValueError(f"the value heads ({Hv}) must be a multiple of the key heads ({Hk})")
+        gp = _given(g, "g", torch.float32, (B, Hv), dev)
+        bp = _given(beta, "beta", torch.float32, (B, Hv), dev)
+        sp = _given(s, "s", torch.float32, (B, Hv, Dk, Dv), dev)
+        y = _made(y, "y", v.dtype, (B, Hv, Dv), dev)
+        _check(lib().s5_gated_delta_step(B, Hk, Hv, Dk, Dv, io, ldq, ldk, ldv, Dk ** -0.5 if scale is None else scale,
+                                         q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp, sp, y.data_ptr(),
+                                         _stream_handle(stream)), "s5_gated_delta_step")
+    return y
+
+
+def _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, interleaved):
+    import torch
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [T, Hq, D] or [B, L, Hq, D]")
+    lead, dev, io = tuple(q.shape[:-2]), q.device, _io_code(q.dtype)
+    ldq = _heads(q, "q", q.dtype, lead, dev)
+    ldk = _heads(k, "k", q.dtype, lead, dev)
+    (Hq, D), Hk = q.shape[-2:], k.shape[-2]
+    if k.shape[-1] != D:
+        raise ValueError(f"the heads of q and k must have one size, got {D} and {k.shape[-1]}")
+    flags = {"rms": QK_RMS, "l2": QK_L2, None: 0}.get(norm)
+    if flags is None:
+        raise ValueError(f"norm must be 'rms', 'l2' or None, got {norm!r}")
+    if norm is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights need a norm")
+    R = 0
+    if freqs is not None:
+        R = 2 * freqs.numel()
+        if freqs.dim() != 1 or R > D:
+            raise ValueError(f"freqs must be [R/2] with R <= {D}, got {tuple(freqs.shape)}")
+    T = 1
+    for n in lead:
+        T *= n
+    d = QkDesc(ctypes.sizeof(QkDesc), flags | (QK_INTERLEAVED if interleaved else 0), io, T, max(1, lead[-1]), Hq, Hk, D, R,
+               ldq, ldk, eps, rope_scale, q.data_ptr(), k.data_ptr(),
+               _given(q_weight, "q_weight", torch.float32, (D,), dev), _given(k_weight, "k_weight", torch.float32, (D,), dev),
+               _given(freqs, "freqs", torch.float64, (R // 2,), dev) if R else None,
+               _given(positions, "positions", torch.int32, lead, dev))
+    return d, dev
+
+
+def qk_norm_rope(q, k, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, freqs=None, positions=None, rope_scale=1.0,
+                 interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norm of each query and key head and rotation of its first features by
+    its token's position, in one pass (s5_qk_norm_rope): n = x w / sqrt(m + eps)
+    with m the mean ("rms") or sum ("l2") of x^2 (norm None: n = x), then each
+    pair (a, b) of the first R features becomes rope_scale (a cos - b sin,
+    b cos + a sin) at position * freqs.
+
+    q [B, L, Hq, D] or [T, Hq, D], k with Hk heads, float32 or bfloat16, may be
+    slices of one projection; weights [D] float32 or None. freqs [R/2] float64
+    radians per position (rope_frequencies), None: no rotation; pairs are
+    (j, j + R/2), or (2j, 2j + 1) if interleaved. positions int32, shaped as
+    the tokens; None counts 0, 1, ... along L (T). Returns contiguous
+    (q_out, k_out); a contiguous input may be its own output."""
+    with _On(q, stream):
+        d, dev = _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, interleaved)
+        q_out = _made(q_out, "q_out", q.dtype, tuple(q.shape), dev)
+        k_out = _made(k_out, "k_out", q.dtype, tuple(k.shape), dev)
+        d.q_out, d.k_out = q_out.data_ptr(), k_out.data_ptr()
+        _check(lib().s5_qk_norm_rope(ctypes.byref(d), _stream_handle(stream)), "s5_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, freqs=None,
+                          positions=None, rope_scale=1.0, interleaved=False, dq=None, dk=None, dq_weight=None,
+                          dk_weight=None, stream=None):
+    """Gradients of qk_norm_rope (s5_qk_norm_rope_backward) from dq_out and
+    dk_out, those of its results, with its inputs and options. Returns
+    (dq, dk, dq_weight, dk_weight), a weight's gradient None without the
+    weight."""
+    import torch
+    with _On(q, stream):
+        d, dev = _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, interleaved)
+        d.dq_out = _given(dq_out, "dq_out", q.dtype, tuple(q.shape), dev)
+        d.dk_out = _given(dk_out, "dk_out", q.dtype, tuple(k.shape), dev)
+        dq = _made(dq, "dq", q.dtype, tuple(q.shape), dev)
+        dk = _made(dk, "dk", q.dtype, tuple(k.shape), dev)
+        if q_weight is not None or dq_weight is not None:
+            dq_weight = _made(dq_weight, "dq_weight", torch.float32, (d.D,), dev)
+            d.dq_weight = dq_weight.data_ptr()
+        if k_weight is not None or dk_weight is not None:
+            dk_weight = _made(dk_weight, "dk_weight", torch.float32, (d.D,), dev)
+            d.dk_weight = dk_weight.data_ptr()
+        d.q_out, d.k_out = dq.data_ptr(), dk.data_ptr()
+        need = ctypes.c_int64()
+        _check(lib().s5_qk_workspace(ctypes.byref(d), ctypes.byref(need)), "s5_qk_norm_rope_backward")
+        ws = _workspace(need.value, dev)
+        if ws is not None:
+            d.workspace, d.workspace_bytes = ws.data_ptr(), need.value
+        _check(lib().s5_qk_norm_rope_backward(ctypes.byref(d), _stream_handle(stream)), "s5_qk_norm_rope_backward")
+    return dq, dk, dq_weight, dk_weight
+
+
+def rope_frequencies(rotary_dim, base=10000.0, *, factor=1.0, scaling=None, original_length=None, fast=32.0, slow=1.0,
+                     device="cuda"):
+    """Radians per position of each of the rotary_dim / 2 pairs, float64:
+    base ** (-2 j / rotary_dim), changed for contexts `factor` times longer than
+    trained by `scaling`:
+      None      as they are
+      "linear"  all divided by factor (positions squeezed together)
+      "base"    the base times factor ** (R / (R - 2)): the fastest pair keeps its
+                frequency, the slowest is divided by factor
+      "parts"   pairs that turn at least `fast` times over original_length stay,
+                those with at most `slow` turns are divided by factor, those
+                between in proportion to their turns
+    The factor that goes with "parts" (rope_scale) is 0.1 log(factor) + 1."""
+    import math
+
+    import torch
+    R = int(rotary_dim)
+    if R < 2 or R % 2:
+        raise ValueError(f"rotary_dim must be even and >= 2, got {rotary_dim}")
+    if not (base > 0 and math.isfinite(base)) or not (factor >= 1 and math.isfinite(factor)):
+        raise ValueError("base must be > 0 and factor >= 1")
+    if scaling == "base":
+        if R < 4:
+            raise ValueError("scaling 'base' needs two pairs")
+        base = base * factor ** (R / (R - 2))
+    f = base ** (-torch.arange(0, R, 2, dtype=torch.float64) / R)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if original_length is None or original_length < 1 or not fast > slow > 0:
+            raise ValueError("scaling 'parts' needs original_length >= 1 and fast > slow > 0")
+        keep = ((original_length * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    elif scaling not in (None, "base"):
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts', got {scaling!r}")
+    return f.to(device)

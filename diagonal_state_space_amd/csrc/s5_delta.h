@@ -1,0 +1,64 @@
+// Internal launcher declarations of the gated delta rule and of the pass that
+// prepares its queries and keys (validated arguments; include/s5.h has the
+// contracts).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace s5 {
+
+// Norm and rotation of query and key heads: rows of T tokens and Hq + Hk heads.
+struct QkArgs {
+  int64_t T, L;            // tokens; position of token t without `positions`: t % L
+  int Hq, Hk, D, R;        // heads, features of a head, rotated features (even, <= D)
+  int64_t ldq, ldk;        // elements between the tokens of q and of k
+  bool bf16_io, interleaved, norm;
+  float inv_m;             // 1/D (root mean square) or 1 (Euclidean)
+  float eps, rope_scale;
+  const void *q, *k;
+  const float *wq, *wk;    // [D] or null
+  const double* freqs;     // [R/2] radians per position
+  const int32_t* positions;  // [T] or null
+  void *q_out, *k_out;     // contiguous; backward: the gradients of q and k
+  // backward only
+  const void *dq_out, *dk_out;   // contiguous
+  float *dwq, *dwk;              // [D] or null
+  float* partials;               // qk_partial_blocks() * 2 * D floats, with dwq or dwk
+};
+
+// workgroups of the backward pass, each of which leaves one row of partial
+// weight gradients
+int qk_partial_blocks(const QkArgs& a);
+hipError_t launch_qk(const QkArgs& a, bool backward, hipStream_t stream);
+hipError_t launch_zero(float* p, int n, hipStream_t stream);
+
+// Gated delta rule over B sequences of up to L tokens.
+struct DeltaArgs {
+  int B, L, Hk, Hv, Dk, Dv;
+  int64_t ldq, ldk, ldv;   // elements between the tokens of q, k and v
+  bool bf16_io;
+  float scale;
+  const void *q, *k, *v;
+  const float *g, *beta;   // [B, L, Hv]
+  const float* s0;         // [B, Hv, Dk, Dv] or null (zero)
+  const int32_t* lengths;  // [B] or null (all L)
+  void* y;                 // [B, L, Hv, Dv]
+  float* s_last;           // [B, Hv, Dk, Dv] or null; may be s0 itself
+  void* ws;
+  // backward only
+  const void* dy;
+  const float* ds_last;    // or null (zero)
+  void *dq, *dk, *dv;
+  float *dg, *dbeta;
+  float* ds0;              // or null
+};
+
+// one token after the other, the state in registers
+hipError_t launch_delta_tokens(const DeltaArgs& a, hipStream_t stream);
+
+// whole sequences; bytes of workspace they need
+int64_t delta_workspace(const DeltaArgs& a, bool backward);
+hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream);
+
+}  // namespace s5

@@ -341,6 +341,192 @@ s5_status s5_glu(int64_t T, int64_t H, s5_dtype io, int variant, const void* y, 
                  const float* bias, void* out, hipStream_t stream);
 
 /*
+ * s5_gated_delta - the gated delta rule, a linear recurrence whose state is a
+ * matrix for each head. With a_t = exp(g_t), for value head h of Hv, which
+ * reads query and key head h / (Hv / Hk) (integer division):
+ *     u_t = beta_t (v_t - (a_t S_{t-1})^T k_t)
+ *     S_t = a_t S_{t-1} + k_t u_t^T                    S in R^{Dk x Dv}
+ *     y_t = scale S_t^T q_t
+ * s5_gated_delta_backward gives the gradients of all its inputs from those of
+ * y and of the last state; s5_gated_delta_step is one token for each of B
+ * sequences, the state updated in place. The rule is used with keys of unit
+ * length and beta in [0, 2] (s5_qk_norm_rope prepares them); the keys and
+ * strengths of another scale are computed as given and may grow without bound.
+ *
+ * Fields of s5_delta_desc (one struct for the forward and backward calls):
+ *   size        sizeof(s5_delta_desc)
+ *   io          element type of q, k, v, y and of dq, dk, dv, dy
+ *   B, L        sequences and steps of the arrays (>= 0)
+ *   Hk, Hv      query/key heads and value heads; Hv a multiple of Hk
+ *   Dk, Dv      features of a key (1..S5_DELTA_MAX_DK) and of a value
+ *               (1..S5_DELTA_MAX_DV)
+ *   q_stride, k_stride, v_stride   elements from one token to the next (>=
+ *               Hk*Dk, Hk*Dk, Hv*Dv), so that q, k and v may be slices of one
+ *               projection's output; token (b, t) is row b*L + t
+ *   scale       factor of y
+ *   q, k [B,L,Hk,Dk], v [B,L,Hv,Dv]   rows of a token contiguous, aligned to
+ *               their element
+ *   g, beta     [B,L,Hv] float32 log decay (<= 0; -inf clears the state) and
+ *               write strength
+ *   s0          [B,Hv,Dk,Dv] float32 state before step 0, or NULL (zero)
+ *   lengths     [B] int32 valid steps of each sequence (clamped to 0..L), or
+ *               NULL (all L). Steps at and behind the length are not read,
+ *               their rows of the outputs not written, and the last state is
+ *               that after the last valid step.
+ *   y           [B,L,Hv,Dv] out (forward)
+ *   s_last      [B,Hv,Dk,Dv] float32 out (forward), or NULL; may be s0 itself
+ *   dy          [B,L,Hv,Dv] gradient of y (backward)
+ *   ds_last     [B,Hv,Dk,Dv] float32 gradient of the last state, or NULL (zero)
+ *   dq, dk, dv  out (backward), contiguous [B,L,Hk,Dk], [B,L,Hk,Dk],
+ *               [B,L,Hv,Dv]; dq and dk sum over the value heads of their head
+ *   dg, dbeta   [B,L,Hv] float32 out (backward); dg is 0 where g is -inf
+ *   ds0         [B,Hv,Dk,Dv] float32 out (backward), or NULL
+ *   workspace, workspace_bytes   device memory of at least the bytes that
+ *               s5_gated_delta_workspace gives for the call, 256-byte aligned
+ *               (NULL where that is 0). It holds nothing between calls; two
+ *               calls that may run at once need two.
+ * All other arrays contiguous and 16-byte aligned (g, beta, lengths: to their
+ * element). The fields of the other direction are ignored. The current device
+ * is the arrays'. Nothing is allocated: the calls can be captured in a graph.
+ * Precision: the state, sums and decays are float32, products with float32
+ * values as exact as float32 products (on the matrix cores as three bf16
+ * parts), so for bf16 io only the outputs of type io are rounded to bf16.
+ * The result of a call does not depend on the launch order (no atomics).
+ * Errors: S5_ERR_INVALID_ARGUMENT (null pointer, wrong size field, negative
+ * B or L, heads or features < 1, Hv not a multiple of Hk, a token stride below
+ * the row, a scale that is not finite, workspace too small, an output
+ * overlapping an input or another output), S5_ERR_UNSUPPORTED (io, feature
+ * limits, B*L or B*Hv*Dv above INT32_MAX, misalignment), S5_ERR_HIP.
+ */
+#define S5_DELTA_MAX_DK 128
+#define S5_DELTA_MAX_DV 512
+
+typedef struct {
+  uint32_t size;
+  s5_dtype io;
+  int64_t B, L, Hk, Hv, Dk, Dv;
+  int64_t q_stride, k_stride, v_stride;
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  const float* s0;
+  const int32_t* lengths;
+  void* y;
+  float* s_last;
+  const void* dy;
+  const float* ds_last;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dg;
+  float* dbeta;
+  float* ds0;
+  void* workspace;
+  int64_t workspace_bytes;
+} s5_delta_desc;
+
+/* Bytes of workspace of the forward (backward = 0) or backward call; reads
+ * io, the sizes and whether optional arrays are given. */
+s5_status s5_gated_delta_workspace(const s5_delta_desc* desc, int backward, int64_t* bytes);
+s5_status s5_gated_delta(const s5_delta_desc* desc, hipStream_t stream);
+s5_status s5_gated_delta_backward(const s5_delta_desc* desc, hipStream_t stream);
+
+/*
+ * s5_gated_delta_step - one token of s5_gated_delta for each of B sequences:
+ * q, k [B,Hk,Dk], v [B,Hv,Dv] (row strides as above), g, beta [B,Hv], s
+ * [B,Hv,Dk,Dv] float32 read and overwritten in place, y [B,Hv,Dv] out. Equal,
+ * up to rounding, to s5_gated_delta with L = 1 and s0 = s_last = s. The sums
+ * run on the vector units in float32. Errors as s5_gated_delta.
+ */
+s5_status s5_gated_delta_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, s5_dtype io,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                              const void* q, const void* k, const void* v, const float* g,
+                              const float* beta, float* s, void* y, hipStream_t stream);
+
+/*
+ * s5_qk_norm_rope - prepares queries and keys: each head's vector normalised,
+ * scaled by a weight and its first R features rotated by its token's position,
+ * in one pass over q and k:
+ *     n = x / sqrt(m + eps) * w,  m = mean of x^2 (S5_QK_RMS) or sum of x^2
+ *                                 (S5_QK_L2); n = x with neither flag
+ *     pair j of R/2 is features (j, j + R/2), with S5_QK_INTERLEAVED (2j, 2j + 1):
+ *     (a, b) -> rope_scale (a cos - b sin, b cos + a sin) at position * freqs[j]
+ *     features from R on: n
+ * s5_qk_norm_rope_backward gives the gradients of q, k and the weights from
+ * those of the outputs; nothing is kept between the calls.
+ *
+ * Fields of s5_qk_desc:
+ *   size        sizeof(s5_qk_desc)
+ *   flags       S5_QK_* bits (RMS and L2 exclude each other)
+ *   io          element type of q, k and all gradients but the weights'
+ *   T, L        tokens (>= 0; 0 is a no-op) and steps of a sequence (>= 1): without
+ *               `positions` token t has position t % L
+ *   Hq, Hk, D   heads of q and of k (>= 1), features of a head (1..S5_QK_MAX_D)
+ *   R           rotated features, even, 0..D (0: none; freqs is then ignored)
+ *   q_stride, k_stride   elements from one token to the next (>= Hq*D, Hk*D)
+ *   eps         added under the root (> 0 with a norm)
+ *   rope_scale  factor of the rotation (1, or the attention factor that goes
+ *               with stretched frequencies)
+ *   q, k        [T,Hq,D], [T,Hk,D], heads of a token contiguous, aligned to
+ *               their element
+ *   q_weight, k_weight   [D] float32, or NULL (ones); only with a norm
+ *   freqs       [R/2] float64 radians per position (any scaling for long
+ *               contexts is in them); angles are reduced in float64
+ *   positions   [T] int32, or NULL
+ *   q_out, k_out   forward: results; backward: the gradients of q and k;
+ *               contiguous. A contiguous q (k) may be its own q_out (k_out).
+ *   dq_out, dk_out   [T,Hq,D], [T,Hk,D] contiguous gradients of the results
+ *               (backward); may be q_out and k_out themselves
+ *   dq_weight, dk_weight   [D] float32 out (backward), or NULL; only where
+ *               the weight is given
+ *   workspace, workspace_bytes   as in s5_delta_desc; s5_qk_workspace gives
+ *               the bytes of the backward call (the forward call needs none)
+ * Contiguous arrays and the weights 16-byte aligned (freqs, positions: to
+ * their element).
+ * Precision: float32 (the weight gradients' last sum in float64, in a fixed
+ * order), one rounding to io.
+ * Errors: S5_ERR_INVALID_ARGUMENT (null pointer, wrong size field, unknown or
+ * excluded flags, weights or their gradients without a norm or weight, T < 0,
+ * L, Hq, Hk or D < 1, R odd or outside 0..D, a stride below the row, eps not
+ * finite or not > 0 with a norm, rope_scale not finite, workspace too small,
+ * overlaps), S5_ERR_UNSUPPORTED (io, D above the limit, T*(Hq+Hk) above
+ * INT32_MAX, misalignment), S5_ERR_HIP.
+ */
+#define S5_QK_MAX_D 256
+enum { S5_QK_RMS = 1u << 0, S5_QK_L2 = 1u << 1, S5_QK_INTERLEAVED = 1u << 2 };
+
+typedef struct {
+  uint32_t size;
+  uint32_t flags;
+  s5_dtype io;
+  int64_t T, L, Hq, Hk, D, R;
+  int64_t q_stride, k_stride;
+  float eps;
+  float rope_scale;
+  const void* q;
+  const void* k;
+  const float* q_weight;
+  const float* k_weight;
+  const double* freqs;
+  const int32_t* positions;
+  void* q_out;
+  void* k_out;
+  const void* dq_out;
+  const void* dk_out;
+  float* dq_weight;
+  float* dk_weight;
+  void* workspace;
+  int64_t workspace_bytes;
+} s5_qk_desc;
+
+s5_status s5_qk_workspace(const s5_qk_desc* desc, int64_t* bytes);
+s5_status s5_qk_norm_rope(const s5_qk_desc* desc, hipStream_t stream);
+s5_status s5_qk_norm_rope_backward(const s5_qk_desc* desc, hipStream_t stream);
+
+/*
  * s5_forward_noalloc - s5_forward for callers that cannot allocate device
  * memory: code under HIP graph capture, tight serving loops, and harnesses
  * that forbid hipMalloc. Same arguments, same kernels, same results (bit for
