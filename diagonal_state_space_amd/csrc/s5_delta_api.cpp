@@ -53,7 +53,9 @@ s5_status delta_sizes(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, 
   constexpr int64_t kMost = int64_t{1} << 28;   // spans in bytes stay below 2^63
   if (ldq > kMost || ldk > kMost || ldv > kMost) return S5_ERR_UNSUPPORTED;
   if (B > 0 && (L > INT32_MAX / B || Hv * Dv > INT32_MAX / B)) return S5_ERR_UNSUPPORTED;
-  if (B > 0 && L > 0 && Hv > INT64_C(0x7fffffffff) / (B * L)) return S5_ERR_UNSUPPORTED;
+  // workgroups of 256 threads, one for each chunk of 32 or 64 steps and head
+  constexpr int64_t kGroups = (int64_t{1} << 24) - 1;
+  if (B > 0 && (Hv > kGroups / B / 16 || (L + 31) / 32 > kGroups / (B * Hv))) return S5_ERR_UNSUPPORTED;
   return S5_OK;
 }
 

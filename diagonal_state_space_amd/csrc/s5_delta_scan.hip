@@ -1,0 +1,311 @@
+// Second kernel of the chunked gated delta rule: the chunks of a sequence one
+// after the other, the state in registers.
+//
+// Columns of the state are independent, so each wave owns 16 columns of one
+// head's state (as accumulator tiles) and needs nothing from the others: per
+// chunk, with the fragments of T and P of the first kernel,
+//   X = K S,  O = Q S,  R = beta (V - from X),  U = T R,
+//   y = scale (from O + P U),  S <- whole S + K^T (to U).
+// Every result is the next product's operand as it lies in the accumulators
+// (the fragments' product order is that of two tiles), so the chain runs
+// without an exchange or a barrier. What the waves share - k, its transpose,
+// q, T and P of the chunk - is staged in LDS once for the workgroup, fetched
+// into registers one chunk ahead.
+// The state's chain is exact to float32 (three bf16 parts); what only reaches
+// y of bf16 io takes two parts.
+//
+// A value that is not finite must not reach earlier steps through a zero of T
+// or P: rows from the first such one on are taken out of R for this column and
+// set to NaN in the results, the state's column too.
+#include "s5_delta_tile.h"
+
+namespace s5 {
+
+using namespace delta;
+
+namespace {
+
+constexpr float kNaN = __builtin_nanf("");
+
+template <bool BF16, int KP, int NW, bool KEEP>
+struct Scan {
+  static constexpr int C = chunk_of<BF16>();
+  static constexpr int NI = BF16 ? 1 : 3;      // parts of k and q
+  static constexpr int NO = BF16 ? 2 : 3;      // parts on the way to y
+  static constexpr int KS = KP / 32, MT = C / 16, CS = C / 32, KT = KP / 16;
+  static constexpr int kThreads = 64 * NW;
+  static constexpr int kBlocks = (C / 4) * (KP / 8);            // staged blocks of k
+  static constexpr int kJobs = (kBlocks + kThreads - 1) / kThreads;
+  // what of the chunk's record is staged: T, P and the decays, or T and the decays
+  static constexpr int kRecT = tri_frags<C>() * 3 * kFrag;
+  static constexpr int kRec = (KEEP ? kRecT : Record<C>::decays(false, NO)) + 4 * C * 4;
+  static constexpr int kRecJobs = (kRec / 16 + kThreads - 1) / kThreads;
+  static constexpr int oK = 0, oKT = oK + MT * KS * NI * kFrag, oQ = oKT + KT * CS * NI * kFrag;
+  static constexpr int oRec = oQ + (KEEP ? 0 : MT * KS * NI * kFrag);
+  static constexpr int kLds = oRec + kRec;
+};
+
+// KEEP: no outputs; the states at the chunks' starts and U are stored for the
+// backward pass (keep_s [bh][chunk][Dk][Dv], keep_u [bh][chunk][C][Dv])
+template <bool BF16, int KP, int NW, bool KEEP>
+__global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks, int groups, bool vec, float* keep_s, float* keep_u) {
+  using Z = Scan<BF16, KP, NW, KEEP>;
+  constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // workgroups go round the eight dies one by one: the column groups of a head
+  // follow each other on one die, whose L2 then holds what they share
+  const int die = blockIdx.x & 7, turn = blockIdx.x >> 3;
+  const int bh = (turn / groups) * 8 + die, cg = turn % groups;
+  if (bh >= a.B * a.Hv) return;
+  const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / (a.Hv / a.Hk);
+  const int col = (cg * NW + w) * 16 + m;
+  const bool wave_live = (cg * NW + w) * 16 < a.Dv, live = col < a.Dv;
+  const int len = length_of(a, b);
+  const int nc = (len + C - 1) / C;
+  constexpr int64_t es = BF16 ? 2 : 4;
+
+  f32x4 S[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * t + 4 * g + r;
+      S[t][r] = a.s0 != nullptr && live && row < a.Dk ? a.s0[(static_cast<int64_t>(bh) * a.Dk + row) * a.Dv + col] : 0.0f;
+    }
+
+  Block<BF16> kb[Z::kJobs], qb[Z::kJobs];
+  uint4 rb[Z::kRecJobs];
+  float vb[MT][4];
+  auto fetch = [&](int n) {
+    const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
+    const Rows kr{static_cast<const char*>(a.k) + (tok * a.ldk + static_cast<int64_t>(hk) * a.Dk) * es, a.ldk, len - n * C, a.Dk, vec};
+    const Rows qr{static_cast<const char*>(a.q) + (tok * a.ldq + static_cast<int64_t>(hk) * a.Dk) * es, a.ldq, len - n * C, a.Dk, vec};
+#pragma unroll
+    for (int j = 0; j < Z::kJobs; ++j) {
+      const int i = tid + j * Z::kThreads;
+      if (i < Z::kBlocks) {
+        kb[j] = load_block<BF16>(kr, 4 * (i / (KP / 8)), 8 * (i % (KP / 8)));
+        if constexpr (!KEEP) qb[j] = load_block<BF16>(qr, 4 * (i / (KP / 8)), 8 * (i % (KP / 8)));
+      }
+    }
+    const unsigned char* rec = static_cast<const unsigned char*>(a.ws) +
+                               (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(KEEP, NO);
+#pragma unroll
+    for (int j = 0; j < Z::kRecJobs; ++j) {
+      int o = (tid + j * Z::kThreads) * 16;
+      if (o < Z::kRec) {
+        if (KEEP && o >= Z::kRecT) o += Record<C>::decays(true, NO) - Z::kRecT;
+        rb[j] = *reinterpret_cast<const uint4*>(rec + o);
+      }
+    }
+    const int64_t v0 = tok * a.ldv + static_cast<int64_t>(h) * a.Dv + col;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * t + 4 * g + r;
+        vb[t][r] = live && i < len - n * C ? load_el<BF16>(a.v, v0 + i * a.ldv) : 0.0f;
+      }
+  };
+
+  if (nc > 0) fetch(0);
+  for (int n = 0; n < nc; ++n) {
+    __syncthreads();   // the previous chunk's fragments are read
+#pragma unroll
+    for (int j = 0; j < Z::kJobs; ++j) {
+      const int i = tid + j * Z::kThreads;
+      if (i < Z::kBlocks) {
+        const Parts<BF16> p(kb[j]);
+        store_rows<BF16, KS>(smem + Z::oK, p, i / (KP / 8), i % (KP / 8));
+        store_cols<BF16, C>(smem + Z::oKT, p, i / (KP / 8), i % (KP / 8));
+        if constexpr (!KEEP) store_rows<BF16, KS>(smem + Z::oQ, Parts<BF16>(qb[j]), i / (KP / 8), i % (KP / 8));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < Z::kRecJobs; ++j) {
+      const int o = (tid + j * Z::kThreads) * 16;
+      if (o < Z::kRec) *reinterpret_cast<uint4*>(smem + Z::oRec + o) = rb[j];
+    }
+    float V[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) V[t][r] = vb[t][r];
+    __syncthreads();
+    if (n + 1 < nc) fetch(n + 1);
+    if (!wave_live) continue;
+
+    const unsigned char* rec = smem + Z::oRec;
+    const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - 4 * C * 4);
+    if constexpr (KEEP) {
+      float* p = keep_s + (static_cast<int64_t>(bh) * chunks + n) * a.Dk * a.Dv;
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * t + 4 * g + r;
+          if (live && row < a.Dk) p[static_cast<int64_t>(row) * a.Dv + col] = S[t][r];
+        }
+    }
+    f32x4 X[MT], O[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) X[t] = O[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const Frag<3> s = to_frag<3>(S[2 * ks], S[2 * ks + 1]);
+      const Frag<NO> so = to_frag<NO>(S[2 * ks], S[2 * ks + 1]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        X[t] = mma(read_rows<NI, KS>(smem + Z::oK, t, ks), s, X[t]);
+        if constexpr (!KEEP) O[t] = mma(read_rows<NI, KS>(smem + Z::oQ, t, ks), so, O[t]);
+      }
+    }
+    float from[MT][4];
+    float odd = 0.0f;   // NaN if anything is not finite
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const float4 f = *reinterpret_cast<const float4*>(dec + 16 * t + 4 * g);
+      const float4 be = *reinterpret_cast<const float4*>(dec + 2 * C + 16 * t + 4 * g);
+      const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        from[t][r] = ff[r];
+        X[t][r] = bb[r] * (V[t][r] - ff[r] * X[t][r]);
+        odd = fmaf(X[t][r], 0.0f, odd);
+      }
+    }
+    int first = reinterpret_cast<const int*>(dec)[3 * C + 1];
+    if (first < C || __any(odd != odd)) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (!(fabsf(X[t][r]) < INFINITY)) first = min(first, 16 * t + 4 * g + r);
+      first = min(first, __shfl_xor(first, 16));
+      first = min(first, __shfl_xor(first, 32));
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * t + 4 * g + r >= first) X[t][r] = 0.0f;
+    }
+    Frag<3> rf[CS];
+#pragma unroll
+    for (int ks = 0; ks < CS; ++ks) rf[ks] = to_frag<3>(X[2 * ks], X[2 * ks + 1]);
+    f32x4 U[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      U[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks <= t / 2; ++ks)
+        U[t] = mma(read_frag<3>(rec + Record<C>::T, tri_frag<C>(t, ks), 0), rf[ks], U[t]);
+    }
+    const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
+    if constexpr (KEEP) {
+      float* p = keep_u + (static_cast<int64_t>(bh) * chunks + n) * C * a.Dv;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = 16 * t + 4 * g + r;
+          if (live) p[static_cast<int64_t>(i) * a.Dv + col] = i < first ? U[t][r] : kNaN;
+        }
+    } else {
+      Frag<NO> uf[CS];
+#pragma unroll
+      for (int ks = 0; ks < CS; ++ks) uf[ks] = to_frag<NO>(U[2 * ks], U[2 * ks + 1]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[t][r] *= from[t][r];
+#pragma unroll
+        for (int ks = 0; ks <= t / 2; ++ks)
+          O[t] = mma(read_frag<NO>(rec + Record<C>::P, tri_frag<C>(t, ks), 0), uf[ks], O[t]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = 16 * t + 4 * g + r;
+          if (live && i < len - n * C)
+            store_el<BF16>(a.y, ((tok + i) * a.Hv + h) * a.Dv + col, i < first ? a.scale * O[t][r] : kNaN);
+        }
+      }
+    }
+    const float whole = dec[3 * C];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const float4 to = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
+      const float tt[4] = {to.x, to.y, to.z, to.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) U[t][r] *= tt[r];
+    }
+    Frag<3> ud[CS];
+#pragma unroll
+    for (int ks = 0; ks < CS; ++ks) ud[ks] = to_frag<3>(U[2 * ks], U[2 * ks + 1]);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[t][r] *= whole;
+#pragma unroll
+      for (int ks = 0; ks < CS; ++ks) S[t] = mma(read_cols<NI, C>(smem + Z::oKT, t, ks), ud[ks], S[t]);
+      if (first < C) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[t][r] = kNaN;
+      }
+    }
+  }
+
+  if (a.s_last != nullptr && live) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * t + 4 * g + r;
+        if (row < a.Dk) a.s_last[(static_cast<int64_t>(bh) * a.Dk + row) * a.Dv + col] = S[t][r];
+      }
+  }
+}
+
+template <bool BF16, int KP, bool KEEP>
+hipError_t run(const DeltaArgs& a, float* keep_s, float* keep_u, hipStream_t stream) {
+  constexpr int NW = 4;
+  using Z = Scan<BF16, KP, NW, KEEP>;
+  auto* kern = k_delta_scan<BF16, KP, NW, KEEP>;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
+  if (attr != hipSuccess) return attr;
+  const int chunks = (a.L + Z::C - 1) / Z::C;
+  const int groups = (a.Dv + 16 * NW - 1) / (16 * NW);
+  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups;
+  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(Z::kThreads), Z::kLds, stream>>>(a, chunks, groups, delta_vectored(a),
+                                                                                     keep_s, keep_u);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_scan(const DeltaArgs& a, float* keep_s, float* keep_u, hipStream_t stream) {
+  const bool wide = a.Dk > 64, keep = keep_s != nullptr;
+  if (a.bf16_io) {
+    if (keep) return wide ? run<true, 128, true>(a, keep_s, keep_u, stream) : run<true, 64, true>(a, keep_s, keep_u, stream);
+    return wide ? run<true, 128, false>(a, nullptr, nullptr, stream) : run<true, 64, false>(a, nullptr, nullptr, stream);
+  }
+  if (keep) return wide ? run<false, 128, true>(a, keep_s, keep_u, stream) : run<false, 64, true>(a, keep_s, keep_u, stream);
+  return wide ? run<false, 128, false>(a, nullptr, nullptr, stream) : run<false, 64, false>(a, nullptr, nullptr, stream);
+}
+
+int64_t delta_workspace(const DeltaArgs& a, bool) {
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
+  if (a.bf16_io) return heads * ((a.L + 63) / 64) * Record<64>::bytes(false, 2);
+  return heads * ((a.L + 31) / 32) * Record<32>::bytes(false, 3);
+}
+
+hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream) {
+  if (a.L > 0) {
+    const hipError_t e = launch_delta_prep(a, false, stream);
+    if (e != hipSuccess) return e;
+  }
+  return launch_delta_scan(a, nullptr, nullptr, stream);
+}
+
+}  // namespace s5

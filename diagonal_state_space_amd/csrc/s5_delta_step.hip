@@ -167,8 +167,4 @@ hipError_t launch_delta_tokens(const DeltaArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-int64_t delta_workspace(const DeltaArgs&, bool) { return 0; }
-
-hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream) { return launch_delta_tokens(a, stream); }
-
 }  // namespace s5

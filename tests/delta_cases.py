@@ -14,6 +14,13 @@ transposed products, twice as long: a factor 2). One element is off by at most
 16 times that relative to the root mean square (an error of 16 standard
 deviations). Results stored as bfloat16 may be off by half a step more, 2^-8 of
 the value.
+The products that only lead to a y of bf16 io take their float32 operands in
+two bf16 parts: the first cut to 8 bits leaves less than 2^-7 of the operand,
+the second rounds that to 8 bits, an error below 2^-16 of the operand, spread
+evenly (standard deviation 2^-16 / sqrt(3)). Three such operands enter y (the
+state; P and U), whose terms have independent signs: sqrt(3) 2^-16 / sqrt(3) =
+2^-16 relative to y's root mean square, added to the bound before the rounding
+to bf16 (which is off by up to 2^-8, 256 times as much).
 The norm and rotation is a sum of up to 256 squares and a dozen roundings:
 8 * 2^-24 relative to the rotated row's norm, one element 2^-24 * 32.
 """
@@ -61,6 +68,10 @@ def to_gpu(x, io):
 
 def delta_bound(L, grad=False):
     return 1.7e-6 * np.sqrt(1 + L / 64) * (2 if grad else 1)
+
+
+def y_bound(L, io):
+    return delta_bound(L) + (2.0 ** -16 if io == "bf16" else 0.0)
 
 
 def check(name, got, ref, rel, io="f32", element=16.0):

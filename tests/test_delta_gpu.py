@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import oracle.delta_oracle as orc
-from delta_cases import check, delta_bound, delta_inputs, to_gpu
+from delta_cases import check, delta_bound, delta_inputs, to_gpu, y_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -58,7 +58,7 @@ def test_forward(shape, io):
     x = delta_inputs(*shape, io, seed=sum(shape), state=state)
     y, s = _run(x, io, packed)
     yr, sr = orc.gated_delta(**x)
-    check("y", y, yr, delta_bound(shape[1]), io)
+    check("y", y, yr, y_bound(shape[1], io), io)
     check("state", s, sr, delta_bound(shape[1]))
 
 
@@ -77,7 +77,7 @@ def test_lengths_leave_the_rows_behind(io):
     _, s = _run(x, io, lengths=torch.from_numpy(lengths).cuda(), y=y)
     for b, t in enumerate(np.clip(lengths, 0, L)):
         assert (y[b, t:] == 7.0).all()
-        check(f"y{b}", y[b, :t], yr[b, :t], delta_bound(L), io)
+        check(f"y{b}", y[b, :t], yr[b, :t], y_bound(L, io), io)
     check("state", s, sr, delta_bound(L))
     np.testing.assert_array_equal(s[0].cpu().numpy(), x["s0"][0])
     fresh, _ = _run(x, io, lengths=torch.from_numpy(lengths).cuda())
@@ -98,7 +98,7 @@ def test_decays_that_forget_at_once_and_never(io):
     x["beta"][:, 1::3] = 1.0
     yr, sr = orc.gated_delta(**x)
     y, s = _run(x, io)
-    check("y", y, yr, delta_bound(150), io)
+    check("y", y, yr, y_bound(150, io), io)
     for h in range(4):
         check(f"state{h}", s[:, h], sr[:, h], delta_bound(150))
 
@@ -113,7 +113,7 @@ def test_equal_keys(io):
     x["beta"][..., 1] = 0.05
     yr, sr = orc.gated_delta(**x)
     y, s = _run(x, io)
-    check("y", y, yr, delta_bound(190), io)
+    check("y", y, yr, y_bound(190, io), io)
     check("state", s, sr, delta_bound(190))
 
 
@@ -124,7 +124,7 @@ def test_large_values_stay_relative():
     x["s0"] *= 2.0 ** 20
     y, s = _run(x, "bf16")
     yr, sr = orc.gated_delta(**x)
-    check("y", y, yr, delta_bound(100), "bf16")
+    check("y", y, yr, y_bound(100, "bf16"), "bf16")
     check("state", s, sr, delta_bound(100))
 
 
@@ -166,7 +166,7 @@ def test_state_in_place_and_scale():
     assert s2 is keep and torch.equal(s2, s) and torch.equal(y2, y)
     y3, none = s5.gated_delta(**d, scale=2.0)
     assert none is None and torch.equal(y3, y)
-    check("y", y, orc.gated_delta(**x, scale=2.0)[0], delta_bound(90), "bf16")
+    check("y", y, orc.gated_delta(**x, scale=2.0)[0], y_bound(90, "bf16"), "bf16")
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
@@ -185,7 +185,7 @@ def test_step(shape, io):
               row[:, 2 * Hk * Dk:].unflatten(-1, (Hv, Dv))]
     s = d["s0"].clone()
     y = s5.gated_delta_step(d["q"], d["k"], d["v"], d["g"], d["beta"], s)
-    check("y", y, yr[:, 0], delta_bound(1), io)
+    check("y", y, yr[:, 0], y_bound(1, io), io)
     check("state", s, sr, delta_bound(1))
     y2 = s5.gated_delta_step(*packed, d["g"], d["beta"], d["s0"])
     assert torch.equal(y2, y) and torch.equal(d["s0"], s)
@@ -222,7 +222,7 @@ def test_as_used(io):
         ys.append(s5.gated_delta_step(qi, ki, v[:, i], g[:, i].contiguous(), beta[:, i].contiguous(), s)[:, None])
     n64 = lambda x: x.float().cpu().numpy().astype(np.float64)  # noqa: E731
     yr, sr = orc.gated_delta(n64(qa), n64(ka), n64(v), n64(g), n64(beta))
-    check("y", torch.cat(ys, 1), yr, delta_bound(T), io)
+    check("y", torch.cat(ys, 1), yr, y_bound(T, io), io)
     check("state", s, sr, delta_bound(T))
 
 
