@@ -103,7 +103,8 @@ class HipEvents:
 # entry point, the C ABI layer's validation): edits there leave the traffic
 # record valid
 DIGEST_EXCLUDE = {"s5_step.hip", "s5_glu.hip", "s5_discretize.hip", "s5_api.cpp", "s5_qk.hip", "s5_delta.h",
-                  "s5_delta_api.cpp", "s5_delta_step.hip"}
+                  "s5_delta_tile.h", "s5_delta_api.cpp", "s5_delta_step.hip", "s5_delta_prep.hip", "s5_delta_scan.hip",
+                  "s5_delta_back.hip"}
 
 
 def kernel_source_digest() -> str:

@@ -26,6 +26,7 @@ PEAK_SOURCES = ["s5_peak.hip"]
 
 SOURCES = ["s5_api.cpp", "s5_discretize.hip", "s5_forward.hip", "s5_pack.hip", "s5_step.hip", "s5_glu.hip",
            "s5_delta_api.cpp", "s5_qk.hip", "s5_delta_step.hip", "s5_delta_prep.hip", "s5_delta_scan.hip",
+           "s5_delta_back.hip",
            "s5_fused_bf16_ti.hip", "s5_fused_bf16_tv.hip", "s5_fused_f32_ti.hip", "s5_fused_f32_tv.hip"]
 
 # Packed-FP32 instructions are disabled for all device code.

@@ -57,15 +57,23 @@ struct DeltaArgs {
 // one token after the other, the state in registers
 hipError_t launch_delta_tokens(const DeltaArgs& a, hipStream_t stream);
 
-// the chunked form: preparation of all chunks, then the chunks in order
-// (keep_s, keep_u: no outputs, the states at the chunks' starts and the chunks'
-// writes for the backward pass)
+// What the chains leave for the gradients (float32, columns padded with zeros
+// to 16): states S at the chunks' starts and gradients D' of their end states
+// [B*Hv][chunks][dkp][dvp], the chunks' writes U and gradients dR [B*Hv][chunks][C][dvp].
+struct DeltaKeep {
+  float *s, *d, *u, *r;
+  int dkp, dvp;
+};
+
+// the chunked form: preparation of all chunks, then the chunks in order (with
+// `keep` no outputs but S and U for the backward pass)
 bool delta_vectored(const DeltaArgs& a);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
-hipError_t launch_delta_scan(const DeltaArgs& a, float* keep_s, float* keep_u, hipStream_t stream);
+hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaKeep* keep, hipStream_t stream);
 
 // whole sequences; bytes of workspace they need
 int64_t delta_workspace(const DeltaArgs& a, bool backward);
 hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream);
+hipError_t launch_delta_backward(const DeltaArgs& a, hipStream_t stream);
 
 }  // namespace s5

@@ -144,7 +144,7 @@ s5_status run_delta(const s5_delta_desc* x, bool backward, hipStream_t stream) {
     const Range outs[] = {range_of(x->dq, qk), range_of(x->dk, qk), range_of(x->dv, vy), range_of(x->dg, gb),
                           range_of(x->dbeta, gb), range_of(x->ds0, state), ws};
     if (any_overlap(ins, outs)) return S5_ERR_INVALID_ARGUMENT;
-    return S5_ERR_UNSUPPORTED;
+    return s5::launch_delta_backward(delta_args(*x), stream) == hipSuccess ? S5_OK : S5_ERR_HIP;
   }
   const Range outs[] = {range_of(x->y, vy), range_of(x->s_last, state), ws};
   if (any_overlap(ins, outs)) return S5_ERR_INVALID_ARGUMENT;

@@ -67,17 +67,10 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
   // sums of g (a wave's 64 lanes hold the chunk)
   if (w == 0) {
     const bool live = l < C && l < left;
-    float gi = live ? a.g[(tok + l) * a.Hv + h] : 0.0f;
+    const float gi = live ? a.g[(tok + l) * a.Hv + h] : 0.0f;
     const float be = live ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
-    // e^-110 is 0 in float32: a cleared state without -inf - (-inf)
-    gi = gi < -110.0f ? -110.0f : gi;
-    double s = gi;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double up = __shfl_up(s, o);
-      if (l >= o) s += up;
-    }
-    const bool bad = !(fabsf(gi) < INFINITY) || !(fabsf(be) < INFINITY);
+    const double s = chunk_sums(gi);
+    const bool bad = !(gi < INFINITY) || !(fabsf(be) < INFINITY);
     const uint64_t mask = __ballot(bad);
     if (l < C) {
       s_g[l] = s;

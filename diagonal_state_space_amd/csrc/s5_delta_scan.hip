@@ -46,9 +46,9 @@ struct Scan {
 };
 
 // KEEP: no outputs; the states at the chunks' starts and U are stored for the
-// backward pass (keep_s [bh][chunk][Dk][Dv], keep_u [bh][chunk][C][Dv])
+// backward pass
 template <bool BF16, int KP, int NW, bool KEEP>
-__global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks, int groups, bool vec, float* keep_s, float* keep_u) {
+__global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks, int groups, bool vec, DeltaKeep keep) {
   using Z = Scan<BF16, KP, NW, KEEP>;
   constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -140,13 +140,12 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
     const unsigned char* rec = smem + Z::oRec;
     const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - 4 * C * 4);
     if constexpr (KEEP) {
-      float* p = keep_s + (static_cast<int64_t>(bh) * chunks + n) * a.Dk * a.Dv;
+      float* p = keep.s + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp;
 #pragma unroll
       for (int t = 0; t < KT; ++t)
+        if (16 * t < a.Dk) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * t + 4 * g + r;
-          if (live && row < a.Dk) p[static_cast<int64_t>(row) * a.Dv + col] = S[t][r];
+          for (int r = 0; r < 4; ++r) p[static_cast<int64_t>(16 * t + 4 * g + r) * keep.dvp + col] = S[t][r];
         }
     }
     f32x4 X[MT], O[MT];
@@ -204,13 +203,13 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
     }
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     if constexpr (KEEP) {
-      float* p = keep_u + (static_cast<int64_t>(bh) * chunks + n) * C * a.Dv;
+      float* p = keep.u + (static_cast<int64_t>(bh) * chunks + n) * C * keep.dvp;
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * t + 4 * g + r;
-          if (live) p[static_cast<int64_t>(i) * a.Dv + col] = i < first ? U[t][r] : kNaN;
+          p[static_cast<int64_t>(i) * keep.dvp + col] = i < first ? U[t][r] : kNaN;
         }
     } else {
       Frag<NO> uf[CS];
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
     }
   }
 
-  if (a.s_last != nullptr && live) {
+  if (!KEEP && a.s_last != nullptr && live) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
 }
 
 template <bool BF16, int KP, bool KEEP>
-hipError_t run(const DeltaArgs& a, float* keep_s, float* keep_u, hipStream_t stream) {
+hipError_t run(const DeltaArgs& a, const DeltaKeep& keep, hipStream_t stream) {
   constexpr int NW = 4;
   using Z = Scan<BF16, KP, NW, KEEP>;
   auto* kern = k_delta_scan<BF16, KP, NW, KEEP>;
@@ -277,27 +276,21 @@ hipError_t run(const DeltaArgs& a, float* keep_s, float* keep_u, hipStream_t str
   const int chunks = (a.L + Z::C - 1) / Z::C;
   const int groups = (a.Dv + 16 * NW - 1) / (16 * NW);
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups;
-  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(Z::kThreads), Z::kLds, stream>>>(a, chunks, groups, delta_vectored(a),
-                                                                                     keep_s, keep_u);
+  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(Z::kThreads), Z::kLds, stream>>>(a, chunks, groups, delta_vectored(a), keep);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_delta_scan(const DeltaArgs& a, float* keep_s, float* keep_u, hipStream_t stream) {
-  const bool wide = a.Dk > 64, keep = keep_s != nullptr;
-  if (a.bf16_io) {
-    if (keep) return wide ? run<true, 128, true>(a, keep_s, keep_u, stream) : run<true, 64, true>(a, keep_s, keep_u, stream);
-    return wide ? run<true, 128, false>(a, nullptr, nullptr, stream) : run<true, 64, false>(a, nullptr, nullptr, stream);
+hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaKeep* keep, hipStream_t stream) {
+  const bool wide = a.Dk > 64;
+  if (keep != nullptr) {
+    if (a.bf16_io) return wide ? run<true, 128, true>(a, *keep, stream) : run<true, 64, true>(a, *keep, stream);
+    return wide ? run<false, 128, true>(a, *keep, stream) : run<false, 64, true>(a, *keep, stream);
   }
-  if (keep) return wide ? run<false, 128, true>(a, keep_s, keep_u, stream) : run<false, 64, true>(a, keep_s, keep_u, stream);
-  return wide ? run<false, 128, false>(a, nullptr, nullptr, stream) : run<false, 64, false>(a, nullptr, nullptr, stream);
-}
-
-int64_t delta_workspace(const DeltaArgs& a, bool) {
-  const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
-  if (a.bf16_io) return heads * ((a.L + 63) / 64) * Record<64>::bytes(false, 2);
-  return heads * ((a.L + 31) / 32) * Record<32>::bytes(false, 3);
+  const DeltaKeep none{};
+  if (a.bf16_io) return wide ? run<true, 128, false>(a, none, stream) : run<true, 64, false>(a, none, stream);
+  return wide ? run<false, 128, false>(a, none, stream) : run<false, 64, false>(a, none, stream);
 }
 
 hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream) {
@@ -305,7 +298,7 @@ hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream) {
     const hipError_t e = launch_delta_prep(a, false, stream);
     if (e != hipSuccess) return e;
   }
-  return launch_delta_scan(a, nullptr, nullptr, stream);
+  return launch_delta_scan(a, nullptr, stream);
 }
 
 }  // namespace s5

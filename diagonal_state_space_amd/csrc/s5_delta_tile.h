@@ -276,6 +276,23 @@ struct Record {
   static constexpr int bytes(bool backward, int np) { return decays(backward, np) + 4 * C * 4; }
 };
 
+// a log decay below this is 0 as a float32 factor: sums of g stay finite with
+// it in the place of -inf, without -inf - (-inf)
+constexpr float kLeastDecay = -110.0f;
+
+// inclusive sums of g over a wave's lanes (one chunk), float64: their
+// differences stay exact to float32 however fast a head forgets
+__device__ __forceinline__ double chunk_sums(float g) {
+  const int l = threadIdx.x & 63;
+  double s = g < kLeastDecay ? kLeastDecay : g;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double up = __shfl_up(s, o);
+    if (l >= o) s += up;
+  }
+  return s;
+}
+
 __device__ __forceinline__ int length_of(const DeltaArgs& a, int b) {
   if (a.lengths == nullptr) return a.L;
   const int n = a.lengths[b];

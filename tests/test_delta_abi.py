@@ -58,7 +58,8 @@ def test_delta_forward_refusals(bad, status):
     *[({n: None}, INVALID) for n in ("dy", "dq", "dk", "dv", "dg", "dbeta")],
     (dict(dq=at(11) + 8), UNSUPPORTED), (dict(dq=at(0)), INVALID), (dict(dv=at(9)), INVALID), (dict(dk=at(11)), INVALID),
     (dict(dg=at(14), dbeta=at(14)), INVALID), (dict(ds0=at(10)), INVALID), (dict(ds0=at(5)), INVALID),
-    ])
+    (dict(workspace=None), INVALID), (dict(workspace_bytes=16), INVALID), (dict(workspace=at(17) + 128), UNSUPPORTED),
+    (dict(workspace=at(1)), INVALID), (dict(workspace=at(11)), INVALID)])
 def test_delta_backward_refusals(bad, status):
     assert delta(True, **bad) == status
 
