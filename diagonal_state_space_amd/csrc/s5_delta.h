@@ -46,6 +46,7 @@ struct DeltaArgs {
   void* y;                 // [B, L, Hv, Dv]
   float* s_last;           // [B, Hv, Dk, Dv] or null; may be s0 itself
   void* ws;
+  unsigned char *frags, *recs;   // in ws: operand fragments of k and q, records of the chunks
   // backward only
   const void* dy;
   const float* ds_last;    // or null (zero)
@@ -67,7 +68,8 @@ struct DeltaKeep {
 
 // the chunked form: preparation of all chunks, then the chunks in order (with
 // `keep` no outputs but S and U for the backward pass)
-bool delta_vectored(const DeltaArgs& a);
+// `work` finds the workspace's parts and gives the bytes of fragments and records
+int64_t delta_work(DeltaArgs& a, bool backward);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaKeep* keep, hipStream_t stream);
 

@@ -25,26 +25,23 @@ using namespace delta;
 
 namespace {
 
-template <bool BF16, int KP, int NW>
-struct Back {
-  static constexpr int C = chunk_of<BF16>();
-  static constexpr int NI = BF16 ? 1 : 3;
-  static constexpr int KS = KP / 32, MT = C / 16, CS = C / 32, KT = KP / 16;
-  static constexpr int kThreads = 64 * NW;
-  static constexpr int kBlocks = (C / 4) * (KP / 8);
-  static constexpr int kJobs = (kBlocks + kThreads - 1) / kThreads;
-  static constexpr int kRec0 = Record<C>::P;                        // T transposed, P transposed, the decays
-  static constexpr int kRec = Record<C>::bytes(true, 3) - kRec0;
-  static constexpr int kRecJobs = (kRec / 16 + kThreads - 1) / kThreads;
-  static constexpr int oK = 0, oKT = oK + MT * KS * NI * kFrag, oQT = oKT + KT * CS * NI * kFrag;
-  static constexpr int oRec = oQT + KT * CS * NI * kFrag;
-  static constexpr int kLds = oRec + kRec;
+// LDS of a chunk: fragments of k (by rows, by columns) and q (by columns) and
+// the decays, two of them where they fit (one more wave copies them); the transposed T and P, which the
+// next chunk's replace as soon as they are read.
+template <bool BF16, int KP>
+struct Back : Shape<BF16, KP> {
+  using Z = Shape<BF16, KP>;
+  static constexpr int kTri = tri_frags<Z::C>() * 3 * kFrag;
+  static constexpr int kBuf = 3 * Z::kMat + kFrag;
+  static constexpr bool kTwo = 2 * kBuf + 2 * kTri <= kMaxLds;
+  static constexpr int oTri = (kTwo ? 2 : 1) * kBuf;
+  static constexpr int kLds = oTri + 2 * kTri;
 };
 
 template <bool BF16, int KP, int NW>
-__global__ void __launch_bounds__(64 * NW) k_delta_back_scan(DeltaArgs a, int chunks, int groups, bool vec, DeltaKeep keep) {
-  using Z = Back<BF16, KP, NW>;
-  constexpr int C = Z::C, NI = Z::NI, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT;
+__global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, int chunks, int groups, DeltaKeep keep) {
+  using Z = Back<BF16, KP>;
+  constexpr int C = Z::C, NI = Z::NI, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -56,7 +53,31 @@ __global__ void __launch_bounds__(64 * NW) k_delta_back_scan(DeltaArgs a, int ch
   const bool wave_live = (cg * NW + w) * 16 < a.Dv, live = col < a.Dv;
   const int len = length_of(a, b);
   const int nc = (len + C - 1) / C;
-  constexpr int64_t es = BF16 ? 2 : 4;
+
+  if (w == NW) {   // the copying wave
+    auto record = [&](int n) { return a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true, 3); };
+    auto copy_tri = [&](int n) { lds_copy<1>(smem + Z::oTri, record(n) + Record<C>::P, 2 * Z::kTri, 0); };
+    auto copy = [&](int n) {
+      unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
+      lds_copy<1>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(true), 3 * Z::kMat, 0);
+      lds_copy<1>(dst + 3 * Z::kMat, record(n) + Record<C>::decays(true, 3), kFrag, 0);
+    };
+    if (nc > 0) {
+      if (Z::kTwo) copy(nc - 1);
+      copy_tri(nc - 1);
+    }
+    for (int n = nc - 1; n >= 0; --n) {
+      if constexpr (!Z::kTwo) {
+        barrier_copied();
+        copy(n);
+      }
+      barrier_copied();
+      if (Z::kTwo && n > 0) copy(n - 1);
+      barrier_copied();
+      if (n > 0) copy_tri(n - 1);
+    }
+    return;
+  }
 
   f32x4 D[KT];
 #pragma unroll
@@ -67,112 +88,83 @@ __global__ void __launch_bounds__(64 * NW) k_delta_back_scan(DeltaArgs a, int ch
       D[t][r] = a.ds_last != nullptr && live && row < a.Dk ? a.ds_last[(static_cast<int64_t>(bh) * a.Dk + row) * a.Dv + col] : 0.0f;
     }
 
-  Block<BF16> kb[Z::kJobs], qb[Z::kJobs];
-  uint4 rb[Z::kRecJobs];
-  float ob[MT][4];
+  uint32_t ob[MT][4];
+  const int ldy = a.Hv * a.Dv * es;
+  const int yo = live ? 4 * g * ldy + col * es : kNowhere;
+  const unsigned char* s_tt = smem + Z::oTri;
+  const unsigned char* s_pt = s_tt + Z::kTri;
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-    const Rows kr{static_cast<const char*>(a.k) + (tok * a.ldk + static_cast<int64_t>(hk) * a.Dk) * es, a.ldk, len - n * C, a.Dk, vec};
-    const Rows qr{static_cast<const char*>(a.q) + (tok * a.ldq + static_cast<int64_t>(hk) * a.Dk) * es, a.ldq, len - n * C, a.Dk, vec};
-#pragma unroll
-    for (int j = 0; j < Z::kJobs; ++j) {
-      const int i = tid + j * Z::kThreads;
-      if (i < Z::kBlocks) {
-        kb[j] = load_block<BF16>(kr, 4 * (i / (KP / 8)), 8 * (i % (KP / 8)));
-        qb[j] = load_block<BF16>(qr, 4 * (i / (KP / 8)), 8 * (i % (KP / 8)));
-      }
-    }
-    const unsigned char* rec = static_cast<const unsigned char*>(a.ws) +
-                               (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true, 3) + Z::kRec0;
-#pragma unroll
-    for (int j = 0; j < Z::kRecJobs; ++j) {
-      const int o = (tid + j * Z::kThreads) * 16;
-      if (o < Z::kRec) rb[j] = *reinterpret_cast<const uint4*>(rec + o);
-    }
-    const int64_t y0 = (tok * a.Hv + h) * a.Dv + col;
-    const int64_t ldy = static_cast<int64_t>(a.Hv) * a.Dv;
+    const Buf yr = rows_buf(static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * t + 4 * g + r;
-        ob[t][r] = live && i < len - n * C ? load_el<BF16>(a.dy, y0 + i * ldy) : 0.0f;
-      }
+      for (int r = 0; r < 4; ++r) ob[t][r] = load_raw<BF16>(yr, yo + (16 * t + r) * ldy);
   };
 
   if (nc > 0) fetch(nc - 1);
   for (int n = nc - 1; n >= 0; --n) {
-    __syncthreads();   // the previous chunk's fragments are read
-#pragma unroll
-    for (int j = 0; j < Z::kJobs; ++j) {
-      const int i = tid + j * Z::kThreads;
-      if (i < Z::kBlocks) {
-        const Parts<BF16> p(kb[j]);
-        store_rows<BF16, KS>(smem + Z::oK, p, i / (KP / 8), i % (KP / 8));
-        store_cols<BF16, C>(smem + Z::oKT, p, i / (KP / 8), i % (KP / 8));
-        store_cols<BF16, C>(smem + Z::oQT, Parts<BF16>(qb[j]), i / (KP / 8), i % (KP / 8));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < Z::kRecJobs; ++j) {
-      const int o = (tid + j * Z::kThreads) * 16;
-      if (o < Z::kRec) *reinterpret_cast<uint4*>(smem + Z::oRec + o) = rb[j];
-    }
+    if constexpr (!Z::kTwo) barrier_read();   // the previous chunk is read
+    barrier_read();                           // the chunk is there, the previous one read
     f32x4 dO[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dO[t][r] = ob[t][r];
-    __syncthreads();
+      for (int r = 0; r < 4; ++r) dO[t][r] = value<BF16>(ob[t][r]);
     if (n > 0) fetch(n - 1);
-    if (!wave_live) continue;
 
-    const unsigned char* rec = smem + Z::oRec;
-    const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - 4 * C * 4);
-    float* kd = keep.d + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp;
+    const unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
+    const unsigned char *s_kt = s_k + Z::kMat, *s_qt = s_k + 2 * Z::kMat;
+    const float* dec = reinterpret_cast<const float*>(s_k + 3 * Z::kMat);
+    f32x4 dU[MT], P[MT], dR[MT];
+    if (wave_live) {
+      float* kd = keep.d + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp;
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
-      if (16 * t < a.Dk) {
+      for (int t = 0; t < KT; ++t)
+        if (16 * t < a.Dk) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) kd[static_cast<int64_t>(16 * t + 4 * g + r) * keep.dvp + col] = D[t][r];
+          for (int r = 0; r < 4; ++r) kd[static_cast<int64_t>(16 * t + 4 * g + r) * keep.dvp + col] = D[t][r];
+        }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) dU[t] = P[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const Frag<3> d = to_frag<3>(D[2 * ks], D[2 * ks + 1]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) dU[t] = mma(read_rows<NI, KS>(s_k, t, ks), d, dU[t]);
       }
-    f32x4 dU[MT], P[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) dU[t] = P[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const Frag<3> d = to_frag<3>(D[2 * ks], D[2 * ks + 1]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) dU[t] = mma(read_rows<NI, KS>(smem + Z::oK, t, ks), d, dU[t]);
-    }
-    {
       Frag<NI> of[CS];
 #pragma unroll
       for (int ks = 0; ks < CS; ++ks) of[ks] = to_frag<NI>(dO[2 * ks], dO[2 * ks + 1]);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int ks = t / 2; ks < CS; ++ks)
-          P[t] = mma(read_frag<3>(rec + (Record<C>::PT - Record<C>::P), tri_frag_t<C>(t, ks), 0), of[ks], P[t]);
+        for (int ks = t / 2; ks < CS; ++ks) P[t] = mma(read_frag<3>(s_pt, tri_frag_t<C>(t, ks), 0), of[ks], P[t]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const float4 to = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
+        const float tt[4] = {to.x, to.y, to.z, to.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dU[t][r] = fmaf(tt[r], dU[t][r], a.scale * P[t][r]);
+      }
+      Frag<3> uf[CS];
+#pragma unroll
+      for (int ks = 0; ks < CS; ++ks) uf[ks] = to_frag<3>(dU[2 * ks], dU[2 * ks + 1]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        dR[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = t / 2; ks < CS; ++ks) dR[t] = mma(read_frag<3>(s_tt, tri_frag_t<C>(t, ks), 0), uf[ks], dR[t]);
+      }
     }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const float4 to = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
-      const float tt[4] = {to.x, to.y, to.z, to.w};
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dU[t][r] = fmaf(tt[r], dU[t][r], a.scale * P[t][r]);
-    }
-    Frag<3> uf[CS];
-#pragma unroll
-    for (int ks = 0; ks < CS; ++ks) uf[ks] = to_frag<3>(dU[2 * ks], dU[2 * ks + 1]);
+    barrier_read();   // T and P are read
+    if (!wave_live) continue;
+
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     float* kr = keep.r + (static_cast<int64_t>(bh) * chunks + n) * C * keep.dvp;
-    f32x4 dR[MT];
+    const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      dR[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int ks = t / 2; ks < CS; ++ks) dR[t] = mma(read_frag<3>(rec, tri_frag_t<C>(t, ks), 0), uf[ks], dR[t]);
       const float4 f = *reinterpret_cast<const float4*>(dec + 16 * t + 4 * g);
       const float4 be = *reinterpret_cast<const float4*>(dec + 2 * C + 16 * t + 4 * g);
       const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w};
@@ -181,7 +173,7 @@ __global__ void __launch_bounds__(64 * NW) k_delta_back_scan(DeltaArgs a, int ch
         const int i = 16 * t + 4 * g + r;
         kr[static_cast<int64_t>(i) * keep.dvp + col] = dR[t][r];
         dR[t][r] *= bb[r];
-        if (live && i < len - n * C) store_el<BF16>(a.dv, ((tok + i) * a.Hv + h) * a.Dv + col, dR[t][r]);
+        store_el<BF16>(vr, yo + (16 * t + r) * ldy, dR[t][r]);
         dR[t][r] *= -ff[r];
         dO[t][r] *= a.scale * ff[r];
       }
@@ -199,8 +191,8 @@ __global__ void __launch_bounds__(64 * NW) k_delta_back_scan(DeltaArgs a, int ch
       for (int r = 0; r < 4; ++r) D[t][r] *= whole;
 #pragma unroll
       for (int ks = 0; ks < CS; ++ks) {
-        D[t] = mma(read_cols<NI, C>(smem + Z::oKT, t, ks), rf[ks], D[t]);
-        D[t] = mma(read_cols<NI, C>(smem + Z::oQT, t, ks), of[ks], D[t]);
+        D[t] = mma(read_cols<NI, C>(s_kt, t, ks), rf[ks], D[t]);
+        D[t] = mma(read_cols<NI, C>(s_qt, t, ks), of[ks], D[t]);
       }
     }
   }
@@ -526,27 +518,25 @@ __global__ void __launch_bounds__(256) k_delta_grad(DeltaArgs a, int chunks, Del
   }
 }
 
-DeltaKeep keep_of(const DeltaArgs& a, int64_t* bytes) {
+// finds the workspace's parts; bytes of all of them
+int64_t keep_of(DeltaArgs& a, DeltaKeep& k) {
   const int C = a.bf16_io ? 64 : 32;
   const int64_t chunks = static_cast<int64_t>(a.B) * a.Hv * ((a.L + C - 1) / C);
-  DeltaKeep k{};
   k.dkp = (a.Dk + 15) & ~15;
   k.dvp = (a.Dv + 15) & ~15;
-  const int64_t rec = chunks * (a.bf16_io ? Record<64>::bytes(true, 3) : Record<32>::bytes(true, 3));
-  const int64_t state = chunks * k.dkp * k.dvp * 4, rows = chunks * C * k.dvp * 4;
-  char* p = static_cast<char*>(a.ws);
-  k.s = reinterpret_cast<float*>(p + rec);
-  k.d = reinterpret_cast<float*>(p + rec + state);
-  k.u = reinterpret_cast<float*>(p + rec + 2 * state);
-  k.r = reinterpret_cast<float*>(p + rec + 2 * state + rows);
-  if (bytes != nullptr) *bytes = rec + 2 * state + 2 * rows;
-  return k;
+  const int64_t head = delta_work(a, true), state = chunks * k.dkp * k.dvp * 4, rows = chunks * C * k.dvp * 4;
+  unsigned char* p = static_cast<unsigned char*>(a.ws);
+  k.s = reinterpret_cast<float*>(p + head);
+  k.d = reinterpret_cast<float*>(p + head + state);
+  k.u = reinterpret_cast<float*>(p + head + 2 * state);
+  k.r = reinterpret_cast<float*>(p + head + 2 * state + rows);
+  return head + 2 * state + 2 * rows;
 }
 
 template <bool BF16, int KP>
-hipError_t run(const DeltaArgs& a, hipStream_t stream) {
+hipError_t run(DeltaArgs a, hipStream_t stream) {
   constexpr int NW = 4, C = chunk_of<BF16>();
-  using Z = Back<BF16, KP, NW>;
+  using Z = Back<BF16, KP>;
   using G = Grad<BF16, KP>;
   auto* scan = k_delta_back_scan<BF16, KP, NW>;
   auto* grad = k_delta_grad<BF16, KP>;
@@ -557,14 +547,15 @@ hipError_t run(const DeltaArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   const int chunks = (a.L + C - 1) / C;
   const int groups = (a.Dv + 16 * NW - 1) / (16 * NW);
-  const DeltaKeep keep = keep_of(a, nullptr);
+  DeltaKeep keep{};
+  keep_of(a, keep);
   if (a.L > 0) {
     hipError_t e = launch_delta_prep(a, true, stream);
     if (e == hipSuccess) e = launch_delta_scan(a, &keep, stream);
     if (e != hipSuccess) return e;
   }
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups;
-  scan<<<dim3(static_cast<unsigned>(blocks)), dim3(Z::kThreads), Z::kLds, stream>>>(a, chunks, groups, delta_vectored(a), keep);
+  scan<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, keep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.L == 0) return e;
   const bool vec_y = a.Dv % 4 == 0;   // dy is contiguous and 16-byte aligned
@@ -574,15 +565,10 @@ hipError_t run(const DeltaArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t delta_workspace(const DeltaArgs& a, bool backward) {
-  if (backward) {
-    int64_t bytes = 0;
-    keep_of(a, &bytes);
-    return bytes;
-  }
-  const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
-  if (a.bf16_io) return heads * ((a.L + 63) / 64) * Record<64>::bytes(false, 2);
-  return heads * ((a.L + 31) / 32) * Record<32>::bytes(false, 3);
+int64_t delta_workspace(const DeltaArgs& args, bool backward) {
+  DeltaArgs a = args;
+  DeltaKeep k{};
+  return backward ? keep_of(a, k) : delta_work(a, false);
 }
 
 hipError_t launch_delta_backward(const DeltaArgs& a, hipStream_t stream) {

@@ -8,7 +8,7 @@
 //
 // Both products run on the matrix cores from staged k and q; P comes out
 // transposed, which is the order of its operand fragments, and is stored from
-// the registers. The inverse: the 16 x 16 diagonal blocks by substitution, a
+// the registers. A kernel before this one puts k and q into fragments. The inverse: the 16 x 16 diagonal blocks by substitution, a
 // column a lane; then blocks of 32 and 64 from halves,
 //   [X 0; B Y]^-1 = [X^-1 0; -Y^-1 B X^-1  Y^-1],
 // by float32 matrix instructions, the second factor from the accumulators of
@@ -31,16 +31,44 @@ __device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-template <bool BF16, int C, int KP, bool BACK>
-__global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks, bool vec) {
-  constexpr int NI = BF16 ? 1 : 3;
-  constexpr int NO = BF16 ? 2 : 3;
-  constexpr int KS = KP / 32, MT = C / 16;
+// k and q of a chunk and key head as operand fragments
+template <bool BF16, int KP, bool BACK>
+__global__ void __launch_bounds__(kThreads) k_delta_frags(DeltaArgs a, int chunks, bool vec) {
+  using Z = Shape<BF16, KP>;
+  constexpr int C = Z::C, es = Z::es;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x;
+  const int n = blockIdx.x % chunks, bk = blockIdx.x / chunks;
+  const int b = bk / a.Hk, hk = bk - b * a.Hk;
+  const int rows = min(length_of(a, b) - n * C, C);
+  if (rows <= 0) return;
+  const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
+  const int ldk = static_cast<int>(a.ldk) * es, ldq = static_cast<int>(a.ldq) * es;
+  const Buf kr = rows_buf(static_cast<const char*>(a.k) + (tok * a.ldk + static_cast<int64_t>(hk) * a.Dk) * es, rows, ldk, a.Dk * es);
+  const Buf qr = rows_buf(static_cast<const char*>(a.q) + (tok * a.ldq + static_cast<int64_t>(hk) * a.Dk) * es, rows, ldq, a.Dk * es);
+  for (int i = tid; i < (C / 4) * (KP / 8); i += kThreads) {
+    const int tg = i / (KP / 8), dg = i % (KP / 8), nd = a.Dk - 8 * dg;
+    const Parts<BF16> k(load_block<BF16>(kr, block_offset<BF16>(tg, dg, ldk, a.Dk), ldk, nd, vec));
+    const Parts<BF16> q(load_block<BF16>(qr, block_offset<BF16>(tg, dg, ldq, a.Dk), ldq, nd, vec));
+    store_rows<BF16, Z::KS>(smem, k, tg, dg);
+    store_cols<BF16, C>(smem + Z::kMat, k, tg, dg);
+    if constexpr (BACK) store_cols<BF16, C>(smem + 2 * Z::kMat, q, tg, dg);
+    store_rows<BF16, Z::KS>(smem + (BACK ? 3 : 2) * Z::kMat, q, tg, dg);
+  }
+  __syncthreads();
+  uint4* dst = reinterpret_cast<uint4*>(a.frags + static_cast<int64_t>(blockIdx.x) * Z::frags(BACK));
+  for (int i = tid; i < Z::frags(BACK) / 16; i += kThreads) dst[i] = reinterpret_cast<const uint4*>(smem)[i];
+}
+
+template <bool BF16, int KP, bool BACK>
+__global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks) {
+  using Z = Shape<BF16, KP>;
+  constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT;
   constexpr int LD = C + 4;
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* s_k = smem;
-  unsigned char* s_q = s_k + MT * KS * NI * kFrag;
-  constexpr int kStage = 2 * MT * KS * NI * kFrag;
+  unsigned char* s_q = s_k + Z::kMat;
+  constexpr int kStage = 2 * Z::kMat;
   float* s_t = reinterpret_cast<float*>(smem);                        // T, over k and q when they are read
   float* s_a = reinterpret_cast<float*>(smem + (kStage > C * LD * 4 ? kStage : C * LD * 4));   // A
   double* s_g = reinterpret_cast<double*>(s_a + C * LD);              // sums of g
@@ -55,15 +83,9 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
   if (left <= 0) return;
   const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
 
-  // stage k and q
-  const int64_t es = BF16 ? 2 : 4;
-  const Rows kr{static_cast<const char*>(a.k) + (tok * a.ldk + static_cast<int64_t>(hk) * a.Dk) * es, a.ldk, left, a.Dk, vec};
-  const Rows qr{static_cast<const char*>(a.q) + (tok * a.ldq + static_cast<int64_t>(hk) * a.Dk) * es, a.ldq, left, a.Dk, vec};
-  for (int i = tid; i < (C / 4) * (KP / 8); i += kThreads) {
-    const int tg = i / (KP / 8), dg = i % (KP / 8);
-    store_rows<BF16, KS>(s_k, Parts<BF16>(load_block<BF16>(kr, 4 * tg, 8 * dg)), tg, dg);
-    store_rows<BF16, KS>(s_q, Parts<BF16>(load_block<BF16>(qr, 4 * tg, 8 * dg)), tg, dg);
-  }
+  const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(BACK);
+  lds_copy<kWaves>(s_k, fr, Z::kMat, w);
+  lds_copy<kWaves>(s_q, fr + (BACK ? 3 : 2) * Z::kMat, Z::kMat, w);
   // sums of g (a wave's 64 lanes hold the chunk)
   if (w == 0) {
     const bool live = l < C && l < left;
@@ -80,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
   }
   __syncthreads();
 
-  unsigned char* rec = static_cast<unsigned char*>(a.ws) + static_cast<int64_t>(blockIdx.x) * Record<C>::bytes(BACK, NO);
+  unsigned char* rec = a.recs + static_cast<int64_t>(blockIdx.x) * Record<C>::bytes(BACK, NO);
   // A: wave w the row tiles w, w + 4 (C = 64: one each)
   for (int it = w; it < MT; it += kWaves) {
     for (int jt = 0; jt <= it; ++jt) {
@@ -242,23 +264,29 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
 
 template <bool BF16, int KP, bool BACK>
 hipError_t run(const DeltaArgs& a, hipStream_t stream) {
-  constexpr int C = chunk_of<BF16>(), NI = BF16 ? 1 : 3;
+  using Z = Shape<BF16, KP>;
+  constexpr int C = Z::C;
+  constexpr int square = C * (C + 4) * 4, stage = 2 * Z::kMat;
+  constexpr int lds = (stage > square ? stage : square) + square + C * 8 + C * 4 + 16;
+  auto* frags = k_delta_frags<BF16, KP, BACK>;
+  auto* prep = k_delta_prep<BF16, KP, BACK>;
+  static const hipError_t attr[2] = {
+      hipFuncSetAttribute(reinterpret_cast<const void*>(frags), hipFuncAttributeMaxDynamicSharedMemorySize, Z::frags(BACK)),
+      hipFuncSetAttribute(reinterpret_cast<const void*>(prep), hipFuncAttributeMaxDynamicSharedMemorySize, lds)};
+  for (hipError_t e : attr)
+    if (e != hipSuccess) return e;
   const int chunks = (a.L + C - 1) / C;
-  const int stage = 2 * (C / 16) * (KP / 32) * NI * kFrag, square = C * (C + 4) * 4;
-  const size_t lds = (stage > square ? stage : square) + square + C * 8 + C * 4 + 16;
-  const int64_t blocks = static_cast<int64_t>(a.B) * a.Hv * chunks;
-  k_delta_prep<BF16, C, KP, BACK><<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), lds, stream>>>(
-      a, chunks, delta_vectored(a));
+  const int V = BF16 ? 8 : 4;
+  auto ok = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  const bool vec = a.Dk % V == 0 && a.ldq % V == 0 && a.ldk % V == 0 && ok(a.q) && ok(a.k);
+  frags<<<dim3(static_cast<unsigned>(a.B * a.Hk * chunks)), dim3(kThreads), Z::frags(BACK), stream>>>(a, chunks, vec);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  prep<<<dim3(static_cast<unsigned>(a.B * a.Hv * chunks)), dim3(kThreads), lds, stream>>>(a, chunks);
   return hipGetLastError();
 }
 
 }  // namespace
-
-bool delta_vectored(const DeltaArgs& a) {
-  const int V = a.bf16_io ? 8 : 4;
-  auto ok = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  return a.Dk % V == 0 && a.ldq % V == 0 && a.ldk % V == 0 && ok(a.q) && ok(a.k);
-}
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream) {
   const bool wide = a.Dk > 64;
@@ -268,6 +296,25 @@ hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stre
   }
   if (backward) return wide ? run<false, 128, true>(a, stream) : run<false, 64, true>(a, stream);
   return wide ? run<false, 128, false>(a, stream) : run<false, 64, false>(a, stream);
+}
+
+namespace {
+
+template <bool BF16, int KP>
+int64_t work(DeltaArgs& a, bool backward) {
+  using Z = Shape<BF16, KP>;
+  const int64_t chunks = (a.L + Z::C - 1) / Z::C;
+  const int64_t frags = a.B * chunks * a.Hk * Z::frags(backward);
+  a.frags = static_cast<unsigned char*>(a.ws);
+  a.recs = a.frags + frags;
+  return frags + a.B * chunks * a.Hv * Record<Z::C>::bytes(backward, Z::NO);
+}
+
+}  // namespace
+
+int64_t delta_work(DeltaArgs& a, bool backward) {
+  if (a.bf16_io) return a.Dk > 64 ? work<true, 128>(a, backward) : work<true, 64>(a, backward);
+  return a.Dk > 64 ? work<false, 128>(a, backward) : work<false, 64>(a, backward);
 }
 
 }  // namespace s5

@@ -27,30 +27,26 @@ namespace {
 
 constexpr float kNaN = __builtin_nanf("");
 
-template <bool BF16, int KP, int NW, bool KEEP>
-struct Scan {
-  static constexpr int C = chunk_of<BF16>();
-  static constexpr int NI = BF16 ? 1 : 3;      // parts of k and q
-  static constexpr int NO = BF16 ? 2 : 3;      // parts on the way to y
-  static constexpr int KS = KP / 32, MT = C / 16, CS = C / 32, KT = KP / 16;
-  static constexpr int kThreads = 64 * NW;
-  static constexpr int kBlocks = (C / 4) * (KP / 8);            // staged blocks of k
-  static constexpr int kJobs = (kBlocks + kThreads - 1) / kThreads;
-  // what of the chunk's record is staged: T, P and the decays, or T and the decays
-  static constexpr int kRecT = tri_frags<C>() * 3 * kFrag;
-  static constexpr int kRec = (KEEP ? kRecT : Record<C>::decays(false, NO)) + 4 * C * 4;
-  static constexpr int kRecJobs = (kRec / 16 + kThreads - 1) / kThreads;
-  static constexpr int oK = 0, oKT = oK + MT * KS * NI * kFrag, oQ = oKT + KT * CS * NI * kFrag;
-  static constexpr int oRec = oQ + (KEEP ? 0 : MT * KS * NI * kFrag);
-  static constexpr int kLds = oRec + kRec;
+// One more wave copies the chunks. LDS of a chunk: fragments of k (by rows, by columns) and q, T, P and the
+// decays (KEEP: without q and P); two of them where they fit, the next chunk
+// on its way while one is worked on.
+template <bool BF16, int KP, bool KEEP>
+struct Scan : Shape<BF16, KP> {
+  using Z = Shape<BF16, KP>;
+  static constexpr int kFrags = (KEEP ? 2 : 3) * Z::kMat;
+  static constexpr int kRecT = tri_frags<Z::C>() * 3 * kFrag;
+  static constexpr int kRec = KEEP ? kRecT + kFrag : Record<Z::C>::bytes(false, Z::NO);
+  static constexpr int kBuf = kFrags + kRec;
+  static constexpr bool kTwo = 2 * kBuf <= kMaxLds;
+  static constexpr int kLds = (kTwo ? 2 : 1) * kBuf;
 };
 
 // KEEP: no outputs; the states at the chunks' starts and U are stored for the
 // backward pass
 template <bool BF16, int KP, int NW, bool KEEP>
-__global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks, int groups, bool vec, DeltaKeep keep) {
-  using Z = Scan<BF16, KP, NW, KEEP>;
-  constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT;
+__global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int chunks, int groups, DeltaKeep keep) {
+  using Z = Scan<BF16, KP, KEEP>;
+  constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -64,7 +60,30 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
   const bool wave_live = (cg * NW + w) * 16 < a.Dv, live = col < a.Dv;
   const int len = length_of(a, b);
   const int nc = (len + C - 1) / C;
-  constexpr int64_t es = BF16 ? 2 : 4;
+
+  if (w == NW) {   // the copying wave
+    auto copy = [&](int n) {
+      unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
+      const unsigned char* rec = a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(KEEP, NO);
+      lds_copy<1>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(KEEP), Z::kFrags, 0);
+      if constexpr (KEEP) {
+        lds_copy<1>(dst + Z::kFrags, rec + Record<C>::T, Z::kRecT, 0);
+        lds_copy<1>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(true, 3), kFrag, 0);
+      } else {
+        lds_copy<1>(dst + Z::kFrags, rec, Z::kRec, 0);
+      }
+    };
+    if (Z::kTwo && nc > 0) copy(0);
+    for (int n = 0; n < nc; ++n) {
+      if constexpr (!Z::kTwo) {
+        barrier_copied();
+        copy(n);
+      }
+      barrier_copied();
+      if (Z::kTwo && n + 1 < nc) copy(n + 1);
+    }
+    return;
+  }
 
   f32x4 S[KT];
 #pragma unroll
@@ -75,70 +94,34 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
       S[t][r] = a.s0 != nullptr && live && row < a.Dk ? a.s0[(static_cast<int64_t>(bh) * a.Dk + row) * a.Dv + col] : 0.0f;
     }
 
-  Block<BF16> kb[Z::kJobs], qb[Z::kJobs];
-  uint4 rb[Z::kRecJobs];
-  float vb[MT][4];
+  uint32_t vb[MT][4];
+  const int ldv = static_cast<int>(a.ldv) * es, ldy = a.Hv * a.Dv * es;
+  const int vo = live ? 4 * g * ldv + col * es : kNowhere, yo = live ? 4 * g * ldy + col * es : kNowhere;
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-    const Rows kr{static_cast<const char*>(a.k) + (tok * a.ldk + static_cast<int64_t>(hk) * a.Dk) * es, a.ldk, len - n * C, a.Dk, vec};
-    const Rows qr{static_cast<const char*>(a.q) + (tok * a.ldq + static_cast<int64_t>(hk) * a.Dk) * es, a.ldq, len - n * C, a.Dk, vec};
-#pragma unroll
-    for (int j = 0; j < Z::kJobs; ++j) {
-      const int i = tid + j * Z::kThreads;
-      if (i < Z::kBlocks) {
-        kb[j] = load_block<BF16>(kr, 4 * (i / (KP / 8)), 8 * (i % (KP / 8)));
-        if constexpr (!KEEP) qb[j] = load_block<BF16>(qr, 4 * (i / (KP / 8)), 8 * (i % (KP / 8)));
-      }
-    }
-    const unsigned char* rec = static_cast<const unsigned char*>(a.ws) +
-                               (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(KEEP, NO);
-#pragma unroll
-    for (int j = 0; j < Z::kRecJobs; ++j) {
-      int o = (tid + j * Z::kThreads) * 16;
-      if (o < Z::kRec) {
-        if (KEEP && o >= Z::kRecT) o += Record<C>::decays(true, NO) - Z::kRecT;
-        rb[j] = *reinterpret_cast<const uint4*>(rec + o);
-      }
-    }
-    const int64_t v0 = tok * a.ldv + static_cast<int64_t>(h) * a.Dv + col;
+    const Buf vr = rows_buf(static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es, min(len - n * C, C),
+                            ldv, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * t + 4 * g + r;
-        vb[t][r] = live && i < len - n * C ? load_el<BF16>(a.v, v0 + i * a.ldv) : 0.0f;
-      }
+      for (int r = 0; r < 4; ++r) vb[t][r] = load_raw<BF16>(vr, vo + (16 * t + r) * ldv);
   };
 
   if (nc > 0) fetch(0);
   for (int n = 0; n < nc; ++n) {
-    __syncthreads();   // the previous chunk's fragments are read
-#pragma unroll
-    for (int j = 0; j < Z::kJobs; ++j) {
-      const int i = tid + j * Z::kThreads;
-      if (i < Z::kBlocks) {
-        const Parts<BF16> p(kb[j]);
-        store_rows<BF16, KS>(smem + Z::oK, p, i / (KP / 8), i % (KP / 8));
-        store_cols<BF16, C>(smem + Z::oKT, p, i / (KP / 8), i % (KP / 8));
-        if constexpr (!KEEP) store_rows<BF16, KS>(smem + Z::oQ, Parts<BF16>(qb[j]), i / (KP / 8), i % (KP / 8));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < Z::kRecJobs; ++j) {
-      const int o = (tid + j * Z::kThreads) * 16;
-      if (o < Z::kRec) *reinterpret_cast<uint4*>(smem + Z::oRec + o) = rb[j];
-    }
+    if constexpr (!Z::kTwo) barrier_read();   // the previous chunk is read
+    barrier_read();                           // the chunk is there, the previous one read
+    if (!wave_live) continue;
     float V[MT][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) V[t][r] = vb[t][r];
-    __syncthreads();
+      for (int r = 0; r < 4; ++r) V[t][r] = value<BF16>(vb[t][r]);
     if (n + 1 < nc) fetch(n + 1);
-    if (!wave_live) continue;
 
-    const unsigned char* rec = smem + Z::oRec;
-    const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - 4 * C * 4);
+    const unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
+    const unsigned char *s_kt = s_k + Z::kMat, *s_q = s_k + 2 * Z::kMat, *rec = s_k + Z::kFrags;
+    const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - kFrag);
     if constexpr (KEEP) {
       float* p = keep.s + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp;
 #pragma unroll
@@ -157,8 +140,8 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
       const Frag<NO> so = to_frag<NO>(S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        X[t] = mma(read_rows<NI, KS>(smem + Z::oK, t, ks), s, X[t]);
-        if constexpr (!KEEP) O[t] = mma(read_rows<NI, KS>(smem + Z::oQ, t, ks), so, O[t]);
+        X[t] = mma(read_rows<NI, KS>(s_k, t, ks), s, X[t]);
+        if constexpr (!KEEP) O[t] = mma(read_rows<NI, KS>(s_q, t, ks), so, O[t]);
       }
     }
     float from[MT][4];
@@ -212,6 +195,7 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
           p[static_cast<int64_t>(i) * keep.dvp + col] = i < first ? U[t][r] : kNaN;
         }
     } else {
+      const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
       Frag<NO> uf[CS];
 #pragma unroll
       for (int ks = 0; ks < CS; ++ks) uf[ks] = to_frag<NO>(U[2 * ks], U[2 * ks + 1]);
@@ -225,8 +209,7 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * t + 4 * g + r;
-          if (live && i < len - n * C)
-            store_el<BF16>(a.y, ((tok + i) * a.Hv + h) * a.Dv + col, i < first ? a.scale * O[t][r] : kNaN);
+          store_el<BF16>(yr, yo + (16 * t + r) * ldy, i < first ? a.scale * O[t][r] : kNaN);
         }
       }
     }
@@ -246,7 +229,7 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[t][r] *= whole;
 #pragma unroll
-      for (int ks = 0; ks < CS; ++ks) S[t] = mma(read_cols<NI, C>(smem + Z::oKT, t, ks), ud[ks], S[t]);
+      for (int ks = 0; ks < CS; ++ks) S[t] = mma(read_cols<NI, C>(s_kt, t, ks), ud[ks], S[t]);
       if (first < C) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[t][r] = kNaN;
@@ -268,7 +251,7 @@ __global__ void __launch_bounds__(64 * NW) k_delta_scan(DeltaArgs a, int chunks,
 template <bool BF16, int KP, bool KEEP>
 hipError_t run(const DeltaArgs& a, const DeltaKeep& keep, hipStream_t stream) {
   constexpr int NW = 4;
-  using Z = Scan<BF16, KP, NW, KEEP>;
+  using Z = Scan<BF16, KP, KEEP>;
   auto* kern = k_delta_scan<BF16, KP, NW, KEEP>;
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
@@ -276,7 +259,7 @@ hipError_t run(const DeltaArgs& a, const DeltaKeep& keep, hipStream_t stream) {
   const int chunks = (a.L + Z::C - 1) / Z::C;
   const int groups = (a.Dv + 16 * NW - 1) / (16 * NW);
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups;
-  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(Z::kThreads), Z::kLds, stream>>>(a, chunks, groups, delta_vectored(a), keep);
+  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, keep);
   return hipGetLastError();
 }
 
@@ -293,7 +276,9 @@ hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaKeep* keep, hipStrea
   return wide ? run<false, 128, false>(a, none, stream) : run<false, 64, false>(a, none, stream);
 }
 
-hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream) {
+hipError_t launch_delta(const DeltaArgs& args, hipStream_t stream) {
+  DeltaArgs a = args;
+  delta_work(a, false);
   if (a.L > 0) {
     const hipError_t e = launch_delta_prep(a, false, stream);
     if (e != hipSuccess) return e;

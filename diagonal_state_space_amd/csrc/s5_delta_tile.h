@@ -92,6 +92,7 @@ __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4
 // writes of a staging wave over the banks.
 
 constexpr int kFrag = 1024;   // bytes of one part of a fragment
+constexpr int kMaxLds = 160 * 1024;
 
 __device__ __forceinline__ int slot_of(int g, int m, int mix) { return (g * 16 + (m ^ (mix & 15))) * 16; }
 
@@ -126,49 +127,61 @@ struct Block {
   uint4 r[BF16 ? 4 : 8];
 };
 
-struct Rows {
-  const void* p;      // element 0 of the chunk's first token and the head
-  int64_t ld;         // elements between tokens
-  int tokens, dims;   // valid ones; the rest is zero
-  bool vec;           // whole 16-byte groups are aligned
-};
+// Rows of a chunk through a buffer descriptor that ends with the last valid
+// one: what lies behind reads as zero and is not written, without a branch.
+// Features that do not exist go to an offset behind every chunk.
+typedef __amdgpu_buffer_rsrc_t Buf;
+constexpr int kNowhere = 0x60000000;
+constexpr int kBufferWord3 = 0x00020000;          // raw buffer, 32-bit data format
+constexpr int64_t kMaxStride = int64_t{1} << 22;   // elements between tokens: 64 rows stay below 2^30 bytes
 
+// `rows` rows of `width` bytes, `ld` bytes apart, from p
+__device__ __forceinline__ Buf rows_buf(const void* p, int rows, int ld, int width) {
+  const int bytes = rows > 0 ? (rows - 1) * ld + width : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, kBufferWord3);
+}
+
+__device__ __forceinline__ uint4 load16(Buf r, int o) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+}
+
+// four tokens `ld` bytes apart, the first at byte `o` (kNowhere: a block of
+// features that do not exist); nd of the eight features exist
 template <bool BF16>
-__device__ __forceinline__ Block<BF16> load_block(const Rows& x, int t0, int d0) {
+__device__ __forceinline__ Block<BF16> load_block(Buf buf, int o, int ld, int nd, bool vec) {
   Block<BF16> b;
-  const int nd = x.dims - d0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int64_t i = (t0 + j) * x.ld + d0;
-    const bool live = t0 + j < x.tokens;
-    if constexpr (BF16) {
-      const uint16_t* p = static_cast<const uint16_t*>(x.p) + i;
-      if (live && nd >= 8 && x.vec) {
-        b.r[j] = *reinterpret_cast<const uint4*>(p);
+    const int at = o + j * ld;
+    if (vec) {
+      if constexpr (BF16) {
+        b.r[j] = load16(buf, at);
       } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (live) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (c < nd) w[c >> 1] |= static_cast<uint32_t>(p[c]) << (16 * (c & 1));
-        }
-        b.r[j] = uint4{w[0], w[1], w[2], w[3]};
+        b.r[2 * j] = load16(buf, at);
+        b.r[2 * j + 1] = load16(buf, nd > 4 ? at + 16 : kNowhere);
       }
+    } else if constexpr (BF16) {
+      uint32_t w[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        w[c] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(buf, c < nd ? at + 2 * c : kNowhere, 0, 0));
+      b.r[j] = uint4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
     } else {
-      const uint32_t* p = static_cast<const uint32_t*>(x.p) + i;
-      if (live && nd >= 8 && x.vec) {
-        b.r[2 * j] = reinterpret_cast<const uint4*>(p)[0];
-        b.r[2 * j + 1] = reinterpret_cast<const uint4*>(p)[1];
-      } else {
-        uint32_t w[8];
+      uint32_t w[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = live && c < nd ? p[c] : 0u;
-        b.r[2 * j] = uint4{w[0], w[1], w[2], w[3]};
-        b.r[2 * j + 1] = uint4{w[4], w[5], w[6], w[7]};
-      }
+      for (int c = 0; c < 8; ++c)
+        w[c] = __builtin_amdgcn_raw_buffer_load_b32(buf, c < nd ? at + 4 * c : kNowhere, 0, 0);
+      b.r[2 * j] = uint4{w[0], w[1], w[2], w[3]};
+      b.r[2 * j + 1] = uint4{w[4], w[5], w[6], w[7]};
     }
   }
   return b;
+}
+
+// byte offset of the block (tg, dg) of rows `ld` bytes apart with `dims` features
+template <bool BF16>
+__device__ __forceinline__ int block_offset(int tg, int dg, int ld, int dims) {
+  return 8 * dg < dims ? 4 * tg * ld + 8 * dg * (BF16 ? 2 : 4) : kNowhere;
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& r, int i) { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
@@ -248,6 +261,23 @@ __device__ __forceinline__ void store_el(void* p, int64_t i, float x) {
   else static_cast<float*>(p)[i] = x;
 }
 
+// an element's bits, and its value (apart: a conversion at the load would wait for it)
+template <bool BF16>
+__device__ __forceinline__ uint32_t load_raw(Buf r, int o) {
+  if constexpr (BF16) return static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0));
+  else return __builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0);
+}
+template <bool BF16>
+__device__ __forceinline__ float value(uint32_t raw) {
+  return __uint_as_float(BF16 ? raw << 16 : raw);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_el(Buf r, int o, float x) {
+  if constexpr (BF16) __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(round2(x, x)), r, o, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(x), r, o, 0, 0);
+}
+
 // ---- chunks and their workspace records -----------------------------------------
 // Chunk length: 64 tokens for bf16 io; 32 for float32 io, whose three parts of
 // q and k fill the LDS three times as fast.
@@ -266,15 +296,59 @@ __host__ __device__ constexpr int tri_frag_t(int jt, int ks) { return C == 32 ? 
 // The record of one head's chunk: the parts of T = (I + A)^-1 and of P = M o QK^T
 // (backward: T, its transpose and that of P), then the decays
 //   from[i] = e^{G_i}, to[i] = e^{G_end - G_i}, beta[i], whole = e^{G_end}, bad
-// with bad the first token whose key, decay or strength is not finite (C if none).
+// (1 KB) with bad the first token whose key, decay or strength is not finite (C if none).
 template <int C>
 struct Record {
   static constexpr int T = 0;
   static constexpr int P = tri_frags<C>() * 3 * kFrag;           // backward: T transposed
   static constexpr int PT = 2 * P;                               // backward only
   static constexpr int decays(bool backward, int np) { return backward ? 3 * P : P + tri_frags<C>() * np * kFrag; }
-  static constexpr int bytes(bool backward, int np) { return decays(backward, np) + 4 * C * 4; }
+  static constexpr int bytes(bool backward, int np) { return decays(backward, np) + kFrag; }
 };
+
+// What the kernels share for an io type and padded features of a key (KP = 64
+// or 128): parts of k and q (NI) and of what leads to y only (NO), tiles of 16
+// and steps of 32 tokens (MT, CS) and features (KT, KS), bytes of the fragments
+// of k or q of a chunk. The fragments of a key head's chunk are k by rows, k by
+// columns, q by rows (backward: q by columns before it).
+template <bool BF16, int KP>
+struct Shape {
+  static constexpr int C = chunk_of<BF16>();
+  static constexpr int NI = BF16 ? 1 : 3, NO = BF16 ? 2 : 3;
+  static constexpr int KS = KP / 32, KT = KP / 16, MT = C / 16, CS = C / 32;
+  static constexpr int kMat = MT * KS * NI * kFrag;
+  static constexpr int frags(bool backward) { return (backward ? 4 : 3) * kMat; }
+  static constexpr int es = BF16 ? 2 : 4;
+};
+
+// ---- 1 KB blocks from global memory straight into LDS ------------------------------
+typedef __attribute__((address_space(3))) void lds_void;
+
+// blocks w, w + NW, ... of `bytes` (a multiple of 1 KB) at src to dst
+template <int NW>
+__device__ __forceinline__ void lds_copy(unsigned char* dst, const unsigned char* src, int bytes, int w) {
+  const Buf r = __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(src), 0, bytes, kBufferWord3);
+  const int l = threadIdx.x & 63;
+#pragma unroll 4
+  for (int o = w * kFrag; o < bytes; o += NW * kFrag)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + o), 16, o + l * 16, 0, 0, 0);
+}
+
+// Barriers of kernels whose last wave does nothing but copy the next chunk
+// into LDS (the waves that compute then have no such copy in flight, for which
+// the compiler would wait before each of their LDS reads): it arrives when
+// its copies are there, the others when their reads are done.
+__device__ __forceinline__ void barrier_copied() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void barrier_read() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // a log decay below this is 0 as a float32 factor: sums of g stay finite with
 // it in the place of -inf, without -inf - (-inf)
@@ -295,7 +369,7 @@ __device__ __forceinline__ double chunk_sums(float g) {
 
 __device__ __forceinline__ int length_of(const DeltaArgs& a, int b) {
   if (a.lengths == nullptr) return a.L;
-  const int n = a.lengths[b];
+  const int n = __builtin_amdgcn_readfirstlane(a.lengths[b]);
   return n < 0 ? 0 : n > a.L ? a.L : n;
 }
 

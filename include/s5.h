@@ -396,7 +396,9 @@ s5_status s5_glu(int64_t T, int64_t H, s5_dtype io, int variant, const void* y, 
  * B or L, heads or features < 1, Hv not a multiple of Hk, a token stride below
  * the row, a scale that is not finite, workspace too small, an output
  * overlapping an input or another output), S5_ERR_UNSUPPORTED (io, feature
- * limits, B*L or B*Hv*Dv above INT32_MAX, misalignment), S5_ERR_HIP.
+ * limits, a token stride or Hv*Dv above 2^22 elements, B*L or B*Hv*Dv above
+ * INT32_MAX, B*Hv times the 32-step chunks of L above 2^24 - 1, misalignment),
+ * S5_ERR_HIP.
  */
 #define S5_DELTA_MAX_DK 128
 #define S5_DELTA_MAX_DV 512
