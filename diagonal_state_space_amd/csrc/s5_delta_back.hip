@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
   uint32_t ob[MT][4];
   const int ldy = a.Hv * a.Dv * es;
   const int yo = live ? 4 * g * ldy + col * es : kNowhere;
+  const int ko = (4 * g * keep.dvp + col) * 4;   // rows behind the kept ones are outside their buffer
   const unsigned char* s_tt = smem + Z::oTri;
   const unsigned char* s_pt = s_tt + Z::kTri;
   auto fetch = [&](int n) {
@@ -118,28 +119,21 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     const float* dec = reinterpret_cast<const float*>(s_k + 3 * Z::kMat);
     f32x4 dU[MT], P[MT], dR[MT];
     if (wave_live) {
-      float* kd = keep.d + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp;
+      const Buf kd = rows_buf(keep.d + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp, keep.dkp, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
       for (int t = 0; t < KT; ++t)
-        if (16 * t < a.Dk) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) kd[static_cast<int64_t>(16 * t + 4 * g + r) * keep.dvp + col] = D[t][r];
-        }
+        for (int r = 0; r < 4; ++r) store_el<false>(kd, ko + (16 * t + r) * keep.dvp * 4, D[t][r]);
 #pragma unroll
       for (int t = 0; t < MT; ++t) dU[t] = P[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const Frag<3> d = to_frag<3>(D[2 * ks], D[2 * ks + 1]);
+        Frag<NI> kf[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) dU[t] = mma(read_rows<NI, KS>(s_k, t, ks), d, dU[t]);
+        for (int t = 0; t < MT; ++t) kf[t] = read_rows<NI, KS>(s_k, t, ks);
+        mma(dU, kf, to_frag<3>(D[2 * ks], D[2 * ks + 1]));
       }
-      Frag<NI> of[CS];
-#pragma unroll
-      for (int ks = 0; ks < CS; ++ks) of[ks] = to_frag<NI>(dO[2 * ks], dO[2 * ks + 1]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int ks = t / 2; ks < CS; ++ks) P[t] = mma(read_frag<3>(s_pt, tri_frag_t<C>(t, ks), 0), of[ks], P[t]);
+      tri_mma_t<C, 3, NI>(P, s_pt, dO);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const float4 to = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
@@ -147,21 +141,15 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
 #pragma unroll
         for (int r = 0; r < 4; ++r) dU[t][r] = fmaf(tt[r], dU[t][r], a.scale * P[t][r]);
       }
-      Frag<3> uf[CS];
 #pragma unroll
-      for (int ks = 0; ks < CS; ++ks) uf[ks] = to_frag<3>(dU[2 * ks], dU[2 * ks + 1]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        dR[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int ks = t / 2; ks < CS; ++ks) dR[t] = mma(read_frag<3>(s_tt, tri_frag_t<C>(t, ks), 0), uf[ks], dR[t]);
-      }
+      for (int t = 0; t < MT; ++t) dR[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      tri_mma_t<C, 3, 3>(dR, s_tt, dU);
     }
     barrier_read();   // T and P are read
     if (!wave_live) continue;
 
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-    float* kr = keep.r + (static_cast<int64_t>(bh) * chunks + n) * C * keep.dvp;
+    const Buf kr = rows_buf(keep.r + (static_cast<int64_t>(bh) * chunks + n) * C * keep.dvp, C, keep.dvp * 4, keep.dvp * 4);
     const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -170,30 +158,22 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
       const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * t + 4 * g + r;
-        kr[static_cast<int64_t>(i) * keep.dvp + col] = dR[t][r];
+        store_el<false>(kr, ko + (16 * t + r) * keep.dvp * 4, dR[t][r]);
         dR[t][r] *= bb[r];
         store_el<BF16>(vr, yo + (16 * t + r) * ldy, dR[t][r]);
         dR[t][r] *= -ff[r];
         dO[t][r] *= a.scale * ff[r];
       }
     }
-    Frag<3> rf[CS], of[CS];
-#pragma unroll
-    for (int ks = 0; ks < CS; ++ks) {
-      rf[ks] = to_frag<3>(dR[2 * ks], dR[2 * ks + 1]);
-      of[ks] = to_frag<3>(dO[2 * ks], dO[2 * ks + 1]);
-    }
     const float whole = dec[3 * C];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) D[t][r] *= whole;
 #pragma unroll
-      for (int ks = 0; ks < CS; ++ks) {
-        D[t] = mma(read_cols<NI, C>(s_kt, t, ks), rf[ks], D[t]);
-        D[t] = mma(read_cols<NI, C>(s_qt, t, ks), of[ks], D[t]);
-      }
+    for (int ks = 0; ks < CS; ++ks) {
+      cols_mma<NI, C>(D, s_kt, ks, to_frag<3>(dR[2 * ks], dR[2 * ks + 1]));
+      cols_mma<NI, C>(D, s_qt, ks, to_frag<3>(dO[2 * ks], dO[2 * ks + 1]));
     }
   }
 

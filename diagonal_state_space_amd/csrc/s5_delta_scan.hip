@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
   uint32_t vb[MT][4];
   const int ldv = static_cast<int>(a.ldv) * es, ldy = a.Hv * a.Dv * es;
   const int vo = live ? 4 * g * ldv + col * es : kNowhere, yo = live ? 4 * g * ldy + col * es : kNowhere;
+  const int ko = (4 * g * keep.dvp + col) * 4;   // rows behind the kept ones are outside their buffer
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     const Buf vr = rows_buf(static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es, min(len - n * C, C),
@@ -123,25 +124,26 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     const unsigned char *s_kt = s_k + Z::kMat, *s_q = s_k + 2 * Z::kMat, *rec = s_k + Z::kFrags;
     const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - kFrag);
     if constexpr (KEEP) {
-      float* p = keep.s + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp;
+      const Buf p = rows_buf(keep.s + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp, keep.dkp, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
       for (int t = 0; t < KT; ++t)
-        if (16 * t < a.Dk) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) p[static_cast<int64_t>(16 * t + 4 * g + r) * keep.dvp + col] = S[t][r];
-        }
+        for (int r = 0; r < 4; ++r) store_el<false>(p, ko + (16 * t + r) * keep.dvp * 4, S[t][r]);
     }
     f32x4 X[MT], O[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) X[t] = O[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const Frag<3> s = to_frag<3>(S[2 * ks], S[2 * ks + 1]);
-      const Frag<NO> so = to_frag<NO>(S[2 * ks], S[2 * ks + 1]);
+      Frag<NI> kf[MT];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        X[t] = mma(read_rows<NI, KS>(s_k, t, ks), s, X[t]);
-        if constexpr (!KEEP) O[t] = mma(read_rows<NI, KS>(s_q, t, ks), so, O[t]);
+      for (int t = 0; t < MT; ++t) kf[t] = read_rows<NI, KS>(s_k, t, ks);
+      mma(X, kf, to_frag<3>(S[2 * ks], S[2 * ks + 1]));
+      if constexpr (!KEEP) {
+        Frag<NI> qf[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) qf[t] = read_rows<NI, KS>(s_q, t, ks);
+        mma(O, qf, to_frag<NO>(S[2 * ks], S[2 * ks + 1]));
       }
     }
     float from[MT][4];
@@ -173,45 +175,33 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
         for (int r = 0; r < 4; ++r)
           if (16 * t + 4 * g + r >= first) X[t][r] = 0.0f;
     }
-    Frag<3> rf[CS];
-#pragma unroll
-    for (int ks = 0; ks < CS; ++ks) rf[ks] = to_frag<3>(X[2 * ks], X[2 * ks + 1]);
+    // U = T R: 32 products at a time, of the row tiles they reach
     f32x4 U[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      U[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int ks = 0; ks <= t / 2; ++ks)
-        U[t] = mma(read_frag<3>(rec + Record<C>::T, tri_frag<C>(t, ks), 0), rf[ks], U[t]);
-    }
+    for (int t = 0; t < MT; ++t) U[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    tri_mma<C, 3>(U, rec + Record<C>::T, X);
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     if constexpr (KEEP) {
-      float* p = keep.u + (static_cast<int64_t>(bh) * chunks + n) * C * keep.dvp;
+      const Buf p = rows_buf(keep.u + (static_cast<int64_t>(bh) * chunks + n) * C * keep.dvp, C, keep.dvp * 4, keep.dvp * 4);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          store_el<false>(p, ko + (16 * t + r) * keep.dvp * 4, 16 * t + 4 * g + r < first ? U[t][r] : kNaN);
+    } else {
+      const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[t][r] *= from[t][r];
+      tri_mma<C, NO>(O, rec + Record<C>::P, U);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * t + 4 * g + r;
-          p[static_cast<int64_t>(i) * keep.dvp + col] = i < first ? U[t][r] : kNaN;
-        }
-    } else {
-      const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
-      Frag<NO> uf[CS];
-#pragma unroll
-      for (int ks = 0; ks < CS; ++ks) uf[ks] = to_frag<NO>(U[2 * ks], U[2 * ks + 1]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) O[t][r] *= from[t][r];
-#pragma unroll
-        for (int ks = 0; ks <= t / 2; ++ks)
-          O[t] = mma(read_frag<NO>(rec + Record<C>::P, tri_frag<C>(t, ks), 0), uf[ks], O[t]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * t + 4 * g + r;
           store_el<BF16>(yr, yo + (16 * t + r) * ldy, i < first ? a.scale * O[t][r] : kNaN);
         }
-      }
     }
     const float whole = dec[3 * C];
 #pragma unroll
@@ -221,19 +211,17 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
 #pragma unroll
       for (int r = 0; r < 4; ++r) U[t][r] *= tt[r];
     }
-    Frag<3> ud[CS];
 #pragma unroll
-    for (int ks = 0; ks < CS; ++ks) ud[ks] = to_frag<3>(U[2 * ks], U[2 * ks + 1]);
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[t][r] *= whole;
 #pragma unroll
-      for (int ks = 0; ks < CS; ++ks) S[t] = mma(read_cols<NI, C>(s_kt, t, ks), ud[ks], S[t]);
-      if (first < C) {
+    for (int ks = 0; ks < CS; ++ks) cols_mma<NI, C>(S, s_kt, ks, to_frag<3>(U[2 * ks], U[2 * ks + 1]));
+    if (first < C) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[t][r] = kNaN;
-      }
     }
   }
 

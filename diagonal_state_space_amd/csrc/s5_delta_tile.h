@@ -83,6 +83,21 @@ __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4
   return c;
 }
 
+// the same for N tiles at once: neighbours in the order of issue do not wait for
+// each other
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4 (&c)[N], const Frag<NA> (&a)[N], const Frag<NB>& b) {
+  constexpr int last = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      if (i + j <= last) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) c[t] = mfma(a[t].p[i], b.p[j], c[t]);
+      }
+}
+
 // ---- fragments in LDS ----------------------------------------------------------
 // A fragment holds 16 rows by 32 products; lane l has row l%16 and, with
 // g = l/16, the products 4g..4g+3 and 16+4g..16+4g+3: the order in which two
@@ -118,6 +133,24 @@ __device__ __forceinline__ Frag<NP> read_rows(const unsigned char* base, int mt,
 template <int NP, int C>
 __device__ __forceinline__ Frag<NP> read_cols(const unsigned char* base, int mt, int ks) {
   return read_frag<NP>(base, mt * (C / 32) + ks, mt);
+}
+
+// s += a x over 32 tokens for the state's KT tiles, four at a time (enough to
+// hide the matrix instructions' latency, and fewer registers than all)
+template <int NP, int C, int KT>
+__device__ __forceinline__ void cols_mma(f32x4 (&s)[KT], const unsigned char* a, int ks, const Frag<3>& x) {
+#pragma unroll
+  for (int t0 = 0; t0 < KT; t0 += 4) {
+    Frag<NP> f[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) f[t] = read_cols<NP, C>(a, t0 + t, ks);
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int j = 0; i + j < 3; ++j)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[t0 + t] = mfma(f[t].p[i], x.p[j], s[t0 + t]);
+  }
 }
 
 // ---- staging of token rows -----------------------------------------------------
@@ -292,6 +325,43 @@ template <int C>
 __host__ __device__ constexpr int tri_frag(int it, int ks) { return it < 2 ? it : 2 * (it - 1) + ks; }
 template <int C>
 __host__ __device__ constexpr int tri_frag_t(int jt, int ks) { return C == 32 ? jt : jt < 2 ? 2 * jt + ks : 2 + jt; }
+
+// c += a x for a lower triangular a in fragments of NP parts and x in accumulator
+// tiles (or its transpose, an upper one)
+template <int C, int NP>
+__device__ __forceinline__ void tri_mma(f32x4 (&c)[C / 16], const unsigned char* a, const f32x4 (&x)[C / 16]) {
+#pragma unroll
+  for (int ks = 0; ks < C / 32; ++ks) {
+    constexpr int MT = C / 16;
+    const Frag<NP> b = to_frag<NP>(x[2 * ks], x[2 * ks + 1]);
+    Frag<NP> f[MT];
+#pragma unroll
+    for (int t = 2 * ks; t < MT; ++t) f[t] = read_frag<NP>(a, tri_frag<C>(t, ks), 0);
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int j = 0; i + j < NP; ++j)
+#pragma unroll
+        for (int t = 2 * ks; t < MT; ++t) c[t] = mfma(f[t].p[i], b.p[j], c[t]);
+  }
+}
+template <int C, int NP, int NB>
+__device__ __forceinline__ void tri_mma_t(f32x4 (&c)[C / 16], const unsigned char* a, const f32x4 (&x)[C / 16]) {
+#pragma unroll
+  for (int ks = C / 32 - 1; ks >= 0; --ks) {
+    constexpr int MT = C / 16;
+    const Frag<NB> b = to_frag<NB>(x[2 * ks], x[2 * ks + 1]);
+    Frag<NP> f[MT];
+#pragma unroll
+    for (int t = 0; t <= 2 * ks + 1; ++t) f[t] = read_frag<NP>(a, tri_frag_t<C>(t, ks), 0);
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int j = 0; j < NB && i + j < NP; ++j)
+#pragma unroll
+        for (int t = 0; t <= 2 * ks + 1; ++t) c[t] = mfma(f[t].p[i], b.p[j], c[t]);
+  }
+}
 
 // The record of one head's chunk: the parts of T = (I + A)^-1 and of P = M o QK^T
 // (backward: T, its transpose and that of P), then the decays
