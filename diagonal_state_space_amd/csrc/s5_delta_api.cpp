@@ -51,7 +51,7 @@ s5_status delta_sizes(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, 
   if (Hv > INT32_MAX / Dv || Hk > INT32_MAX / Dk) return S5_ERR_UNSUPPORTED;
   if (ldq < Hk * Dk || ldk < Hk * Dk || ldv < Hv * Dv) return S5_ERR_INVALID_ARGUMENT;
   constexpr int64_t kMost = int64_t{1} << 22;   // a chunk's rows stay below 2^30 bytes
-  if (ldq > kMost || ldk > kMost || ldv > kMost || Hv * Dv > kMost) return S5_ERR_UNSUPPORTED;
+  if (ldq > kMost || ldk > kMost || ldv > kMost || Hv * Dv > kMost || Hk * Dk > kMost) return S5_ERR_UNSUPPORTED;
   if (B > 0 && (L > INT32_MAX / B || Hv * Dv > INT32_MAX / B)) return S5_ERR_UNSUPPORTED;
   // workgroups of 256 threads, one for each chunk of 32 or 64 steps and head
   constexpr int64_t kGroups = (int64_t{1} << 24) - 1;

@@ -189,38 +189,60 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
 }
 
 // ---- the gradients without a chain ------------------------------------------------
-// Products on the float32 matrix instructions: wave w has the feature tiles
-// w, w + 4 of all tokens. An operand block of 16 rows by 16 products is one
-// float4 a lane (row m, products 4g..4g+3), four instructions.
+// One wave per 16 features of a key. The products over the value features run
+// in steps of 32: S, D', U, dR and dY are split into parts and put into row
+// fragments in LDS once for the workgroup, the next step's loads on their way
+// meanwhile; each wave has its features' rows of E = dY S^T, F = dR S^T and
+// H = U D'^T for all tokens, and a share of the C x C products W1 = dY U^T and
+// W2 = dR U^T. These are computed both ways round, since a product comes out
+// with the rows of its first factor where an operand has its products: the
+// result masked, decayed and split is an operand's fragment as it lies. Then
+// the products over tokens go on in E, F and H.
 
-__device__ __forceinline__ f32x4 mma16(float4 x, float4 y, f32x4 c) {
-  c = __builtin_amdgcn_mfma_f32_16x16x4f32(x.x, y.x, c, 0, 0, 0);
-  c = __builtin_amdgcn_mfma_f32_16x16x4f32(x.y, y.y, c, 0, 0, 0);
-  c = __builtin_amdgcn_mfma_f32_16x16x4f32(x.z, y.z, c, 0, 0, 0);
-  return __builtin_amdgcn_mfma_f32_16x16x4f32(x.w, y.w, c, 0, 0, 0);
+template <bool BF16, int KP>
+struct Grad : Shape<BF16, KP> {
+  using Z = Shape<BF16, KP>;
+  static constexpr int NW = KP / 16, kThreads = 64 * NW;
+  static constexpr int kTri = tri_frags<Z::C>(), kJobs = (4 * kTri + NW - 1) / NW;
+  static constexpr int kTok = 3 * Z::C * 4, kItems = (kTok + kThreads - 1) / kThreads;   // staged rows of 8 of dR, U, dY
+  static constexpr int oR = 0, oU = oR + Z::MT * 3 * kFrag, oY = oU + Z::MT * 3 * kFrag;
+  static constexpr int oS = oY + Z::MT * Z::NI * kFrag, oD = oS + Z::KT * 3 * kFrag, kStage = oD + Z::KT * 3 * kFrag;
+  static constexpr int kW = 4 * kTri * 3 * kFrag;           // over the stage when that is read
+  static constexpr int oG = kStage > kW ? kStage : kW;      // double sums of g
+  static constexpr int oB = oG + Z::C * 8;                  // beta, from, to
+  static constexpr int oRed = oB + 3 * Z::C * 4;            // [NW][3][C] row sums
+  static constexpr int oSum = oRed + NW * 3 * Z::C * 4;     // [NW][2] sums
+  static constexpr int oRV = oSum + NW * 2 * 4;             // [C] dR.V
+  static constexpr int oAcc = oRV + Z::C * 4;               // [NW][2 MT][64] dq and dk, where heads share a key
+  static constexpr int kAcc = NW * 2 * Z::MT * kFrag, kLds = oAcc + kAcc;
+};
+
+// sum over the 16 lanes of a row (in all of them)
+__device__ __forceinline__ float row_sum(float x) {
+  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x128, 0xf, 0xf, true));   // row_ror:8
+  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x124, 0xf, 0xf, true));
+  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x122, 0xf, 0xf, true));
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x121, 0xf, 0xf, true));
+}
+
+// eight values of row `row` (features 8c.. of a step of 32) into row fragments
+template <int NP>
+__device__ __forceinline__ void store_row8(unsigned char* base, const float (&x)[8], int row, int c) {
+  const Frag<NP> f = to_frag<NP>(x);
+  unsigned char* p = base + (row >> 4) * NP * kFrag + 8 * (c >> 1);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const uint4 w = __builtin_bit_cast(uint4, f.p[i]);
+    *reinterpret_cast<uint2*>(p + i * kFrag + slot_of(2 * (c & 1), row & 15, 0)) = uint2{w.x, w.y};
+    *reinterpret_cast<uint2*>(p + i * kFrag + slot_of(2 * (c & 1) + 1, row & 15, 0)) = uint2{w.z, w.w};
+  }
 }
 
 template <bool BF16, int KP>
-struct Grad {
-  static constexpr int C = chunk_of<BF16>(), MT = C / 16, DT = KP / 64;
-  static constexpr int LD = C + 4, LK = KP + (BF16 ? 8 : 4);
-  static constexpr int es = BF16 ? 2 : 4;
-  static constexpr int oQ = C * LK * es, oW1 = 2 * oQ, oW2 = oW1 + C * LD * 4;
-  static constexpr int oG = oW2 + C * LD * 4;               // double sums of g
-  static constexpr int oB = oG + C * 8;                     // beta, from, to
-  static constexpr int oRed = oB + 3 * C * 4;               // [4 waves][3][C] row sums
-  static constexpr int oSum = oRed + 12 * C * 4;            // [4 waves] sums
-  static constexpr int oRV = oSum + 32;                     // [C] dR.V
-  static constexpr int kLds = oRV + C * 4;
-};
-
-template <bool BF16, int KP>
-__global__ void __launch_bounds__(256) k_delta_grad(DeltaArgs a, int chunks, DeltaKeep keep, bool vec_y) {
+__global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, DeltaKeep keep, bool vec_y) {
   using Z = Grad<BF16, KP>;
-  constexpr int C = Z::C, MT = Z::MT, DT = Z::DT, LD = Z::LD, LK = Z::LK;
+  constexpr int C = Z::C, MT = Z::MT, CS = Z::CS, NI = Z::NI, NW = Z::NW, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
-  unsigned char *s_k = smem, *s_q = smem + Z::oQ;
-  float *s_w1 = reinterpret_cast<float*>(smem + Z::oW1), *s_w2 = reinterpret_cast<float*>(smem + Z::oW2);
   double* s_g = reinterpret_cast<double*>(smem + Z::oG);
   float *s_b = reinterpret_cast<float*>(smem + Z::oB), *s_from = s_b + C, *s_to = s_from + C;
   float *s_red = reinterpret_cast<float*>(smem + Z::oRed), *s_sum = reinterpret_cast<float*>(smem + Z::oSum);
@@ -231,219 +253,288 @@ __global__ void __launch_bounds__(256) k_delta_grad(DeltaArgs a, int chunks, Del
   const int b = bk / a.Hk, hk = bk - b * a.Hk;
   const int left = length_of(a, b) - n * C;
   if (left <= 0) return;
+  const int rows = min(left, C);
   const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
   const int group = a.Hv / a.Hk;
+  const int ldy = a.Hv * a.Dv * es, ldw = keep.dvp * 4;
 
-  for (int i = tid; i < C * KP; i += 256) {
-    const int t = i / KP, d = i % KP;
-    const bool ok = t < left && d < a.Dk;
-    const int64_t ki = (tok + t) * a.ldk + static_cast<int64_t>(hk) * a.Dk + d;
-    const int64_t qi = (tok + t) * a.ldq + static_cast<int64_t>(hk) * a.Dk + d;
-    if constexpr (BF16) {
-      reinterpret_cast<uint16_t*>(s_k)[t * LK + d] = ok ? static_cast<const uint16_t*>(a.k)[ki] : uint16_t{0};
-      reinterpret_cast<uint16_t*>(s_q)[t * LK + d] = ok ? static_cast<const uint16_t*>(a.q)[qi] : uint16_t{0};
-    } else {
-      reinterpret_cast<float*>(s_k)[t * LK + d] = ok ? static_cast<const float*>(a.k)[ki] : 0.0f;
-      reinterpret_cast<float*>(s_q)[t * LK + d] = ok ? static_cast<const float*>(a.q)[qi] : 0.0f;
-    }
-  }
-
-  f32x4 dQ[DT][MT], dK[DT][MT];
+  auto value_of = [&](const Frag<NI>& f, int e) {
+    float x = static_cast<float>(f.p[0][e]);
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) dQ[d][t] = dK[d][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 1; p < NI; ++p) x += static_cast<float>(f.p[p][e]);
+    return x;
+  };
 
   for (int hh = 0; hh < group; ++hh) {
     const int h = hk * group + hh;
-    const int64_t bh = static_cast<int64_t>(b) * a.Hv + h;
-    __syncthreads();   // the previous head's sums are read
+    const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, cn = bh * chunks + n;
+    const Buf ks = rows_buf(keep.s + cn * keep.dkp * keep.dvp, keep.dkp, ldw, ldw);
+    const Buf kd = rows_buf(keep.d + cn * keep.dkp * keep.dvp, keep.dkp, ldw, ldw);
+    const Buf ku = rows_buf(keep.u + cn * C * keep.dvp, C, ldw, ldw);
+    const Buf kr = rows_buf(keep.r + cn * C * keep.dvp, C, ldw, ldw);
+    const Buf yr = rows_buf(static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es, rows, ldy, a.Dv * es);
     float gi = 0.0f;
-    if (w == 0) {
-      const bool live = l < C && l < left;
-      gi = live ? a.g[(tok + l) * a.Hv + h] : 0.0f;
-      const double s = chunk_sums(gi);
-      const double end = __shfl(s, C - 1);
-      if (l < C) {
-        s_g[l] = s;
-        s_b[l] = live ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
-        s_from[l] = expf(static_cast<float>(s));
-        s_to[l] = expf(static_cast<float>(end - s));
-      }
-    }
 
-    // contraction over the value features
-    const float* ks = keep.s + (bh * chunks + n) * keep.dkp * keep.dvp;
-    const float* kd = keep.d + (bh * chunks + n) * keep.dkp * keep.dvp;
-    const float* ku = keep.u + (bh * chunks + n) * C * keep.dvp;
-    const float* kr = keep.r + (bh * chunks + n) * C * keep.dvp;
-    f32x4 E[DT][MT], F[DT][MT], H[DT][MT], W1[MT], W2[MT];
+    // a row's eight values: of the kept arrays, and of dy as its bits
+    struct Eight {
+      uint4 lo, hi;
+    };
+    auto load_kept = [&](Buf r, int row, int v) {
+      const int o = v < keep.dvp ? row * ldw + v * 4 : kNowhere;
+      return Eight{load16(r, o), load16(r, o + 16)};
+    };
+    auto load_dy = [&](int row, int v) {
+      const int o = row * ldy + v * es;
+      Eight x{};
+      if (vec_y) {
+        x.lo = load16(yr, v < a.Dv ? o : kNowhere);
+        if constexpr (!BF16) x.hi = load16(yr, v + 4 < a.Dv ? o + 16 : kNowhere);
+      } else {
+        uint32_t e[8];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      W1[t] = W2[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < 8; ++i) e[i] = load_raw<BF16>(yr, v + i < a.Dv ? o + i * es : kNowhere);
+        if constexpr (BF16) {
+          x.lo = uint4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+        } else {
+          x.lo = uint4{e[0], e[1], e[2], e[3]};
+          x.hi = uint4{e[4], e[5], e[6], e[7]};
+        }
+      }
+      return x;
+    };
+    auto floats = [](const Eight& x, float (&f)[8]) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) E[d][t] = F[d][t] = H[d][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+      for (int i = 0; i < 4; ++i) {
+        f[i] = __uint_as_float(word(x.lo, i));
+        f[4 + i] = __uint_as_float(word(x.hi, i));
+      }
+    };
+    Eight es_, ed, et[Z::kItems];
+    const int srow = tid >> 2, sc = tid & 3;    // this thread's row of S and D' and eight of its 32 values
+    auto fetch = [&](int v0) {
+      es_ = load_kept(ks, srow, v0 + 8 * sc);
+      ed = load_kept(kd, srow, v0 + 8 * sc);
+#pragma unroll
+      for (int j = 0; j < Z::kItems; ++j) {
+        const int i = tid + j * Z::kThreads;
+        if (i < Z::kTok) {
+          const int mat = __builtin_amdgcn_readfirstlane(i / (4 * C)), row = (i >> 2) % C, v = v0 + 8 * (i & 3);
+          et[j] = mat == 0 ? load_kept(kr, row, v) : mat == 1 ? load_kept(ku, row, v) : load_dy(row, v);
+        }
+      }
+    };
+
+    f32x4 E[MT], F[MT], H[MT], W[Z::kJobs][2];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) E[t] = F[t] = H[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < Z::kJobs; ++j) W[j][0] = W[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     float sd = 0.0f;   // <D', S>
-    const int64_t ldy = static_cast<int64_t>(a.Hv) * a.Dv;
-    // rows of W1 and W2 of this wave: tiles w and MT - 1 - w (C = 32: the first two waves)
-    const int r1 = w < MT ? w : 0, r2 = w < MT ? MT - 1 - w : 0;
-    for (int v0 = 0; v0 < keep.dvp; v0 += 16) {
-      const int v = v0 + 4 * g;
-      auto load_dy = [&](int t) {
-        const int i = 16 * t + m;
-        float4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (i < left) {
-          const int64_t o = (tok + i) * ldy + static_cast<int64_t>(h) * a.Dv + v;
-          if (vec_y && v + 4 <= a.Dv) {
-            if constexpr (BF16) {
-              const uint2 p = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.dy) + o);
-              x = float4{__uint_as_float(p.x << 16), __uint_as_float(p.x & 0xffff0000u), __uint_as_float(p.y << 16),
-                         __uint_as_float(p.y & 0xffff0000u)};
+    fetch(0);
+    for (int v0 = 0; v0 < keep.dvp; v0 += 32) {
+      __syncthreads();   // the previous step (the previous head) is read
+      {
+        float x[8], y[8];
+        floats(es_, x);
+        floats(ed, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sd = fmaf(x[i], y[i], sd);
+        store_row8<3>(smem + Z::oS, x, srow, sc);
+        store_row8<3>(smem + Z::oD, y, srow, sc);
+#pragma unroll
+        for (int j = 0; j < Z::kItems; ++j) {
+          const int i = tid + j * Z::kThreads;
+          if (i < Z::kTok) {
+            const int mat = __builtin_amdgcn_readfirstlane(i / (4 * C)), row = (i >> 2) % C, c = i & 3;
+            if (BF16 && mat == 2) {
+              unsigned char* p = smem + Z::oY + (row >> 4) * kFrag + 8 * (c >> 1);
+              *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1), row & 15, 0)) = uint2{et[j].lo.x, et[j].lo.y};
+              *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1) + 1, row & 15, 0)) = uint2{et[j].lo.z, et[j].lo.w};
             } else {
-              x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.dy) + o);
+              floats(et[j], x);
+              store_row8<3>(smem + (mat == 0 ? Z::oR : mat == 1 ? Z::oU : Z::oY), x, row, c);
             }
+          }
+        }
+      }
+      if (v0 == 0 && w == 0) {
+        const bool live = l < C && l < left;
+        gi = live ? a.g[(tok + l) * a.Hv + h] : 0.0f;
+        const double s = chunk_sums(gi);
+        const double end = __shfl(s, C - 1);
+        if (l < C) {
+          s_g[l] = s;
+          s_b[l] = live ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
+          s_from[l] = expf(static_cast<float>(s));
+          s_to[l] = expf(static_cast<float>(end - s));
+        }
+      }
+      __syncthreads();
+      if (v0 + 32 < keep.dvp) fetch(v0 + 32);
+      {
+        const Frag<3> sf = read_frag<3>(smem + Z::oS, w, 0);
+        {
+          Frag<NI> y[MT];
+#pragma unroll
+          for (int t = 0; t < MT; ++t) y[t] = read_frag<NI>(smem + Z::oY, t, 0);
+          mma(E, y, sf);
+        }
+        Frag<3> x[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oR, t, 0);
+        mma(F, x, sf);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oU, t, 0);
+        mma(H, x, read_frag<3>(smem + Z::oD, w, 0));
+      }
+      // job: W1, W1 transposed, W2, W2 transposed; the fragment of its operand
+#pragma unroll
+      for (int j = 0; j < Z::kJobs; ++j) {
+        const int job = w + j * NW, mat = job / Z::kTri, f = job % Z::kTri;
+        if (job < 4 * Z::kTri) {
+          const int rt = C == 32 ? f : (mat & 1) ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : (f >> 1) + 1);
+          const int st = C == 32 ? 0 : (mat & 1) ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
+          // tiles of the products (accumulator rows): 2 st, 2 st + 1; the row tile: columns
+          if (mat == 0) {
+            const Frag<NI> c = read_frag<NI>(smem + Z::oY, rt, 0);
+            Frag<3> p[2] = {read_frag<3>(smem + Z::oU, 2 * st, 0), read_frag<3>(smem + Z::oU, 2 * st + 1, 0)};
+            mma(W[j], p, c);
+          } else if (mat == 1) {
+            const Frag<3> c = read_frag<3>(smem + Z::oU, rt, 0);
+            Frag<NI> p[2] = {read_frag<NI>(smem + Z::oY, 2 * st, 0), read_frag<NI>(smem + Z::oY, 2 * st + 1, 0)};
+            mma(W[j], p, c);
           } else {
-            if (v < a.Dv) x.x = load_el<BF16>(a.dy, o);
-            if (v + 1 < a.Dv) x.y = load_el<BF16>(a.dy, o + 1);
-            if (v + 2 < a.Dv) x.z = load_el<BF16>(a.dy, o + 2);
-            if (v + 3 < a.Dv) x.w = load_el<BF16>(a.dy, o + 3);
+            const unsigned char *s1 = smem + (mat == 2 ? Z::oU : Z::oR), *s2 = smem + (mat == 2 ? Z::oR : Z::oU);
+            const Frag<3> c = read_frag<3>(s2, rt, 0);
+            Frag<3> p[2] = {read_frag<3>(s1, 2 * st, 0), read_frag<3>(s1, 2 * st + 1, 0)};
+            mma(W[j], p, c);
           }
-        }
-        return x;
-      };
-      auto load_row = [&](const float* p, int row) { return *reinterpret_cast<const float4*>(p + static_cast<int64_t>(row) * keep.dvp + v); };
-      float4 y[MT], u[MT], r[MT];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        y[t] = load_dy(t);
-        u[t] = load_row(ku, 16 * t + m);
-        r[t] = load_row(kr, 16 * t + m);
-      }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const int row = 16 * (w + 4 * d);
-        if (row < a.Dk) {
-          const float4 s = load_row(ks, row + m), e = load_row(kd, row + m);
-          sd += s.x * e.x + s.y * e.y + s.z * e.z + s.w * e.w;
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            E[d][t] = mma16(y[t], s, E[d][t]);
-            F[d][t] = mma16(r[t], s, F[d][t]);
-            H[d][t] = mma16(u[t], e, H[d][t]);
-          }
-        }
-      }
-      if (w < MT) {
-        const float4 y1 = load_dy(r1), x2 = load_row(kr, 16 * r2 + m);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          if (t <= r1) W1[t] = mma16(y1, u[t], W1[t]);
-          if (t <= r2) W2[t] = mma16(x2, u[t], W2[t]);
         }
       }
     }
-    __syncthreads();   // s_g and the decays are there
-    if (w < MT) {
+    __syncthreads();   // the last step is read
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+    for (int j = 0; j < Z::kJobs; ++j) {
+      const int job = w + j * NW, mat = job / Z::kTri, f = job % Z::kTri;
+      if (job < 4 * Z::kTri) {
+        const int rt = C == 32 ? f : (mat & 1) ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : (f >> 1) + 1);
+        const int st = C == 32 ? 0 : (mat & 1) ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
+        float x[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 16 * t + m, i1 = 16 * r1 + 4 * g + r, i2 = 16 * r2 + 4 * g + r;
-          if (t <= r1) s_w1[i1 * LD + j] = j <= i1 ? W1[t][r] * expf(static_cast<float>(s_g[i1] - s_g[j])) : 0.0f;
-          if (t <= r2) s_w2[i2 * LD + j] = j < i2 ? W2[t][r] * expf(static_cast<float>(s_g[i2] - s_g[j])) : 0.0f;
+        for (int e = 0; e < 8; ++e) {
+          const int p = 16 * (2 * st + (e >> 2)) + 4 * g + (e & 3), q = 16 * rt + m;
+          const int i = (mat & 1) ? p : q, jj = (mat & 1) ? q : p;
+          const float factor = mat < 2 ? a.scale : mat == 3 ? -s_b[i] : 1.0f;
+          const bool in = mat < 2 ? jj <= i : jj < i;
+          x[e] = in ? factor * expf(static_cast<float>(s_g[i] - s_g[jj])) * W[j][e >> 2][e & 3] : 0.0f;
         }
+        const Frag<3> fr = to_frag<3>(x);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(smem + (job * 3 + p) * kFrag + l * 16) = fr.p[p];
+      }
     }
     // dR.V of the tokens of this wave
-    for (int i = w; i < C; i += 4) {
+    for (int i = w; i < C; i += NW) {
       float s = 0.0f;
       if (i < left)
         for (int v = l; v < a.Dv; v += 64)
-          s = fmaf(kr[static_cast<int64_t>(i) * keep.dvp + v], load_el<BF16>(a.v, (tok + i) * a.ldv + static_cast<int64_t>(h) * a.Dv + v), s);
+          s = fmaf(keep.r[(cn * C + i) * keep.dvp + v], load_el<BF16>(a.v, (tok + i) * a.ldv + static_cast<int64_t>(h) * a.Dv + v), s);
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
       if (l == 0) s_rv[i] = s;
     }
-    __syncthreads();
-
-    float qa[MT][4], ka[MT][4], kc[MT][4];   // rows of q.dQ, k.Hrow, k.dKcol
-    float kh = 0.0f;                         // sum of to k.(U D'^T)
+    // k and q of this wave's features, as operands over the tokens; their slots
+    // are also the values at the accumulators' places
+    Frag<NI> kf[CS], qf[CS];
+    {
+      const unsigned char* fr = a.frags + static_cast<int64_t>(blockIdx.x) * Z::frags(true);
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) qa[t][r] = ka[t][r] = kc[t][r] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const int c = 16 * (w + 4 * d) + m;    // feature
-      float4 kv[MT], qv[MT], kb[MT];         // k, q and beta k in accumulator order, the second operand's too
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        float x[4], y[4], z[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * t + 4 * g + r;
-          x[r] = load_el<BF16>(s_k, i * LK + c);
-          y[r] = load_el<BF16>(s_q, i * LK + c);
-          z[r] = s_b[i] * x[r];
-        }
-        kv[t] = float4{x[0], x[1], x[2], x[3]};
-        qv[t] = float4{y[0], y[1], y[2], y[3]};
-        kb[t] = float4{z[0], z[1], z[2], z[3]};
-      }
-      auto rows = [&](const float* p, int it, int jt) { return *reinterpret_cast<const float4*>(p + (16 * it + m) * LD + 16 * jt + 4 * g); };
-      auto cols = [&](const float* p, int it, int jt) {   // rows jt of the transposed
-        const float* x = p + (16 * it + 4 * g) * LD + 16 * jt + m;
-        return float4{x[0], x[LD], x[2 * LD], x[3 * LD]};
-      };
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        f32x4 q1 = {0.0f, 0.0f, 0.0f, 0.0f}, k1 = q1, c1 = q1, c2 = q1;
-#pragma unroll
-        for (int s = 0; s < MT; ++s) {
-          if (s <= t) {
-            q1 = mma16(rows(s_w1, t, s), kv[s], q1);
-            k1 = mma16(rows(s_w2, t, s), kv[s], k1);
-          }
-          if (s >= t) {
-            c1 = mma16(cols(s_w1, s, t), qv[s], c1);
-            c2 = mma16(cols(s_w2, s, t), kb[s], c2);
-          }
-        }
-        const float ke[4] = {kv[t].x, kv[t].y, kv[t].z, kv[t].w}, qe[4] = {qv[t].x, qv[t].y, qv[t].z, qv[t].w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * t + 4 * g + r;
-          const float from = s_from[i], to = s_to[i];
-          const float dq = a.scale * fmaf(from, E[d][t][r], q1[r]);
-          const float hr = -fmaf(from, F[d][t][r], k1[r]);
-          const float uh = to * H[d][t][r];
-          const float dc = fmaf(a.scale, c1[r], uh) - c2[r];
-          qa[t][r] = fmaf(qe[r], dq, qa[t][r]);
-          ka[t][r] = fmaf(ke[r], hr, ka[t][r]);
-          kc[t][r] = fmaf(ke[r], dc, kc[t][r]);
-          kh = fmaf(ke[r], uh, kh);
-          dQ[d][t][r] += dq;
-          dK[d][t][r] += fmaf(s_b[i], hr, dc);
-        }
+      for (int s = 0; s < CS; ++s) {
+        kf[s] = read_cols<NI, C>(fr + Z::kMat, w, s);
+        qf[s] = read_cols<NI, C>(fr + 2 * Z::kMat, w, s);
       }
     }
+    float kh = 0.0f;   // sum of to k.(U D'^T)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const float4 fr = *reinterpret_cast<const float4*>(s_from + 16 * t + 4 * g);
+      const float4 to = *reinterpret_cast<const float4*>(s_to + 16 * t + 4 * g);
+      const float ff[4] = {fr.x, fr.y, fr.z, fr.w}, tt[4] = {to.x, to.y, to.z, to.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        E[t][r] *= a.scale * ff[r];
+        F[t][r] *= ff[r];
+        H[t][r] *= tt[r];
+        kh = fmaf(value_of(kf[t >> 1], 4 * (t & 1) + r), H[t][r], kh);
+      }
+    }
+    __syncthreads();   // W1 and W2 are there
+    auto triangle = [&](f32x4 (&c)[MT], int mat, const Frag<NI> (&x)[CS]) {
+#pragma unroll
+      for (int s = 0; s < CS; ++s) {
+        Frag<3> f[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          if ((mat & 1) ? t <= 2 * s + 1 : t >= 2 * s)
+            f[t] = read_frag<3>(smem, mat * Z::kTri + ((mat & 1) ? tri_frag_t<C>(t, s) : tri_frag<C>(t, s)), 0);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int j = 0; j < NI && i + j < 3; ++j)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+              if ((mat & 1) ? t <= 2 * s + 1 : t >= 2 * s) c[t] = mfma(f[t].p[i], x[s].p[j], c[t]);
+      }
+    };
+    triangle(E, 0, kf);    // dQ
+    triangle(F, 2, kf);    // -Hrow
+    triangle(H, 1, qf);
+    triangle(H, 3, kf);    // dKcol
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) {
-          qa[t][r] += __shfl_xor(qa[t][r], o);
-          ka[t][r] += __shfl_xor(ka[t][r], o);
-          kc[t][r] += __shfl_xor(kc[t][r], o);
-        }
+        const float kv = value_of(kf[t >> 1], 4 * (t & 1) + r), qv = value_of(qf[t >> 1], 4 * (t & 1) + r);
+        const int i = 16 * t + 4 * g + r;
+        float qa = qv * E[t][r], ka = -kv * F[t][r], kc = kv * H[t][r];
+        H[t][r] -= s_b[i] * F[t][r];   // dK of the head
+        qa = row_sum(qa);
+        ka = row_sum(ka);
+        kc = row_sum(kc);
         if (m == 0) {
-          const int i = 16 * t + 4 * g + r;
-          s_red[(w * 3 + 0) * C + i] = qa[t][r];
-          s_red[(w * 3 + 1) * C + i] = ka[t][r];
-          s_red[(w * 3 + 2) * C + i] = kc[t][r];
+          s_red[(w * 3 + 0) * C + i] = qa;
+          s_red[(w * 3 + 1) * C + i] = ka;
+          s_red[(w * 3 + 2) * C + i] = kc;
         }
       }
+    // dq and dk of the heads that share a key: in LDS until the last one
+    f32x4* sum = reinterpret_cast<f32x4*>(smem + Z::oAcc) + w * 2 * MT * 64 + l;
+    if (hh > 0) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        E[t] += sum[t * 64];
+        H[t] += sum[(MT + t) * 64];
+      }
+    }
+    if (hh + 1 < group) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        sum[t * 64] = E[t];
+        sum[(MT + t) * 64] = H[t];
+      }
+    } else {
+      const int c = 16 * w + m, ldo = a.Hk * a.Dk * es;
+      const Buf qo = rows_buf(static_cast<char*>(a.dq) + (tok * a.Hk + hk) * a.Dk * es, rows, ldo, a.Dk * es);
+      const Buf ko = rows_buf(static_cast<char*>(a.dk) + (tok * a.Hk + hk) * a.Dk * es, rows, ldo, a.Dk * es);
+      const int oo = c < a.Dk ? 4 * g * ldo + c * es : kNowhere;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          store_el<BF16>(qo, oo + (16 * t + r) * ldo, E[t][r]);
+          store_el<BF16>(ko, oo + (16 * t + r) * ldo, H[t][r]);
+        }
+    }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       sd += __shfl_xor(sd, o);
@@ -451,19 +542,19 @@ __global__ void __launch_bounds__(256) k_delta_grad(DeltaArgs a, int chunks, Del
     }
     if (l == 0) {
       s_sum[w] = sd;
-      s_sum[4 + w] = kh;
+      s_sum[NW + w] = kh;
     }
     __syncthreads();
     if (w == 0) {
       float q1 = 0.0f, k1 = 0.0f, c1 = 0.0f, s1 = 0.0f, h1 = 0.0f;
       const int i = l < C ? l : 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < NW; ++x) {
         q1 += s_red[(x * 3 + 0) * C + i];
         k1 += s_red[(x * 3 + 1) * C + i];
         c1 += s_red[(x * 3 + 2) * C + i];
         s1 += s_sum[x];
-        h1 += s_sum[4 + x];
+        h1 += s_sum[NW + x];
       }
       const float whole = expf(static_cast<float>(s_g[C - 1]));
       double dg = l < C ? static_cast<double>(q1) + s_b[i] * k1 - c1 : 0.0;
@@ -479,22 +570,6 @@ __global__ void __launch_bounds__(256) k_delta_grad(DeltaArgs a, int chunks, Del
         a.dbeta[(tok + l) * a.Hv + h] = s_rv[l] + k1;
       }
     }
-  }
-
-#pragma unroll
-  for (int d = 0; d < DT; ++d) {
-    const int c = 16 * (w + 4 * d) + m;
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * t + 4 * g + r;
-        if (i < left && c < a.Dk) {
-          const int64_t o = ((tok + i) * a.Hk + hk) * a.Dk + c;
-          store_el<BF16>(a.dq, o, dQ[d][t][r]);
-          store_el<BF16>(a.dk, o, dK[d][t][r]);
-        }
-      }
   }
 }
 
@@ -538,8 +613,8 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   scan<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, keep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.L == 0) return e;
-  const bool vec_y = a.Dv % 4 == 0;   // dy is contiguous and 16-byte aligned
-  grad<<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hk * chunks)), dim3(256), G::kLds, stream>>>(a, chunks, keep, vec_y);
+  const bool vec_y = a.Dv % (BF16 ? 8 : 4) == 0;   // dy is contiguous and 16-byte aligned
+  grad<<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hk * chunks)), dim3(G::kThreads), G::kLds - (a.Hv == a.Hk ? G::kAcc : 0), stream>>>(a, chunks, keep, vec_y);
   return hipGetLastError();
 }
 
