@@ -58,12 +58,17 @@ struct DeltaArgs {
 // one token after the other, the state in registers
 hipError_t launch_delta_tokens(const DeltaArgs& a, hipStream_t stream);
 
-// What the chains leave for the gradients (float32, columns padded with zeros
-// to 16): states S at the chunks' starts and gradients D' of their end states
-// [B*Hv][chunks][dkp][dvp], the chunks' writes U and gradients dR [B*Hv][chunks][C][dvp].
+// What the chains leave for the gradients of a chunk (float32, columns padded
+// with zeros to 16), one after the other for each of [B*Hv][chunks]: the state S
+// at its start and the gradient D' of its end state [dkp][dvp], its writes U and
+// their gradients dR [C][dvp].
 struct DeltaKeep {
-  float *s, *d, *u, *r;
+  float* p;
   int dkp, dvp;
+  __host__ __device__ int at_d() const { return dkp * dvp; }
+  __host__ __device__ int at_u() const { return 2 * dkp * dvp; }
+  __host__ __device__ int at_r(int C) const { return (2 * dkp + C) * dvp; }
+  __host__ __device__ int size(int C) const { return 2 * (dkp + C) * dvp; }
 };
 
 // the chunked form: preparation of all chunks, then the chunks in order (with

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     const float* dec = reinterpret_cast<const float*>(s_k + 3 * Z::kMat);
     f32x4 dU[MT], P[MT], dR[MT];
     if (wave_live) {
-      const Buf kd = rows_buf(keep.d + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp, keep.dkp, keep.dvp * 4, keep.dvp * 4);
+      const Buf kd = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_d(), keep.dkp, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     if (!wave_live) continue;
 
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-    const Buf kr = rows_buf(keep.r + (static_cast<int64_t>(bh) * chunks + n) * C * keep.dvp, C, keep.dvp * 4, keep.dvp * 4);
+    const Buf kr = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_r(C), C, keep.dvp * 4, keep.dvp * 4);
     const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -210,8 +210,8 @@ struct Grad : Shape<BF16, KP> {
   static constexpr int kW = 4 * kTri * 3 * kFrag;           // over the stage when that is read
   static constexpr int oG = kStage > kW ? kStage : kW;      // double sums of g
   static constexpr int oB = oG + Z::C * 8;                  // beta, from, to
-  static constexpr int oRed = oB + 3 * Z::C * 4;            // [NW][3][C] row sums
-  static constexpr int oSum = oRed + NW * 3 * Z::C * 4;     // [NW][2] sums
+  static constexpr int oRed = oB + 3 * Z::C * 4;            // [NW][2][C] row sums
+  static constexpr int oSum = oRed + NW * 2 * Z::C * 4;     // [NW][2] sums
   static constexpr int oRV = oSum + NW * 2 * 4;             // [C] dR.V
   static constexpr int oAcc = oRV + Z::C * 4;               // [NW][2 MT][64] dq and dk, where heads share a key
   static constexpr int kAcc = NW * 2 * Z::MT * kFrag, kLds = oAcc + kAcc;
@@ -219,10 +219,10 @@ struct Grad : Shape<BF16, KP> {
 
 // sum over the 16 lanes of a row (in all of them)
 __device__ __forceinline__ float row_sum(float x) {
-  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x128, 0xf, 0xf, true));   // row_ror:8
-  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x124, 0xf, 0xf, true));
-  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x122, 0xf, 0xf, true));
-  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x121, 0xf, 0xf, true));
+  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xf, 0xf, true));   // row_ror:8
+  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x124, 0xf, 0xf, true));
+  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x122, 0xf, 0xf, true));
+  return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x121, 0xf, 0xf, true));
 }
 
 // eight values of row `row` (features 8c.. of a step of 32) into row fragments
@@ -238,8 +238,9 @@ __device__ __forceinline__ void store_row8(unsigned char* base, const float (&x)
   }
 }
 
-template <bool BF16, int KP>
-__global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, DeltaKeep keep, bool vec_y) {
+// VEC: whole 16-byte groups of dy are aligned
+template <bool BF16, int KP, bool VEC>
+__global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, DeltaKeep keep) {
   using Z = Grad<BF16, KP>;
   constexpr int C = Z::C, MT = Z::MT, CS = Z::CS, NI = Z::NI, NW = Z::NW, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -268,10 +269,8 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
   for (int hh = 0; hh < group; ++hh) {
     const int h = hk * group + hh;
     const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, cn = bh * chunks + n;
-    const Buf ks = rows_buf(keep.s + cn * keep.dkp * keep.dvp, keep.dkp, ldw, ldw);
-    const Buf kd = rows_buf(keep.d + cn * keep.dkp * keep.dvp, keep.dkp, ldw, ldw);
-    const Buf ku = rows_buf(keep.u + cn * C * keep.dvp, C, ldw, ldw);
-    const Buf kr = rows_buf(keep.r + cn * C * keep.dvp, C, ldw, ldw);
+    const float* kept = keep.p + cn * keep.size(C);
+    const Buf kb = rows_buf(kept, 1, 0, keep.size(C) * 4);
     const Buf yr = rows_buf(static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es, rows, ldy, a.Dv * es);
     float gi = 0.0f;
 
@@ -279,14 +278,14 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
     struct Eight {
       uint4 lo, hi;
     };
-    auto load_kept = [&](Buf r, int row, int v) {
-      const int o = v < keep.dvp ? row * ldw + v * 4 : kNowhere;
-      return Eight{load16(r, o), load16(r, o + 16)};
+    auto load_kept = [&](int at, int row, int rows, int v) {
+      const int o = row < rows && v < keep.dvp ? at * 4 + row * ldw + v * 4 : kNowhere;
+      return Eight{load16(kb, o), load16(kb, o + 16)};
     };
     auto load_dy = [&](int row, int v) {
       const int o = row * ldy + v * es;
       Eight x{};
-      if (vec_y) {
+      if constexpr (VEC) {
         x.lo = load16(yr, v < a.Dv ? o : kNowhere);
         if constexpr (!BF16) x.hi = load16(yr, v + 4 < a.Dv ? o + 16 : kNowhere);
       } else {
@@ -312,14 +311,14 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
     Eight es_, ed, et[Z::kItems];
     const int srow = tid >> 2, sc = tid & 3;    // this thread's row of S and D' and eight of its 32 values
     auto fetch = [&](int v0) {
-      es_ = load_kept(ks, srow, v0 + 8 * sc);
-      ed = load_kept(kd, srow, v0 + 8 * sc);
+      es_ = load_kept(0, srow, keep.dkp, v0 + 8 * sc);
+      ed = load_kept(keep.at_d(), srow, keep.dkp, v0 + 8 * sc);
 #pragma unroll
       for (int j = 0; j < Z::kItems; ++j) {
         const int i = tid + j * Z::kThreads;
         if (i < Z::kTok) {
           const int mat = __builtin_amdgcn_readfirstlane(i / (4 * C)), row = (i >> 2) % C, v = v0 + 8 * (i & 3);
-          et[j] = mat == 0 ? load_kept(kr, row, v) : mat == 1 ? load_kept(ku, row, v) : load_dy(row, v);
+          et[j] = mat == 2 ? load_dy(row, v) : load_kept(mat == 0 ? keep.at_r(C) : keep.at_u(), row, C, v);
         }
       }
     };
@@ -331,8 +330,22 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
     for (int j = 0; j < Z::kJobs; ++j) W[j][0] = W[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     float sd = 0.0f;   // <D', S>
     fetch(0);
+    __syncthreads();     // the previous head's sums and decays are read
+    if (w == 0) {
+      const bool live = l < C && l < left;
+      gi = live ? a.g[(tok + l) * a.Hv + h] : 0.0f;
+      const double s = chunk_sums(gi);
+      const double end = __shfl(s, C - 1);
+      if (l < C) {
+        s_g[l] = s;
+        s_b[l] = live ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
+        s_from[l] = expf(static_cast<float>(s));
+        s_to[l] = expf(static_cast<float>(end - s));
+      }
+    }
+#pragma clang loop unroll(disable)
     for (int v0 = 0; v0 < keep.dvp; v0 += 32) {
-      __syncthreads();   // the previous step (the previous head) is read
+      __syncthreads();   // the previous step is read
       {
         float x[8], y[8];
         floats(es_, x);
@@ -357,18 +370,6 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
           }
         }
       }
-      if (v0 == 0 && w == 0) {
-        const bool live = l < C && l < left;
-        gi = live ? a.g[(tok + l) * a.Hv + h] : 0.0f;
-        const double s = chunk_sums(gi);
-        const double end = __shfl(s, C - 1);
-        if (l < C) {
-          s_g[l] = s;
-          s_b[l] = live ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
-          s_from[l] = expf(static_cast<float>(s));
-          s_to[l] = expf(static_cast<float>(end - s));
-        }
-      }
       __syncthreads();
       if (v0 + 32 < keep.dvp) fetch(v0 + 32);
       {
@@ -379,13 +380,16 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
           for (int t = 0; t < MT; ++t) y[t] = read_frag<NI>(smem + Z::oY, t, 0);
           mma(E, y, sf);
         }
+        __builtin_amdgcn_sched_barrier(0);   // one product's fragments at a time: more would spill
         Frag<3> x[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oR, t, 0);
         mma(F, x, sf);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oU, t, 0);
         mma(H, x, read_frag<3>(smem + Z::oD, w, 0));
+        __builtin_amdgcn_sched_barrier(0);
       }
       // job: W1, W1 transposed, W2, W2 transposed; the fragment of its operand
 #pragma unroll
@@ -410,6 +414,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
             mma(W[j], p, c);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     __syncthreads();   // the last step is read
@@ -426,22 +431,28 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
           const int i = (mat & 1) ? p : q, jj = (mat & 1) ? q : p;
           const float factor = mat < 2 ? a.scale : mat == 3 ? -s_b[i] : 1.0f;
           const bool in = mat < 2 ? jj <= i : jj < i;
-          x[e] = in ? factor * expf(static_cast<float>(s_g[i] - s_g[jj])) * W[j][e >> 2][e & 3] : 0.0f;
+          x[e] = in ? factor * decay_exp(s_g[i] - s_g[jj]) * W[j][e >> 2][e & 3] : 0.0f;
         }
         const Frag<3> fr = to_frag<3>(x);
 #pragma unroll
         for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(smem + (job * 3 + p) * kFrag + l * 16) = fr.p[p];
       }
     }
-    // dR.V of the tokens of this wave
-    for (int i = w; i < C; i += NW) {
+    // dR.V: every wave C / NW tokens side by side, kLanes lanes a token
+    {
+      constexpr int kLanes = 64 * NW / C;
+      const int i = tid / kLanes, lv = 4 * (tid % kLanes), ldv = static_cast<int>(a.ldv) * es;
+      const Buf vr = rows_buf(static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es, rows, ldv, a.Dv * es);
       float s = 0.0f;
-      if (i < left)
-        for (int v = l; v < a.Dv; v += 64)
-          s = fmaf(keep.r[(cn * C + i) * keep.dvp + v], load_el<BF16>(a.v, (tok + i) * a.ldv + static_cast<int64_t>(h) * a.Dv + v), s);
+      for (int v = lv; v < a.Dv; v += 4 * kLanes) {
+        const uint4 r = load16(kb, (keep.at_r(C) + i * keep.dvp + v) * 4);
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
-      if (l == 0) s_rv[i] = s;
+        for (int e = 0; e < 4; ++e)
+          s = fmaf(__uint_as_float(word(r, e)), value<BF16>(load_raw<BF16>(vr, v + e < a.Dv ? i * ldv + (v + e) * es : kNowhere)), s);
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor(s, o);
+      if (tid % kLanes == 0) s_rv[i] = s;
     }
     // k and q of this wave's features, as operands over the tokens; their slots
     // are also the values at the accumulators' places
@@ -487,24 +498,25 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
       }
     };
     triangle(E, 0, kf);    // dQ
+    __builtin_amdgcn_sched_barrier(0);
     triangle(F, 2, kf);    // -Hrow
+    __builtin_amdgcn_sched_barrier(0);
     triangle(H, 1, qf);
+    __builtin_amdgcn_sched_barrier(0);
     triangle(H, 3, kf);    // dKcol
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float kv = value_of(kf[t >> 1], 4 * (t & 1) + r), qv = value_of(qf[t >> 1], 4 * (t & 1) + r);
         const int i = 16 * t + 4 * g + r;
-        float qa = qv * E[t][r], ka = -kv * F[t][r], kc = kv * H[t][r];
-        H[t][r] -= s_b[i] * F[t][r];   // dK of the head
-        qa = row_sum(qa);
-        ka = row_sum(ka);
-        kc = row_sum(kc);
+        const float row = s_b[i] * F[t][r];
+        const float ga = row_sum(qv * E[t][r] - kv * (H[t][r] + row)), ka = row_sum(-kv * F[t][r]);
+        H[t][r] -= row;   // dK of the head
         if (m == 0) {
-          s_red[(w * 3 + 0) * C + i] = qa;
-          s_red[(w * 3 + 1) * C + i] = ka;
-          s_red[(w * 3 + 2) * C + i] = kc;
+          s_red[2 * w * C + i] = ga;
+          s_red[(2 * w + 1) * C + i] = ka;
         }
       }
     // dq and dk of the heads that share a key: in LDS until the last one
@@ -546,18 +558,17 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
     }
     __syncthreads();
     if (w == 0) {
-      float q1 = 0.0f, k1 = 0.0f, c1 = 0.0f, s1 = 0.0f, h1 = 0.0f;
+      float g1 = 0.0f, k1 = 0.0f, s1 = 0.0f, h1 = 0.0f;
       const int i = l < C ? l : 0;
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
-        q1 += s_red[(x * 3 + 0) * C + i];
-        k1 += s_red[(x * 3 + 1) * C + i];
-        c1 += s_red[(x * 3 + 2) * C + i];
+        g1 += s_red[2 * x * C + i];
+        k1 += s_red[(2 * x + 1) * C + i];
         s1 += s_sum[x];
         h1 += s_sum[NW + x];
       }
       const float whole = expf(static_cast<float>(s_g[C - 1]));
-      double dg = l < C ? static_cast<double>(q1) + s_b[i] * k1 - c1 : 0.0;
+      double dg = l < C ? g1 : 0.0f;
       if (l == C - 1) dg += static_cast<double>(whole) * s1 + h1;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -579,13 +590,9 @@ int64_t keep_of(DeltaArgs& a, DeltaKeep& k) {
   const int64_t chunks = static_cast<int64_t>(a.B) * a.Hv * ((a.L + C - 1) / C);
   k.dkp = (a.Dk + 15) & ~15;
   k.dvp = (a.Dv + 15) & ~15;
-  const int64_t head = delta_work(a, true), state = chunks * k.dkp * k.dvp * 4, rows = chunks * C * k.dvp * 4;
-  unsigned char* p = static_cast<unsigned char*>(a.ws);
-  k.s = reinterpret_cast<float*>(p + head);
-  k.d = reinterpret_cast<float*>(p + head + state);
-  k.u = reinterpret_cast<float*>(p + head + 2 * state);
-  k.r = reinterpret_cast<float*>(p + head + 2 * state + rows);
-  return head + 2 * state + 2 * rows;
+  const int64_t head = delta_work(a, true);
+  k.p = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + head);
+  return head + chunks * k.size(C) * 4;
 }
 
 template <bool BF16, int KP>
@@ -594,10 +601,12 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   using Z = Back<BF16, KP>;
   using G = Grad<BF16, KP>;
   auto* scan = k_delta_back_scan<BF16, KP, NW>;
-  auto* grad = k_delta_grad<BF16, KP>;
-  static const hipError_t attr[2] = {
+  auto* grad_vec = k_delta_grad<BF16, KP, true>;
+  auto* grad_one = k_delta_grad<BF16, KP, false>;
+  static const hipError_t attr[3] = {
       hipFuncSetAttribute(reinterpret_cast<const void*>(scan), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(grad), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds)};
+      hipFuncSetAttribute(reinterpret_cast<const void*>(grad_vec), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds),
+      hipFuncSetAttribute(reinterpret_cast<const void*>(grad_one), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds)};
   for (hipError_t e : attr)
     if (e != hipSuccess) return e;
   const int chunks = (a.L + C - 1) / C;
@@ -613,8 +622,9 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   scan<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, keep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.L == 0) return e;
-  const bool vec_y = a.Dv % (BF16 ? 8 : 4) == 0;   // dy is contiguous and 16-byte aligned
-  grad<<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hk * chunks)), dim3(G::kThreads), G::kLds - (a.Hv == a.Hk ? G::kAcc : 0), stream>>>(a, chunks, keep, vec_y);
+  // dy is contiguous and 16-byte aligned
+  auto* grad = a.Dv % (BF16 ? 8 : 4) == 0 ? grad_vec : grad_one;
+  grad<<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hk * chunks)), dim3(G::kThreads), G::kLds - (a.Hv == a.Hk ? G::kAcc : 0), stream>>>(a, chunks, keep);
   return hipGetLastError();
 }
 

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
       for (int r = 0; r < 4; ++r) {
         const int i = 16 * it + 4 * g + r;
         float x = 0.0f;
-        if (j < i) x = s_b[i] * expf(static_cast<float>(s_g[i] - s_g[j])) * acc[r];
+        if (j < i) x = s_b[i] * decay_exp(s_g[i] - s_g[j]) * acc[r];
         s_a[i * LD + j] = x;
         // a key that is not finite, or whose length is not
         if (i == j && !(acc[r] < INFINITY)) atomicMin(s_bad, i);
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
       for (int r = 0; r < 4; ++r) {
         const int p = 16 * pt + 4 * g + r, q = 16 * rt + m;   // product and row
         const int i = BACK ? p : q, j = BACK ? q : p;
-        x[4 * half + r] = j <= i ? expf(static_cast<float>(s_g[i] - s_g[j])) * acc[r] : 0.0f;
+        x[4 * half + r] = j <= i ? decay_exp(s_g[i] - s_g[j]) * acc[r] : 0.0f;
       }
     }
     constexpr int NPP = BACK ? 3 : NO;
@@ -155,6 +155,10 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
   }
   __syncthreads();
   const int bad = *s_bad;
+  if (bad < C) {   // rows from a token that is not finite on stay those of I
+    for (int i = bad * LD + tid; i < C * LD; i += kThreads) s_a[i] = 0.0f;
+    __syncthreads();
+  }
 
   // diagonal blocks: column m of block w, rows one after the other
   for (int d = w; d < MT; d += kWaves) {
@@ -162,10 +166,15 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == m ? 1.0f : 0.0f;
-      const float* row = s_a + (16 * d + i) * LD + 16 * d;
-      const bool ok = 16 * d + i < bad;    // rows from a bad token on stay those of I
+      const float4* row = reinterpret_cast<const float4*>(s_a + (16 * d + i) * LD + 16 * d);
 #pragma unroll
-      for (int j = 0; j < i; ++j) s = fmaf(ok ? -row[j] : 0.0f, x[j], s);
+      for (int j = 0; j < i; j += 4) {
+        const float4 v = row[j >> 2];
+        s = fmaf(-v.x, x[j], s);
+        if (j + 1 < i) s = fmaf(-v.y, x[j + 1], s);
+        if (j + 2 < i) s = fmaf(-v.z, x[j + 2], s);
+        if (j + 3 < i) s = fmaf(-v.w, x[j + 3], s);
+      }
       x[i] = s;
     }
     if (g == 0) {
@@ -184,11 +193,6 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
     return *reinterpret_cast<const float4*>(p + (16 * it + m) * LD + 16 * jt + 4 * g);
   };
   auto column = [&](int kt, int jt, int r) { return s_t[(16 * kt + 4 * g + r) * LD + 16 * jt + m]; };
-  auto a_block = [&](int it, int jt) {
-    float4 v = quad(s_a, it, jt);
-    if (16 * it + m >= bad) v = float4{0.0f, 0.0f, 0.0f, 0.0f};
-    return v;
-  };
   auto put = [&](int it, int jt, f32x4 v) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) s_t[(16 * it + 4 * g + r) * LD + 16 * jt + m] = -v[r];
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
   if (w < MT / 2) {
     const int it = 2 * w + 1, jt = 2 * w;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, out = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float4 p = a_block(it, jt);
+    const float4 p = quad(s_a, it, jt);
     const float pa[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc = mfma4(pa[r], column(jt, jt, r), acc);
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
     for (int kt = 2; kt <= it; ++kt) {
       f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int lt = jt; lt < 2; ++lt) {
-        const float4 p = a_block(kt, lt);
+        const float4 p = quad(s_a, kt, lt);
         const float pa[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc = mfma4(pa[r], column(lt, jt, r), acc);

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     const unsigned char *s_kt = s_k + Z::kMat, *s_q = s_k + 2 * Z::kMat, *rec = s_k + Z::kFrags;
     const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - kFrag);
     if constexpr (KEEP) {
-      const Buf p = rows_buf(keep.s + (static_cast<int64_t>(bh) * chunks + n) * keep.dkp * keep.dvp, keep.dkp, keep.dvp * 4, keep.dvp * 4);
+      const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C), keep.dkp, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     tri_mma<C, 3>(U, rec + Record<C>::T, X);
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     if constexpr (KEEP) {
-      const Buf p = rows_buf(keep.u + (static_cast<int64_t>(bh) * chunks + n) * C * keep.dvp, C, keep.dvp * 4, keep.dvp * 4);
+      const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_u(), C, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll

@@ -437,6 +437,11 @@ __device__ __forceinline__ double chunk_sums(float g) {
   return s;
 }
 
+// e^x for the factors M_ij <= 1 of products: the hardware's exponential of
+// x log2(e), off by up to (1 + |x|) 2^-24 of e^x and so by less than 2^-23 of
+// the factor of neighbours, which the small ones are added to
+__device__ __forceinline__ float decay_exp(double x) { return __expf(static_cast<float>(x)); }
+
 __device__ __forceinline__ int length_of(const DeltaArgs& a, int b) {
   if (a.lengths == nullptr) return a.L;
   const int n = __builtin_amdgcn_readfirstlane(a.lengths[b]);
