@@ -434,28 +434,34 @@ def set_profiling_events(events) -> None:
 # ---- gated delta rule, and the norm and rotation of its queries and keys ------
 
 
-class _On:
-    """The device of `t` as the current one and, if a stream is given, that
-    stream as torch's: outputs and workspaces are then allocated for the
-    stream that the kernels run on. Costs nothing where both already are."""
+# These calls take a few microseconds on the GPU where a model decodes, so the
+# checks are written for the case that they pass: one comparison of each
+# property, and the words for what is wrong only after that.
 
-    def __init__(self, t, stream):
-        import torch
-        self.contexts = []
-        if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(t.device))
-        if stream is not None:
-            if t.device.type == "cuda" and stream.device != t.device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-            self.contexts.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
+def _on(t, stream):
+    """None where t's device is the current one and no stream is given; else a
+    context that makes both torch's, so that outputs and workspaces are
+    allocated for the stream that the kernels run on."""
+    import torch
+    if t.device.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU device, got {t.device}")
+    if stream is None and t.device.index == torch.cuda.current_device():
+        return None
+    import contextlib
+    c = contextlib.ExitStack()
+    c.enter_context(torch.cuda.device(t.device))
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        c.enter_context(torch.cuda.stream(stream))
+    return c
 
-    def __exit__(self, *e):
-        for c in reversed(self.contexts):
-            c.__exit__(*e)
+
+def _raw_stream(device) -> int:
+    """Handle of torch's current stream on the device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _same_device(t, name, device):
@@ -467,6 +473,11 @@ def _given(t, name, dtype, shape, device):
     """Pointer of a checked contiguous tensor, None for None."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _dev_tensor(t, name, dtype, shape)
     _same_device(t, name, device)
     return t.data_ptr()
@@ -488,21 +499,23 @@ def _heads(t, name, dtype, lead, device):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
-    _same_device(t, name, device)
-    if t.dtype != dtype:
+    if t.device != device:
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+        _same_device(t, name, device)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     n = len(lead)
-    if t.dim() != n + 2 or tuple(t.shape[:n]) != tuple(lead):
-        raise ValueError(f"{name} must have shape {tuple(lead)} + (heads, features), got {tuple(t.shape)}")
-    H, D = t.shape[n:]
+    shape = t.shape
+    if len(shape) != n + 2 or shape[:n] != lead:
+        raise ValueError(f"{name} must have shape {tuple(lead)} + (heads, features), got {tuple(shape)}")
+    H, D = shape[n:]
     if H < 1 or D < 1:
-        raise ValueError(f"{name} must have heads and features, got {tuple(t.shape)}")
-    st = t.stride()
+        raise ValueError(f"{name} must have heads and features, got {tuple(shape)}")
     row = H * D
-    if t.numel() == 0 or t.is_contiguous():
+    if t.is_contiguous() or t.numel() == 0:
         return row
+    st = t.stride()
     if (D > 1 and st[n + 1] != 1) or (H > 1 and st[n] != D):
         raise ValueError(f"{name}: the heads and features of a token must be contiguous, got strides {st}")
     ld, rows = None, 1   # from the innermost leading dimension outwards
@@ -520,9 +533,16 @@ def _heads(t, name, dtype, lead, device):
     return ld
 
 
-def _workspace(nbytes, device):
+def _workspace(desc, device, fn, *more):
+    """Allocates what the library asks for (fn: its query) and enters it in desc."""
     import torch
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    need = ctypes.c_int64()
+    _check(fn(ctypes.byref(desc), *more, ctypes.byref(need)), fn.__name__)
+    if need.value == 0:
+        return None
+    ws = torch.empty(need.value, dtype=torch.uint8, device=device)
+    desc.workspace, desc.workspace_bytes = ws.data_ptr(), need.value
+    return ws
 
 
 def _delta_desc(q, k, v, g, beta, s0, scale, lengths):
@@ -547,17 +567,6 @@ def _delta_desc(q, k, v, g, beta, s0, scale, lengths):
     return d, dev
 
 
-def _run_delta(desc, backward, stream, device):
-    L = lib()
-    need = ctypes.c_int64()
-    name = "s5_gated_delta_backward" if backward else "s5_gated_delta"
-    _check(L.s5_gated_delta_workspace(ctypes.byref(desc), int(backward), ctypes.byref(need)), name)
-    ws = _workspace(need.value, device)
-    if ws is not None:
-        desc.workspace, desc.workspace_bytes = ws.data_ptr(), need.value
-    _check(getattr(L, name)(ctypes.byref(desc), _stream_handle(stream)), name)
-
-
 def gated_delta(q, k, v, g, beta, s0=None, *, scale=None, lengths=None, final_state=False, y=None, s_last=None,
                 stream=None):
     """The gated delta rule (s5_gated_delta) over whole sequences:
@@ -573,15 +582,19 @@ def gated_delta(q, k, v, g, beta, s0=None, *, scale=None, lengths=None, final_st
     Returns (y, s_last), s_last None unless final_state is set or a buffer is
     given (which may be s0)."""
     import torch
-    with _On(v, stream):
-        d, dev = _delta_desc(q, k, v, g, beta, s0, scale, lengths)
-        B, L, Hv, Dv = v.shape
-        y = _made(y, "y", v.dtype, (B, L, Hv, Dv), dev, zero=lengths is not None)
-        if final_state or s_last is not None:
-            s_last = _made(s_last, "s_last", torch.float32, (B, Hv, d.Dk, Dv), dev)
-            d.s_last = s_last.data_ptr()
-        d.y = y.data_ptr()
-        _run_delta(d, False, stream, dev)
+    on = _on(v, stream)
+    if on is not None:
+        with on:
+            return gated_delta(q, k, v, g, beta, s0, scale=scale, lengths=lengths, final_state=final_state, y=y, s_last=s_last)
+    d, dev = _delta_desc(q, k, v, g, beta, s0, scale, lengths)
+    B, L, Hv, Dv = v.shape
+    y = _made(y, "y", v.dtype, (B, L, Hv, Dv), dev, zero=lengths is not None)
+    if final_state or s_last is not None:
+        s_last = _made(s_last, "s_last", torch.float32, (B, Hv, d.Dk, Dv), dev)
+        d.s_last = s_last.data_ptr()
+    d.y = y.data_ptr()
+    ws = _workspace(d, dev, lib().s5_gated_delta_workspace, 0)   # noqa: F841  (held until the call is enqueued)
+    _check(lib().s5_gated_delta(ctypes.byref(d), _raw_stream(dev)), "s5_gated_delta")
     return y, s_last
 
 
@@ -593,22 +606,27 @@ def gated_delta_backward(dy, q, k, v, g, beta, s0=None, ds_last=None, *, scale=N
     ds0), ds0 None unless s0 or a buffer for it is given. With lengths the
     rows behind are zero in gradients made here and left in given ones."""
     import torch
-    with _On(v, stream):
-        d, dev = _delta_desc(q, k, v, g, beta, s0, scale, lengths)
-        B, L, Hv, Dv = v.shape
-        f32, zero = torch.float32, lengths is not None
-        d.dy = _given(dy, "dy", v.dtype, (B, L, Hv, Dv), dev)
-        d.ds_last = _given(ds_last, "ds_last", f32, (B, Hv, d.Dk, Dv), dev)
-        dq = _made(dq, "dq", v.dtype, tuple(q.shape), dev, zero)
-        dk = _made(dk, "dk", v.dtype, tuple(k.shape), dev, zero)
-        dv = _made(dv, "dv", v.dtype, (B, L, Hv, Dv), dev, zero)
-        dg = _made(dg, "dg", f32, (B, L, Hv), dev, zero)
-        dbeta = _made(dbeta, "dbeta", f32, (B, L, Hv), dev, zero)
-        if s0 is not None or ds0 is not None:
-            ds0 = _made(ds0, "ds0", f32, (B, Hv, d.Dk, Dv), dev)
-            d.ds0 = ds0.data_ptr()
-        d.dq, d.dk, d.dv, d.dg, d.dbeta = (t.data_ptr() for t in (dq, dk, dv, dg, dbeta))
-        _run_delta(d, True, stream, dev)
+    on = _on(v, stream)
+    if on is not None:
+        with on:
+            return gated_delta_backward(dy, q, k, v, g, beta, s0, ds_last, scale=scale, lengths=lengths, dq=dq, dk=dk, dv=dv,
+                                        dg=dg, dbeta=dbeta, ds0=ds0)
+    d, dev = _delta_desc(q, k, v, g, beta, s0, scale, lengths)
+    B, L, Hv, Dv = v.shape
+    f32, zero = torch.float32, lengths is not None
+    d.dy = _given(dy, "dy", v.dtype, (B, L, Hv, Dv), dev)
+    d.ds_last = _given(ds_last, "ds_last", f32, (B, Hv, d.Dk, Dv), dev)
+    dq = _made(dq, "dq", v.dtype, tuple(q.shape), dev, zero)
+    dk = _made(dk, "dk", v.dtype, tuple(k.shape), dev, zero)
+    dv = _made(dv, "dv", v.dtype, (B, L, Hv, Dv), dev, zero)
+    dg = _made(dg, "dg", f32, (B, L, Hv), dev, zero)
+    dbeta = _made(dbeta, "dbeta", f32, (B, L, Hv), dev, zero)
+    if s0 is not None or ds0 is not None:
+        ds0 = _made(ds0, "ds0", f32, (B, Hv, d.Dk, Dv), dev)
+        d.ds0 = ds0.data_ptr()
+    d.dq, d.dk, d.dv, d.dg, d.dbeta = (t.data_ptr() for t in (dq, dk, dv, dg, dbeta))
+    ws = _workspace(d, dev, lib().s5_gated_delta_workspace, 1)   # noqa: F841  (held until the call is enqueued)
+    _check(lib().s5_gated_delta_backward(ctypes.byref(d), _raw_stream(dev)), "s5_gated_delta_backward")
     return dq, dk, dv, dg, dbeta, ds0
 
 
@@ -619,24 +637,29 @@ def gated_delta_step(q, k, v, g, beta, s, *, scale=None, y=None, stream=None):
     import torch
     if v.dim() != 3:
         raise ValueError("v must be [B, Hv, Dv]")
+    on = _on(v, stream)
+    if on is not None:
+        with on:
+            return gated_delta_step(q, k, v, g, beta, s, scale=scale, y=y)
     B, Hv, Dv = v.shape
-    dev, io = v.device, _io_code(v.dtype)
-    with _On(v, stream):
-        ldv = _heads(v, "v", v.dtype, (B,), dev)
-        ldk = _heads(k, "k", v.dtype, (B,), dev)
-        ldq = _heads(q, "q", v.dtype, (B,), dev)
-        Hk, Dk = k.shape[1:]
-        if q.shape != k.shape:
-            raise ValueError(f"q and k must have one shape, got {tuple(q.shape)} and {tuple(k.shape)}")
-        if Hv % Hk:
-            raise ValueError(f"the value heads ({Hv}) must be a multiple of the key heads ({Hk})")
-        gp = _given(g, "g", torch.float32, (B, Hv), dev)
-        bp = _given(beta, "beta", torch.float32, (B, Hv), dev)
-        sp = _given(s, "s", torch.float32, (B, Hv, Dk, Dv), dev)
-        y = _made(y, "y", v.dtype, (B, Hv, Dv), dev)
-        _check(lib().s5_gated_delta_step(B, Hk, Hv, Dk, Dv, io, ldq, ldk, ldv, Dk ** -0.5 if scale is None else scale,
-                                         q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp, sp, y.data_ptr(),
-                                         _stream_handle(stream)), "s5_gated_delta_step")
+    dev, dtype = v.device, v.dtype
+    io = _io_code(dtype)
+    ldv = _heads(v, "v", dtype, (B,), dev)
+    ldk = _heads(k, "k", dtype, (B,), dev)
+    ldq = _heads(q, "q", dtype, (B,), dev)
+    Hk, Dk = k.shape[1:]
+    if q.shape != k.shape:
+        raise ValueError(f"q and k must have one shape, got {tuple(q.shape)} and {tuple(k.shape)}")
+    if Hv % Hk:
+        raise ValueError(f"the value heads ({Hv}) must be a multiple of the key heads ({Hk})")
+    f32 = torch.float32
+    gp = _given(g, "g", f32, (B, Hv), dev)
+    bp = _given(beta, "beta", f32, (B, Hv), dev)
+    sp = _given(s, "s", f32, (B, Hv, Dk, Dv), dev)
+    y = _made(y, "y", dtype, (B, Hv, Dv), dev)
+    _check(lib().s5_gated_delta_step(B, Hk, Hv, Dk, Dv, io, ldq, ldk, ldv, Dk ** -0.5 if scale is None else scale,
+                                     q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp, sp, y.data_ptr(), _raw_stream(dev)),
+           "s5_gated_delta_step")
     return y
 
 
@@ -644,7 +667,7 @@ def _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, 
     import torch
     if q.dim() not in (3, 4):
         raise ValueError("q must be [T, Hq, D] or [B, L, Hq, D]")
-    lead, dev, io = tuple(q.shape[:-2]), q.device, _io_code(q.dtype)
+    lead, dev, io = q.shape[:-2], q.device, _io_code(q.dtype)
     ldq = _heads(q, "q", q.dtype, lead, dev)
     ldk = _heads(k, "k", q.dtype, lead, dev)
     (Hq, D), Hk = q.shape[-2:], k.shape[-2]
@@ -685,12 +708,16 @@ def qk_norm_rope(q, k, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, fr
     (j, j + R/2), or (2j, 2j + 1) if interleaved. positions int32, shaped as
     the tokens; None counts 0, 1, ... along L (T). Returns contiguous
     (q_out, k_out); a contiguous input may be its own output."""
-    with _On(q, stream):
-        d, dev = _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, interleaved)
-        q_out = _made(q_out, "q_out", q.dtype, tuple(q.shape), dev)
-        k_out = _made(k_out, "k_out", q.dtype, tuple(k.shape), dev)
-        d.q_out, d.k_out = q_out.data_ptr(), k_out.data_ptr()
-        _check(lib().s5_qk_norm_rope(ctypes.byref(d), _stream_handle(stream)), "s5_qk_norm_rope")
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return qk_norm_rope(q, k, norm=norm, q_weight=q_weight, k_weight=k_weight, eps=eps, freqs=freqs, positions=positions,
+                                rope_scale=rope_scale, interleaved=interleaved, q_out=q_out, k_out=k_out)
+    d, dev = _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, interleaved)
+    q_out = _made(q_out, "q_out", q.dtype, q.shape, dev)
+    k_out = _made(k_out, "k_out", q.dtype, k.shape, dev)
+    d.q_out, d.k_out = q_out.data_ptr(), k_out.data_ptr()
+    _check(lib().s5_qk_norm_rope(ctypes.byref(d), _raw_stream(dev)), "s5_qk_norm_rope")
     return q_out, k_out
 
 
@@ -702,25 +729,26 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, *, norm="rms", q_weight=None, k_
     (dq, dk, dq_weight, dk_weight), a weight's gradient None without the
     weight."""
     import torch
-    with _On(q, stream):
-        d, dev = _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, interleaved)
-        d.dq_out = _given(dq_out, "dq_out", q.dtype, tuple(q.shape), dev)
-        d.dk_out = _given(dk_out, "dk_out", q.dtype, tuple(k.shape), dev)
-        dq = _made(dq, "dq", q.dtype, tuple(q.shape), dev)
-        dk = _made(dk, "dk", q.dtype, tuple(k.shape), dev)
-        if q_weight is not None or dq_weight is not None:
-            dq_weight = _made(dq_weight, "dq_weight", torch.float32, (d.D,), dev)
-            d.dq_weight = dq_weight.data_ptr()
-        if k_weight is not None or dk_weight is not None:
-            dk_weight = _made(dk_weight, "dk_weight", torch.float32, (d.D,), dev)
-            d.dk_weight = dk_weight.data_ptr()
-        d.q_out, d.k_out = dq.data_ptr(), dk.data_ptr()
-        need = ctypes.c_int64()
-        _check(lib().s5_qk_workspace(ctypes.byref(d), ctypes.byref(need)), "s5_qk_norm_rope_backward")
-        ws = _workspace(need.value, dev)
-        if ws is not None:
-            d.workspace, d.workspace_bytes = ws.data_ptr(), need.value
-        _check(lib().s5_qk_norm_rope_backward(ctypes.byref(d), _stream_handle(stream)), "s5_qk_norm_rope_backward")
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, norm=norm, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                         freqs=freqs, positions=positions, rope_scale=rope_scale, interleaved=interleaved,
+                                         dq=dq, dk=dk, dq_weight=dq_weight, dk_weight=dk_weight)
+    d, dev = _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, interleaved)
+    d.dq_out = _given(dq_out, "dq_out", q.dtype, q.shape, dev)
+    d.dk_out = _given(dk_out, "dk_out", q.dtype, k.shape, dev)
+    dq = _made(dq, "dq", q.dtype, q.shape, dev)
+    dk = _made(dk, "dk", q.dtype, k.shape, dev)
+    if q_weight is not None or dq_weight is not None:
+        dq_weight = _made(dq_weight, "dq_weight", torch.float32, (d.D,), dev)
+        d.dq_weight = dq_weight.data_ptr()
+    if k_weight is not None or dk_weight is not None:
+        dk_weight = _made(dk_weight, "dk_weight", torch.float32, (d.D,), dev)
+        d.dk_weight = dk_weight.data_ptr()
+    d.q_out, d.k_out = dq.data_ptr(), dk.data_ptr()
+    ws = _workspace(d, dev, lib().s5_qk_workspace)   # noqa: F841  (held until the call is enqueued)
+    _check(lib().s5_qk_norm_rope_backward(ctypes.byref(d), _raw_stream(dev)), "s5_qk_norm_rope_backward")
     return dq, dk, dq_weight, dk_weight
 
 
