@@ -71,10 +71,30 @@ struct DeltaKeep {
   __host__ __device__ int size(int C) const { return 2 * (dkp + C) * dvp; }
 };
 
+// Long sequences of few heads are cut into `count` segments of `chunks` chunks
+// that run side by side: their states from a zero start, with the product of
+// their transitions, are found first and joined in order. Of every [B*Hv]
+// [segment]: [dkp][dvp + dkp] floats, the state from zero (after the join the
+// state at the segment's end) and the transition; backward also [dkp][dvp], the
+// gradient of the state at the segment's start.
+struct DeltaSegs {
+  float *p, *back;
+  int count, chunks, dkp, dvp;
+  __host__ __device__ int ld() const { return dvp + dkp; }
+  __host__ __device__ int64_t at(int64_t bh, int seg) const { return (bh * count + seg) * dkp * ld(); }
+  __host__ __device__ int64_t at_back(int64_t bh, int seg) const { return (bh * count + seg) * dkp * dvp; }
+};
+
 // the chunked form: preparation of all chunks, then the chunks in order (with
 // `keep` no outputs but S and U for the backward pass)
-// `work` finds the workspace's parts and gives the bytes of fragments and records
-int64_t delta_work(DeltaArgs& a, bool backward);
+// finds the workspace's parts and gives the bytes of fragments, records and segments
+int64_t delta_work(DeltaArgs& a, DeltaSegs& segs, bool backward);
+hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
+hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep* keep, hipStream_t stream);
+// the gradients at the segments' starts from those of their sums
+hipError_t launch_delta_join_back(const DeltaArgs& a, const DeltaSegs& segs, hipStream_t stream);
+// finds the workspace's parts and gives the bytes of fragments, records and segments
+int64_t delta_work(DeltaArgs& a, DeltaSegs& segs, bool backward);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaKeep* keep, hipStream_t stream);
 

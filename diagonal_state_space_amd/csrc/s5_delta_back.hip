@@ -38,21 +38,27 @@ struct Back : Shape<BF16, KP> {
   static constexpr int kLds = oTri + 2 * kTri;
 };
 
-template <bool BF16, int KP, int NW>
-__global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, int chunks, int groups, DeltaKeep keep) {
+// SUM: only the gradients at the segments' starts, from zero ends (the last
+// segment's from ds_last)
+template <bool BF16, int KP, int NW, bool SUM>
+__global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, int chunks, int groups, DeltaSegs segs, DeltaKeep keep) {
   using Z = Back<BF16, KP>;
   constexpr int C = Z::C, NI = Z::NI, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int die = blockIdx.x & 7, turn = blockIdx.x >> 3;
-  const int bh = (turn / groups) * 8 + die, cg = turn % groups;
+  const int count = SUM ? segs.count - 1 : segs.count;   // sums: segments 1, 2, ...
+  const int cg = turn % groups, seg = (turn / groups) % count + (SUM ? 1 : 0), bh = turn / (groups * count) * 8 + die;
   if (bh >= a.B * a.Hv) return;
   const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / (a.Hv / a.Hk);
   const int col = (cg * NW + w) * 16 + m;
   const bool wave_live = (cg * NW + w) * 16 < a.Dv, live = col < a.Dv;
   const int len = length_of(a, b);
   const int nc = (len + C - 1) / C;
+  const int n0 = seg * segs.chunks, n1 = min(nc, n0 + segs.chunks);
+  if (seg > 0 && n0 >= nc) return;
+  const bool last = n0 + segs.chunks >= nc;
 
   if (w == NW) {   // the copying wave
     auto record = [&](int n) { return a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true, 3); };
@@ -62,31 +68,35 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
       lds_copy<1>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(true), 3 * Z::kMat, 0);
       lds_copy<1>(dst + 3 * Z::kMat, record(n) + Record<C>::decays(true, 3), kFrag, 0);
     };
-    if (nc > 0) {
-      if (Z::kTwo) copy(nc - 1);
-      copy_tri(nc - 1);
+    if (n0 < n1) {
+      if (Z::kTwo) copy(n1 - 1);
+      copy_tri(n1 - 1);
     }
-    for (int n = nc - 1; n >= 0; --n) {
+    for (int n = n1 - 1; n >= n0; --n) {
       if constexpr (!Z::kTwo) {
         barrier_copied();
         copy(n);
       }
       barrier_copied();
-      if (Z::kTwo && n > 0) copy(n - 1);
+      if (Z::kTwo && n > n0) copy(n - 1);
       barrier_copied();
-      if (n > 0) copy_tri(n - 1);
+      if (n > n0) copy_tri(n - 1);
     }
     return;
   }
 
   f32x4 D[KT];
+  {
+    // the end: the call's, or the start of the segment behind
+    const int ld = (last ? a.Dv : segs.dvp) * 4;
+    const Buf p = last ? rows_buf(a.ds_last + static_cast<int64_t>(bh) * a.Dk * a.Dv, a.ds_last != nullptr ? a.Dk : 0, ld, ld)
+                       : rows_buf(segs.back + segs.at_back(bh, seg + 1), SUM ? 0 : segs.dkp, ld, ld);
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * t + 4 * g + r;
-      D[t][r] = a.ds_last != nullptr && live && row < a.Dk ? a.ds_last[(static_cast<int64_t>(bh) * a.Dk + row) * a.Dv + col] : 0.0f;
-    }
+      for (int r = 0; r < 4; ++r)
+        D[t][r] = __uint_as_float(load_raw<false>(p, live ? (16 * t + 4 * g + r) * ld + col * 4 : kNowhere));
+  }
 
   uint32_t ob[MT][4];
   const int ldy = a.Hv * a.Dv * es;
@@ -103,8 +113,8 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
       for (int r = 0; r < 4; ++r) ob[t][r] = load_raw<BF16>(yr, yo + (16 * t + r) * ldy);
   };
 
-  if (nc > 0) fetch(nc - 1);
-  for (int n = nc - 1; n >= 0; --n) {
+  if (n0 < n1) fetch(n1 - 1);
+  for (int n = n1 - 1; n >= n0; --n) {
     if constexpr (!Z::kTwo) barrier_read();   // the previous chunk is read
     barrier_read();                           // the chunk is there, the previous one read
     f32x4 dO[MT];
@@ -112,18 +122,20 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dO[t][r] = value<BF16>(ob[t][r]);
-    if (n > 0) fetch(n - 1);
+    if (n > n0) fetch(n - 1);
 
     const unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
     const unsigned char *s_kt = s_k + Z::kMat, *s_qt = s_k + 2 * Z::kMat;
     const float* dec = reinterpret_cast<const float*>(s_k + 3 * Z::kMat);
     f32x4 dU[MT], P[MT], dR[MT];
     if (wave_live) {
+      if constexpr (!SUM) {
       const Buf kd = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_d(), keep.dkp, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) store_el<false>(kd, ko + (16 * t + r) * keep.dvp * 4, D[t][r]);
+      }
 #pragma unroll
       for (int t = 0; t < MT; ++t) dU[t] = P[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -158,9 +170,9 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
       const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        store_el<false>(kr, ko + (16 * t + r) * keep.dvp * 4, dR[t][r]);
+        if constexpr (!SUM) store_el<false>(kr, ko + (16 * t + r) * keep.dvp * 4, dR[t][r]);
         dR[t][r] *= bb[r];
-        store_el<BF16>(vr, yo + (16 * t + r) * ldy, dR[t][r]);
+        if constexpr (!SUM) store_el<BF16>(vr, yo + (16 * t + r) * ldy, dR[t][r]);
         dR[t][r] *= -ff[r];
         dO[t][r] *= a.scale * ff[r];
       }
@@ -177,14 +189,15 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     }
   }
 
-  if (a.ds0 != nullptr && live) {
+  float* end = SUM ? segs.back + segs.at_back(bh, seg) : seg == 0 && a.ds0 != nullptr ? a.ds0 + static_cast<int64_t>(bh) * a.Dk * a.Dv : nullptr;
+  if (end != nullptr && wave_live) {
+    const int ld = (SUM ? segs.dvp : a.Dv) * 4;
+    const Buf p = rows_buf(end, SUM ? segs.dkp : a.Dk, ld, ld);
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * t + 4 * g + r;
-        if (row < a.Dk) a.ds0[(static_cast<int64_t>(bh) * a.Dk + row) * a.Dv + col] = D[t][r];
-      }
+      for (int r = 0; r < 4; ++r)
+        store_el<false>(p, SUM || live ? (16 * t + 4 * g + r) * ld + col * 4 : kNowhere, D[t][r]);
   }
 }
 
@@ -585,12 +598,12 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
 }
 
 // finds the workspace's parts; bytes of all of them
-int64_t keep_of(DeltaArgs& a, DeltaKeep& k) {
+int64_t keep_of(DeltaArgs& a, DeltaSegs& segs, DeltaKeep& k) {
   const int C = a.bf16_io ? 64 : 32;
   const int64_t chunks = static_cast<int64_t>(a.B) * a.Hv * ((a.L + C - 1) / C);
   k.dkp = (a.Dk + 15) & ~15;
   k.dvp = (a.Dv + 15) & ~15;
-  const int64_t head = delta_work(a, true);
+  const int64_t head = (delta_work(a, segs, true) + 15) & ~int64_t{15};
   k.p = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + head);
   return head + chunks * k.size(C) * 4;
 }
@@ -600,11 +613,13 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   constexpr int NW = 4, C = chunk_of<BF16>();
   using Z = Back<BF16, KP>;
   using G = Grad<BF16, KP>;
-  auto* scan = k_delta_back_scan<BF16, KP, NW>;
+  auto* scan = k_delta_back_scan<BF16, KP, NW, false>;
+  auto* sum = k_delta_back_scan<BF16, KP, NW, true>;
   auto* grad_vec = k_delta_grad<BF16, KP, true>;
   auto* grad_one = k_delta_grad<BF16, KP, false>;
-  static const hipError_t attr[3] = {
+  static const hipError_t attr[4] = {
       hipFuncSetAttribute(reinterpret_cast<const void*>(scan), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds),
+      hipFuncSetAttribute(reinterpret_cast<const void*>(sum), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds),
       hipFuncSetAttribute(reinterpret_cast<const void*>(grad_vec), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds),
       hipFuncSetAttribute(reinterpret_cast<const void*>(grad_one), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds)};
   for (hipError_t e : attr)
@@ -612,15 +627,23 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   const int chunks = (a.L + C - 1) / C;
   const int groups = (a.Dv + 16 * NW - 1) / (16 * NW);
   DeltaKeep keep{};
-  keep_of(a, keep);
+  DeltaSegs segs{};
+  keep_of(a, segs, keep);
   if (a.L > 0) {
     hipError_t e = launch_delta_prep(a, true, stream);
-    if (e == hipSuccess) e = launch_delta_scan(a, &keep, stream);
+    if (e == hipSuccess) e = launch_delta_scan(a, segs, &keep, stream);
     if (e != hipSuccess) return e;
   }
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups;
-  scan<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, keep);
-  hipError_t e = hipGetLastError();
+  hipError_t e = hipSuccess;
+  if (segs.count > 1) {
+    sum<<<dim3(static_cast<unsigned>(blocks * (segs.count - 1))), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
+    e = hipGetLastError();
+    if (e == hipSuccess) e = launch_delta_join_back(a, segs, stream);
+    if (e != hipSuccess) return e;
+  }
+  scan<<<dim3(static_cast<unsigned>(blocks * segs.count)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
+  e = hipGetLastError();
   if (e != hipSuccess || a.L == 0) return e;
   // dy is contiguous and 16-byte aligned
   auto* grad = a.Dv % (BF16 ? 8 : 4) == 0 ? grad_vec : grad_one;
@@ -632,8 +655,9 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
 
 int64_t delta_workspace(const DeltaArgs& args, bool backward) {
   DeltaArgs a = args;
+  DeltaSegs segs{};
   DeltaKeep k{};
-  return backward ? keep_of(a, k) : delta_work(a, false);
+  return backward ? keep_of(a, segs, k) : delta_work(a, segs, false);
 }
 
 hipError_t launch_delta_backward(const DeltaArgs& a, hipStream_t stream) {

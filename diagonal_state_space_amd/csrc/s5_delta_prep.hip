@@ -304,21 +304,55 @@ hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stre
 
 namespace {
 
+// Segments of a call: none where the chain's workgroups (64 columns of a head
+// each) fill half of the compute units or the sequence is short; otherwise as
+// many as the estimate below favours. Microseconds of one chunk, measured with
+// one workgroup on a compute unit at 128 x 128 bf16 (see the scan kernel): a pass
+// for the states 3.1, with outputs 3.9, a segment's join 1.5.
+int segments_of(int64_t heads, int groups, int sum_groups, int chunks) {
+  constexpr double kSum = 3.1, kOut = 3.9, kJoin = 1.5, kUnits = 256.0;
+  if (heads * groups >= 128 || chunks < 16) return 1;
+  auto rounds = [&](double wgs) { return wgs <= kUnits ? 1.0 : wgs / kUnits; };
+  double best = chunks * kOut;
+  int count = 1;
+  for (int n = 3; n <= 32 && n * 4 <= chunks; ++n) {
+    const int each = (chunks + n - 1) / n;
+    if ((chunks + each - 1) / each != n) continue;
+    const double t = each * kSum * rounds(static_cast<double>(heads) * sum_groups * (n - 1)) +
+                     each * kOut * rounds(static_cast<double>(heads) * groups * n) + n * kJoin + 8.0;
+    if (t < 0.9 * best) {
+      best = t;
+      count = n;
+    }
+  }
+  return count;
+}
+
 template <bool BF16, int KP>
-int64_t work(DeltaArgs& a, bool backward) {
+int64_t work(DeltaArgs& a, DeltaSegs& segs, bool backward) {
   using Z = Shape<BF16, KP>;
-  const int64_t chunks = (a.L + Z::C - 1) / Z::C;
-  const int64_t frags = a.B * chunks * a.Hk * Z::frags(backward);
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
+  const int chunks = (a.L + Z::C - 1) / Z::C;
+  const int64_t frags = static_cast<int64_t>(a.B) * a.Hk * chunks * Z::frags(backward);
+  const int64_t recs = heads * chunks * Record<Z::C>::bytes(backward, Z::NO);
   a.frags = static_cast<unsigned char*>(a.ws);
   a.recs = a.frags + frags;
-  return frags + a.B * chunks * a.Hv * Record<Z::C>::bytes(backward, Z::NO);
+  segs.dkp = (a.Dk + 15) & ~15;
+  segs.dvp = (a.Dv + 15) & ~15;
+  segs.count = segments_of(heads, (segs.dvp + 63) / 64, (segs.dvp + segs.dkp + 63) / 64, chunks);
+  segs.chunks = segs.count > 1 ? (chunks + segs.count - 1) / segs.count : chunks;
+  segs.p = reinterpret_cast<float*>(a.recs + recs);
+  const int64_t states = segs.count > 1 ? segs.at(heads, 0) : 0;
+  segs.back = segs.p + states;
+  const int64_t backs = backward && segs.count > 1 ? segs.at_back(heads, 0) : 0;
+  return frags + recs + (states + backs) * 4;
 }
 
 }  // namespace
 
-int64_t delta_work(DeltaArgs& a, bool backward) {
-  if (a.bf16_io) return a.Dk > 64 ? work<true, 128>(a, backward) : work<true, 64>(a, backward);
-  return a.Dk > 64 ? work<false, 128>(a, backward) : work<false, 64>(a, backward);
+int64_t delta_work(DeltaArgs& a, DeltaSegs& segs, bool backward) {
+  if (a.bf16_io) return a.Dk > 64 ? work<true, 128>(a, segs, backward) : work<true, 64>(a, segs, backward);
+  return a.Dk > 64 ? work<false, 128>(a, segs, backward) : work<false, 64>(a, segs, backward);
 }
 
 }  // namespace s5

@@ -30,69 +30,88 @@ constexpr float kNaN = __builtin_nanf("");
 // One more wave copies the chunks. LDS of a chunk: fragments of k (by rows, by columns) and q, T, P and the
 // decays (KEEP: without q and P); two of them where they fit, the next chunk
 // on its way while one is worked on.
-template <bool BF16, int KP, bool KEEP>
+// What a pass of the chunks is for: y and the last state; the states at the
+// chunks' starts and U for the backward pass; a segment's state from zero and
+// its transition (run on the columns of the identity without values), in the
+// workspace layout of the forward or the backward call.
+enum Pass { kOut, kKeep, kSum, kSumBack };
+
+template <bool BF16, int KP, Pass PASS>
 struct Scan : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;
-  static constexpr int kFrags = (KEEP ? 2 : 3) * Z::kMat;
+  static constexpr bool kBack = PASS == kKeep || PASS == kSumBack, kY = PASS == kOut;
+  static constexpr int kFrags = (kY ? 3 : 2) * Z::kMat;
   static constexpr int kRecT = tri_frags<Z::C>() * 3 * kFrag;
-  static constexpr int kRec = KEEP ? kRecT + kFrag : Record<Z::C>::bytes(false, Z::NO);
+  static constexpr int kRec = kY ? Record<Z::C>::bytes(false, Z::NO) : kRecT + kFrag;
   static constexpr int kBuf = kFrags + kRec;
   static constexpr bool kTwo = 2 * kBuf <= kMaxLds;
   static constexpr int kLds = (kTwo ? 2 : 1) * kBuf;
 };
 
-// KEEP: no outputs; the states at the chunks' starts and U are stored for the
-// backward pass
-template <bool BF16, int KP, int NW, bool KEEP>
-__global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int chunks, int groups, DeltaKeep keep) {
-  using Z = Scan<BF16, KP, KEEP>;
+template <bool BF16, int KP, int NW, Pass PASS>
+__global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int chunks, int groups, DeltaSegs segs, DeltaKeep keep) {
+  using Z = Scan<BF16, KP, PASS>;
   constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
+  constexpr bool SUM = PASS == kSum || PASS == kSumBack, KEEP = PASS == kKeep, Y = PASS == kOut;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // workgroups go round the eight dies one by one: the column groups of a head
   // follow each other on one die, whose L2 then holds what they share
   const int die = blockIdx.x & 7, turn = blockIdx.x >> 3;
-  const int bh = (turn / groups) * 8 + die, cg = turn % groups;
+  const int count = SUM ? segs.count - 1 : segs.count;
+  const int cg = turn % groups, seg = (turn / groups) % count, bh = turn / (groups * count) * 8 + die;
   if (bh >= a.B * a.Hv) return;
   const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / (a.Hv / a.Hk);
   const int col = (cg * NW + w) * 16 + m;
-  const bool wave_live = (cg * NW + w) * 16 < a.Dv, live = col < a.Dv;
+  const bool wave_live = (cg * NW + w) * 16 < (SUM ? segs.ld() : a.Dv), live = col < a.Dv;
   const int len = length_of(a, b);
   const int nc = (len + C - 1) / C;
+  const int n0 = seg * segs.chunks, n1 = min(nc, n0 + segs.chunks);
+  if (seg > 0 && n0 >= nc) return;
+  if (SUM && n0 + segs.chunks >= nc) return;    // no segment follows
 
   if (w == NW) {   // the copying wave
     auto copy = [&](int n) {
       unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
-      const unsigned char* rec = a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(KEEP, NO);
-      lds_copy<1>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(KEEP), Z::kFrags, 0);
-      if constexpr (KEEP) {
-        lds_copy<1>(dst + Z::kFrags, rec + Record<C>::T, Z::kRecT, 0);
-        lds_copy<1>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(true, 3), kFrag, 0);
-      } else {
+      const unsigned char* rec = a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(Z::kBack, NO);
+      lds_copy<1>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack), Z::kFrags, 0);
+      if constexpr (Y) {
         lds_copy<1>(dst + Z::kFrags, rec, Z::kRec, 0);
+      } else {
+        lds_copy<1>(dst + Z::kFrags, rec + Record<C>::T, Z::kRecT, 0);
+        lds_copy<1>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(Z::kBack, NO), kFrag, 0);
       }
     };
-    if (Z::kTwo && nc > 0) copy(0);
-    for (int n = 0; n < nc; ++n) {
+    if (Z::kTwo && n0 < n1) copy(n0);
+    for (int n = n0; n < n1; ++n) {
       if constexpr (!Z::kTwo) {
         barrier_copied();
         copy(n);
       }
       barrier_copied();
-      if (Z::kTwo && n + 1 < nc) copy(n + 1);
+      if (Z::kTwo && n + 1 < n1) copy(n + 1);
     }
     return;
   }
 
   f32x4 S[KT];
+  {
+    // the start: the call's, the end of the segment before, or (a segment's
+    // sums) zero and the identity
+    const bool first = seg == 0;
+    const int ld = (first ? a.Dv : segs.ld()) * 4;
+    const Buf p = first ? rows_buf(a.s0 + static_cast<int64_t>(bh) * a.Dk * a.Dv, a.s0 != nullptr ? a.Dk : 0, ld, ld)
+                        : rows_buf(segs.p + segs.at(bh, seg - 1), segs.dkp, ld, ld);
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * t + 4 * g + r;
-      S[t][r] = a.s0 != nullptr && live && row < a.Dk ? a.s0[(static_cast<int64_t>(bh) * a.Dk + row) * a.Dv + col] : 0.0f;
-    }
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * t + 4 * g + r;
+        if constexpr (SUM) S[t][r] = row + segs.dvp == col ? 1.0f : 0.0f;
+        else S[t][r] = __uint_as_float(load_raw<false>(p, live ? row * ld + col * 4 : kNowhere));
+      }
+  }
 
   uint32_t vb[MT][4];
   const int ldv = static_cast<int>(a.ldv) * es, ldy = a.Hv * a.Dv * es;
@@ -108,8 +127,8 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
       for (int r = 0; r < 4; ++r) vb[t][r] = load_raw<BF16>(vr, vo + (16 * t + r) * ldv);
   };
 
-  if (nc > 0) fetch(0);
-  for (int n = 0; n < nc; ++n) {
+  if (n0 < n1) fetch(n0);
+  for (int n = n0; n < n1; ++n) {
     if constexpr (!Z::kTwo) barrier_read();   // the previous chunk is read
     barrier_read();                           // the chunk is there, the previous one read
     if (!wave_live) continue;
@@ -118,7 +137,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) V[t][r] = value<BF16>(vb[t][r]);
-    if (n + 1 < nc) fetch(n + 1);
+    if (n + 1 < n1) fetch(n + 1);
 
     const unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
     const unsigned char *s_kt = s_k + Z::kMat, *s_q = s_k + 2 * Z::kMat, *rec = s_k + Z::kFrags;
@@ -139,7 +158,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
 #pragma unroll
       for (int t = 0; t < MT; ++t) kf[t] = read_rows<NI, KS>(s_k, t, ks);
       mma(X, kf, to_frag<3>(S[2 * ks], S[2 * ks + 1]));
-      if constexpr (!KEEP) {
+      if constexpr (Y) {
         Frag<NI> qf[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) qf[t] = read_rows<NI, KS>(s_q, t, ks);
@@ -188,7 +207,8 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           store_el<false>(p, ko + (16 * t + r) * keep.dvp * 4, 16 * t + 4 * g + r < first ? U[t][r] : kNaN);
-    } else {
+    }
+    if constexpr (Y) {
       const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -225,53 +245,163 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     }
   }
 
-  if (!KEEP && a.s_last != nullptr && live) {
+  if constexpr (SUM) {
+    if (!wave_live) return;
+    const Buf p = rows_buf(segs.p + segs.at(bh, seg), segs.dkp, segs.ld() * 4, segs.ld() * 4);
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
+      for (int r = 0; r < 4; ++r) store_el<false>(p, ((16 * t + 4 * g + r) * segs.ld() + col) * 4, S[t][r]);
+  } else if (Y && a.s_last != nullptr && n0 + segs.chunks >= nc) {
+    const Buf p = rows_buf(a.s_last + static_cast<int64_t>(bh) * a.Dk * a.Dv, a.Dk, a.Dv * 4, a.Dv * 4);
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) store_el<false>(p, live ? ((16 * t + 4 * g + r) * a.Dv + col) * 4 : kNowhere, S[t][r]);
+  }
+}
+
+// Joins the segments: with the states B and transitions M of their sums, the
+// state at the end of segment s is M_s S + B_s (forward, written over B_s), the
+// gradient at its start M_s^T D + B_s (backward). A workgroup has 16 columns of
+// a head, a wave the row tiles w, w + 4; the next segment's M and B are on
+// their way while one is multiplied (float32 matrix instructions).
+template <int KT, bool BACK>
+__global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, DeltaSegs segs, int C) {
+  constexpr int LD = 17, DT = KT / 4;
+  __shared__ float s_x[16 * KT * LD];
+  const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = segs.dvp / 16, bh = blockIdx.x / tiles, col = (blockIdx.x % tiles) * 16 + m;
+  const int nc = (length_of(a, bh / a.Hv) + C - 1) / C;
+  const int last = nc > 0 ? (nc - 1) / segs.chunks : 0;   // the last segment there is
+  const int ld = segs.ld() * 4, ldb = BACK ? segs.dvp * 4 : ld;
+  // segments to join: forward 0 .. last - 1, backward last - 1 .. 1
+  const int from = BACK ? last - 1 : 0, to = BACK ? 0 : last, step = BACK ? -1 : 1;
+  if (BACK ? from <= to : from >= to) return;
+
+  float4 A[DT][KT];
+  float B[DT][4];
+  auto fetch = [&](int s) {
+    const Buf mat = rows_buf(segs.p + segs.at(bh, s), segs.dkp, ld, ld);
+    const Buf vec = BACK ? rows_buf(segs.back + segs.at_back(bh, s), segs.dkp, ldb, ldb) : mat;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const int t = w + 4 * d;
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const bool in = 16 * t < segs.dkp && 16 * k < segs.dkp;
+        if constexpr (BACK) {
+          const int o = (16 * k + 4 * g) * ld + (segs.dvp + 16 * t + m) * 4;
+          A[d][k] = float4{__uint_as_float(load_raw<false>(mat, in ? o : kNowhere)), __uint_as_float(load_raw<false>(mat, in ? o + ld : kNowhere)),
+                           __uint_as_float(load_raw<false>(mat, in ? o + 2 * ld : kNowhere)), __uint_as_float(load_raw<false>(mat, in ? o + 3 * ld : kNowhere))};
+        } else {
+          const uint4 v = load16(mat, in ? (16 * t + m) * ld + (segs.dvp + 16 * k + 4 * g) * 4 : kNowhere);
+          A[d][k] = float4{__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) B[d][r] = __uint_as_float(load_raw<false>(vec, (16 * t + 4 * g + r) * ldb + col * 4));
+    }
+  };
+
+  fetch(from);
+  {
+    // the first segment's start (backward: the gradient that its sums ended with)
+    const int lds = BACK ? ldb : a.Dv * 4;
+    const Buf p = BACK ? rows_buf(segs.back + segs.at_back(bh, last), segs.dkp, lds, lds)
+                       : rows_buf(a.s0 + static_cast<int64_t>(bh) * a.Dk * a.Dv, a.s0 != nullptr ? a.Dk : 0, lds, lds);
+    for (int i = tid; i < 16 * KT * 16; i += 256) {
+      const int row = i >> 4, c = (blockIdx.x % tiles) * 16 + (i & 15);
+      s_x[row * LD + (i & 15)] = __uint_as_float(load_raw<false>(p, BACK || c < a.Dv ? row * lds + c * 4 : kNowhere));
+    }
+  }
+  for (int s = from; s != to; s += step) {
+    __syncthreads();
+    f32x4 acc[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[d][r] = B[d][r];
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const float* x = s_x + (16 * k + 4 * g) * LD + m;
+        acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[d][k].x, x[0], acc[d], 0, 0, 0);
+        acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[d][k].y, x[LD], acc[d], 0, 0, 0);
+        acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[d][k].z, x[2 * LD], acc[d], 0, 0, 0);
+        acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[d][k].w, x[3 * LD], acc[d], 0, 0, 0);
+      }
+    }
+    if (s + step != to) fetch(s + step);
+    __syncthreads();
+    const Buf out = BACK ? rows_buf(segs.back + segs.at_back(bh, s), segs.dkp, ldb, ldb) : rows_buf(segs.p + segs.at(bh, s), segs.dkp, ld, ld);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * t + 4 * g + r;
-        if (row < a.Dk) a.s_last[(static_cast<int64_t>(bh) * a.Dk + row) * a.Dv + col] = S[t][r];
+        const int row = 16 * (w + 4 * d) + 4 * g + r;
+        s_x[row * LD + m] = acc[d][r];
+        store_el<false>(out, row * ldb + col * 4, acc[d][r]);
       }
   }
 }
 
-template <bool BF16, int KP, bool KEEP>
-hipError_t run(const DeltaArgs& a, const DeltaKeep& keep, hipStream_t stream) {
+template <bool BF16, int KP, Pass PASS>
+hipError_t run(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep, hipStream_t stream) {
   constexpr int NW = 4;
-  using Z = Scan<BF16, KP, KEEP>;
-  auto* kern = k_delta_scan<BF16, KP, NW, KEEP>;
+  using Z = Scan<BF16, KP, PASS>;
+  constexpr bool SUM = PASS == kSum || PASS == kSumBack;
+  auto* kern = k_delta_scan<BF16, KP, NW, PASS>;
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
   if (attr != hipSuccess) return attr;
   const int chunks = (a.L + Z::C - 1) / Z::C;
-  const int groups = (a.Dv + 16 * NW - 1) / (16 * NW);
-  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups;
-  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, keep);
+  const int groups = ((SUM ? segs.ld() : a.Dv) + 16 * NW - 1) / (16 * NW);
+  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups * (SUM ? segs.count - 1 : segs.count);
+  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
+  return hipGetLastError();
+}
+
+template <Pass PASS>
+hipError_t dispatch(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep, hipStream_t stream) {
+  if (a.bf16_io) return a.Dk > 64 ? run<true, 128, PASS>(a, segs, keep, stream) : run<true, 64, PASS>(a, segs, keep, stream);
+  return a.Dk > 64 ? run<false, 128, PASS>(a, segs, keep, stream) : run<false, 64, PASS>(a, segs, keep, stream);
+}
+
+template <bool BACK>
+hipError_t join(const DeltaArgs& a, const DeltaSegs& segs, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (segs.dvp / 16)));
+  const int C = a.bf16_io ? chunk_of<true>() : chunk_of<false>();
+  if (a.Dk > 64) k_delta_join<8, BACK><<<grid, dim3(256), 0, stream>>>(a, segs, C);
+  else k_delta_join<4, BACK><<<grid, dim3(256), 0, stream>>>(a, segs, C);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaKeep* keep, hipStream_t stream) {
-  const bool wide = a.Dk > 64;
-  if (keep != nullptr) {
-    if (a.bf16_io) return wide ? run<true, 128, true>(a, *keep, stream) : run<true, 64, true>(a, *keep, stream);
-    return wide ? run<false, 128, true>(a, *keep, stream) : run<false, 64, true>(a, *keep, stream);
-  }
+hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep* keep, hipStream_t stream) {
   const DeltaKeep none{};
-  if (a.bf16_io) return wide ? run<true, 128, false>(a, none, stream) : run<true, 64, false>(a, none, stream);
-  return wide ? run<false, 128, false>(a, none, stream) : run<false, 64, false>(a, none, stream);
+  if (segs.count > 1) {
+    hipError_t e = keep != nullptr ? dispatch<kSumBack>(a, segs, none, stream) : dispatch<kSum>(a, segs, none, stream);
+    if (e == hipSuccess) e = join<false>(a, segs, stream);
+    if (e != hipSuccess) return e;
+  }
+  return keep != nullptr ? dispatch<kKeep>(a, segs, *keep, stream) : dispatch<kOut>(a, segs, none, stream);
+}
+
+hipError_t launch_delta_join_back(const DeltaArgs& a, const DeltaSegs& segs, hipStream_t stream) {
+  return join<true>(a, segs, stream);
 }
 
 hipError_t launch_delta(const DeltaArgs& args, hipStream_t stream) {
   DeltaArgs a = args;
-  delta_work(a, false);
+  DeltaSegs segs{};
+  delta_work(a, segs, false);
   if (a.L > 0) {
     const hipError_t e = launch_delta_prep(a, false, stream);
     if (e != hipSuccess) return e;
   }
-  return launch_delta_scan(a, nullptr, stream);
+  return launch_delta_scan(a, segs, nullptr, stream);
 }
 
 }  // namespace s5

@@ -36,6 +36,10 @@ SHAPES = [
     (2, 200, 2, 2, 48, 96),
     (1, 321, 2, 4, 128, 144),
     (1, 100, 1, 1, 8, 512),
+    # long sequences of few heads run in segments side by side
+    (1, 1537, 1, 2, 64, 48),
+    (2, 2100, 1, 1, 100, 33),
+    (1, 4099, 1, 1, 128, 128),
 ]
 
 
@@ -115,6 +119,32 @@ def test_equal_keys(io):
     y, s = _run(x, io)
     check("y", y, yr, y_bound(190, io), io)
     check("state", s, sr, delta_bound(190))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_segments_and_lengths(io):
+    """Sequences that end in the first, a middle and the last segment, at a
+    segment's first and last steps, and none; then a value that is not finite in
+    a middle segment: what it does not reach keeps its bits."""
+    L = 2500
+    lengths = np.array([0, 1, 700, 1280, 1281, 1279, 2500, 2499], dtype=np.int32)
+    x = delta_inputs(8, L, 1, 1, 32, 24, io, seed=5, decay=(1e-4, 1e-2))
+    ld = torch.from_numpy(lengths).cuda()
+    y0, s0 = _run(x, io, lengths=ld)
+    yr, sr = orc.gated_delta(**x, lengths=lengths)
+    for b, t in enumerate(lengths):
+        check(f"y{b}", y0[b, :t], yr[b, :t], y_bound(L, io), io)
+        assert not y0[b, t:].any()
+    check("state", s0, sr, delta_bound(L))
+    x["v"][6, 1400, 0, 7] = np.inf
+    x["k"][7, 1500, 0, 3] = np.nan
+    y, s = _run(x, io, lengths=ld)
+    assert torch.equal(y[:6], y0[:6]) and torch.equal(s[:6], s0[:6])
+    assert torch.equal(y[6, :1400], y0[6, :1400]) and torch.equal(y[7, :1500], y0[7, :1500])
+    keep = [c for c in range(24) if c != 7]
+    assert torch.equal(y[6][..., keep], y0[6][..., keep]) and torch.equal(s[6][..., keep], s0[6][..., keep])
+    assert not torch.isfinite(y[6, 1400:, 0, 7]).any() and not torch.isfinite(s[6, :, :, 7]).any()
+    assert not torch.isfinite(y[7, 1500:2499]).any() and not torch.isfinite(s[7]).any()
 
 
 def test_large_values_stay_relative():

@@ -51,6 +51,10 @@ SHAPES = [
     (2, 200, 4, 4, 48, 96),
     (1, 321, 2, 4, 128, 144),
     (1, 70, 1, 1, 8, 512),
+    # long sequences of few heads run in segments side by side
+    (1, 1537, 1, 2, 64, 48),
+    (2, 2100, 1, 1, 100, 33),
+    (1, 4099, 1, 1, 128, 128),
 ]
 
 
@@ -85,6 +89,18 @@ def test_lengths_leave_the_rows_behind(io):
             assert torch.equal(a[b, :n], f[b, :n])
     _check(fresh, ref, L, io)
     np.testing.assert_array_equal(given[5][0].cpu().numpy(), x["ds_last"][0])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_segments_and_lengths(io):
+    L = 2500
+    lengths = np.array([0, 1, 700, 1280, 1281, 1279, 2500, 2499], dtype=np.int32)
+    x = delta_inputs(8, L, 1, 1, 32, 24, io, seed=5, decay=(1e-4, 1e-2), grads=True)
+    got = _backward(x, io, lengths=torch.from_numpy(lengths).cuda())
+    _check(got, orc.gated_delta_backward(**x, lengths=lengths), L, io)
+    for b, n in enumerate(lengths):
+        for a in got[:5]:
+            assert not a[b, n:].any()
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
