@@ -127,39 +127,64 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     const unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
     const unsigned char *s_kt = s_k + Z::kMat, *s_qt = s_k + 2 * Z::kMat;
     const float* dec = reinterpret_cast<const float*>(s_k + 3 * Z::kMat);
-    f32x4 dU[MT], P[MT], dR[MT];
+    f32x4 dU[MT], dR[MT];
+    Frag<NI> kx[2][MT];
+    Frag<3> tf[2][MT];
     if (wave_live) {
       if constexpr (!SUM) {
-      const Buf kd = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_d(), keep.dkp, keep.dvp * 4, keep.dvp * 4);
+        const Buf kd = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_d(), keep.dkp, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) store_el<false>(kd, ko + (16 * t + r) * keep.dvp * 4, D[t][r]);
+          for (int r = 0; r < 4; ++r) store_el<false>(kd, ko + (16 * t + r) * keep.dvp * 4, D[t][r]);
       }
+      // dU = to K D' + P^T dO
 #pragma unroll
-      for (int t = 0; t < MT; ++t) dU[t] = P[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int t = 0; t < MT; ++t) dU[t] = dR[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      auto read_x = [&](int ks) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) kx[ks & 1][t] = read_rows<NI, KS>(s_k, t, ks);
+      };
+      read_x(0);
+      stage_end();
+      float4 to[MT];
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        Frag<NI> kf[MT];
+        if (ks + 1 < KS) {
+          read_x(ks + 1);
+        } else {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) kf[t] = read_rows<NI, KS>(s_k, t, ks);
-        mma(dU, kf, to_frag<3>(D[2 * ks], D[2 * ks + 1]));
+          for (int t = 0; t < MT; ++t) to[t] = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
+          read_tri<true, C>(tf[0], s_pt, 0);
+        }
+        stage_end();
+        mma(dU, kx[ks & 1], to_frag<3>(D[2 * ks], D[2 * ks + 1]));
+        stage_end();
       }
-      tri_mma_t<C, 3, NI>(P, s_pt, dO);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        const float4 to = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
-        const float tt[4] = {to.x, to.y, to.z, to.w};
+        const float tt[4] = {to[t].x, to[t].y, to[t].z, to[t].w};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) dU[t][r] = fmaf(tt[r], dU[t][r], a.scale * P[t][r]);
+        for (int r = 0; r < 4; ++r) dU[t][r] *= tt[r];
       }
+      // P^T and then T^T, from the first products to the last
 #pragma unroll
-      for (int t = 0; t < MT; ++t) dR[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      tri_mma_t<C, 3, 3>(dR, s_tt, dU);
+      for (int i = 0; i < 2 * CS; ++i) {
+        if (i + 1 < 2 * CS) read_tri<true, C>(tf[(i + 1) & 1], i + 1 < CS ? s_pt : s_tt, (i + 1) % CS);
+        stage_end();
+        const int ks = i % CS;
+        if (i < CS) mma_tri<true, C>(dU, tf[i & 1], ks, to_frag<NI>(dO[2 * ks], dO[2 * ks + 1]));
+        else mma_tri<true, C>(dR, tf[i & 1], ks, to_frag<3>(dU[2 * ks], dU[2 * ks + 1]));
+        stage_end();
+      }
     }
     barrier_read();   // T and P are read
     if (!wave_live) continue;
 
+    constexpr int kGroups = 2 * CS * KT / 4;   // k's fragments, then q's, four tiles at a time
+    Frag<NI> cf[2][4];
+    auto read_c = [&](int i) { read_cols4<NI, C>(cf[i & 1], i < kGroups / 2 ? s_kt : s_qt, 4 * (i % (KT / 4)), i % (kGroups / 2) / (KT / 4)); };
+    read_c(0);
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     const Buf kr = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_r(C), C, keep.dvp * 4, keep.dvp * 4);
     const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
@@ -167,25 +192,41 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     for (int t = 0; t < MT; ++t) {
       const float4 f = *reinterpret_cast<const float4*>(dec + 16 * t + 4 * g);
       const float4 be = *reinterpret_cast<const float4*>(dec + 2 * C + 16 * t + 4 * g);
-      const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w};
+      const float4 fs = *reinterpret_cast<const float4*>(dec + 3 * C + 16 * t + 4 * g);
+      const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w}, ss[4] = {fs.x, fs.y, fs.z, fs.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if constexpr (!SUM) store_el<false>(kr, ko + (16 * t + r) * keep.dvp * 4, dR[t][r]);
         dR[t][r] *= bb[r];
-        if constexpr (!SUM) store_el<BF16>(vr, yo + (16 * t + r) * ldy, dR[t][r]);
+      }
+      if constexpr (!SUM) {
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) store_el2<BF16>(vr, yo + (16 * t + r) * ldy, ldy, dR[t][r], dR[t][r + 1]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
         dR[t][r] *= -ff[r];
-        dO[t][r] *= a.scale * ff[r];
+        dO[t][r] *= ss[r];
       }
     }
-    const float whole = dec[3 * C];
+    const float whole = dec[C - 1];
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) D[t][r] *= whole;
+    Frag<3> xf[2 * CS];
 #pragma unroll
     for (int ks = 0; ks < CS; ++ks) {
-      cols_mma<NI, C>(D, s_kt, ks, to_frag<3>(dR[2 * ks], dR[2 * ks + 1]));
-      cols_mma<NI, C>(D, s_qt, ks, to_frag<3>(dO[2 * ks], dO[2 * ks + 1]));
+      xf[ks] = to_frag<3>(dR[2 * ks], dR[2 * ks + 1]);
+      xf[CS + ks] = to_frag<3>(dO[2 * ks], dO[2 * ks + 1]);
+    }
+    stage_end();
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      if (i + 1 < kGroups) read_c(i + 1);
+      stage_end();
+      mma_cols4(D, 4 * (i % (KT / 4)), cf[i & 1], xf[i / (KT / 4)]);
+      stage_end();
     }
   }
 

@@ -2,9 +2,9 @@
 // besides the state, for all chunks at once.
 //
 // With G_i the chunk's inclusive sums of g and M_ij = exp(G_i - G_j) (j <= i):
-//   A_ij = beta_i M_ij k_i.k_j (j < i),  T = (I + A)^-1,  P_ij = M_ij q_i.k_j
+//   A_ij = beta_i M_ij k_i.k_j (j < i),  T = (I + A)^-1,  P_ij = scale M_ij q_i.k_j
 // so that the chunk's writes are U = T beta (V - e^G K S) and its outputs
-// e^G Q S + P U. One workgroup of four waves per chunk and value head.
+// scale e^G Q S + P U. One workgroup of four waves per chunk and value head.
 //
 // Both products run on the matrix cores from staged k and q; P comes out
 // transposed, which is the order of its operand fragments, and is stored from
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
       for (int r = 0; r < 4; ++r) {
         const int p = 16 * pt + 4 * g + r, q = 16 * rt + m;   // product and row
         const int i = BACK ? p : q, j = BACK ? q : p;
-        x[4 * half + r] = j <= i ? decay_exp(s_g[i] - s_g[j]) * acc[r] : 0.0f;
+        x[4 * half + r] = j <= i ? a.scale * decay_exp(s_g[i] - s_g[j]) * acc[r] : 0.0f;
       }
     }
     constexpr int NPP = BACK ? 3 : NO;
@@ -256,13 +256,11 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
   }
   if (tid < C) {
     float* dec = reinterpret_cast<float*>(rec + Record<C>::decays(BACK, NO));
-    dec[tid] = expf(static_cast<float>(s_g[tid]));
+    const float from = expf(static_cast<float>(s_g[tid]));
+    dec[tid] = from;
     dec[C + tid] = expf(static_cast<float>(s_g[C - 1] - s_g[tid]));
-    dec[2 * C + tid] = s_b[tid];
-    if (tid == 0) {
-      dec[3 * C] = expf(static_cast<float>(s_g[C - 1]));
-      reinterpret_cast<int*>(dec)[3 * C + 1] = bad;
-    }
+    dec[2 * C + tid] = tid < bad ? s_b[tid] : __builtin_nanf("");
+    dec[3 * C + tid] = a.scale * from;
   }
 }
 

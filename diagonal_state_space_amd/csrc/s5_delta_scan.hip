@@ -5,7 +5,7 @@
 // head's state (as accumulator tiles) and needs nothing from the others: per
 // chunk, with the fragments of T and P of the first kernel,
 //   X = K S,  O = Q S,  R = beta (V - from X),  U = T R,
-//   y = scale (from O + P U),  S <- whole S + K^T (to U).
+//   y = scale from O + P U,  S <- whole S + K^T (to U).
 // Every result is the next product's operand as it lies in the accumulators
 // (the fragments' product order is that of two tiles), so the chain runs
 // without an exchange or a barrier. What the waves share - k, its transpose,
@@ -132,12 +132,6 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     if constexpr (!Z::kTwo) barrier_read();   // the previous chunk is read
     barrier_read();                           // the chunk is there, the previous one read
     if (!wave_live) continue;
-    float V[MT][4];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) V[t][r] = value<BF16>(vb[t][r]);
-    if (n + 1 < n1) fetch(n + 1);
 
     const unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
     const unsigned char *s_kt = s_k + Z::kMat, *s_q = s_k + 2 * Z::kMat, *rec = s_k + Z::kFrags;
@@ -149,38 +143,60 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
 #pragma unroll
         for (int r = 0; r < 4; ++r) store_el<false>(p, ko + (16 * t + r) * keep.dvp * 4, S[t][r]);
     }
-    f32x4 X[MT], O[MT];
+    // X = K S and O = Q S
+    f32x4 X[MT], O[MT], U[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) X[t] = O[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < MT; ++t) X[t] = O[t] = U[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    Frag<NI> kx[2][MT], qx[2][MT];
+    Frag<3> tf[CS][MT];
+    Frag<NO> pf[CS][MT];
+    auto read_x = [&](int ks) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        kx[ks & 1][t] = read_rows<NI, KS>(s_k, t, ks);
+        if constexpr (Y) qx[ks & 1][t] = read_rows<NI, KS>(s_q, t, ks);
+      }
+    };
+    read_x(0);
+    stage_end();
+    float4 from[MT], beta[MT];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      Frag<NI> kf[MT];
+      if (ks + 1 < KS) {
+        read_x(ks + 1);
+      } else {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) kf[t] = read_rows<NI, KS>(s_k, t, ks);
-      mma(X, kf, to_frag<3>(S[2 * ks], S[2 * ks + 1]));
-      if constexpr (Y) {
-        Frag<NI> qf[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) qf[t] = read_rows<NI, KS>(s_q, t, ks);
-        mma(O, qf, to_frag<NO>(S[2 * ks], S[2 * ks + 1]));
+        for (int t = 0; t < MT; ++t) {
+          from[t] = *reinterpret_cast<const float4*>(dec + 16 * t + 4 * g);
+          beta[t] = *reinterpret_cast<const float4*>(dec + 2 * C + 16 * t + 4 * g);
+        }
       }
+      stage_end();
+      mma(X, kx[ks & 1], to_frag<3>(S[2 * ks], S[2 * ks + 1]));
+      if constexpr (Y) mma(O, qx[ks & 1], to_frag<NO>(S[2 * ks], S[2 * ks + 1]));
+      stage_end();
     }
-    float from[MT][4];
-    float odd = 0.0f;   // NaN if anything is not finite
+    // R over X, U = T R
+    read_tri<false, C>(tf[0], rec + Record<C>::T, 0);
+    stage_end();
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const float4 f = *reinterpret_cast<const float4*>(dec + 16 * t + 4 * g);
-      const float4 be = *reinterpret_cast<const float4*>(dec + 2 * C + 16 * t + 4 * g);
-      const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w};
+      const float ff[4] = {from[t].x, from[t].y, from[t].z, from[t].w}, bb[4] = {beta[t].x, beta[t].y, beta[t].z, beta[t].w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        from[t][r] = ff[r];
-        X[t][r] = bb[r] * (V[t][r] - ff[r] * X[t][r]);
-        odd = fmaf(X[t][r], 0.0f, odd);
-      }
+      for (int r = 0; r < 4; ++r) X[t][r] = bb[r] * (value<BF16>(vb[t][r]) - ff[r] * X[t][r]);
     }
-    int first = reinterpret_cast<const int*>(dec)[3 * C + 1];
-    if (first < C || __any(odd != odd)) {
+    if (n + 1 < n1) fetch(n + 1);
+#pragma unroll
+    for (int ks = 0; ks < CS; ++ks) {
+      if (ks + 1 < CS) read_tri<false, C>(tf[ks + 1], rec + Record<C>::T, ks + 1);
+      else if constexpr (Y) read_tri<false, C>(pf[0], rec + Record<C>::P, 0);
+      stage_end();
+      mma_tri<false, C>(U, tf[ks], ks, to_frag<3>(X[2 * ks], X[2 * ks + 1]));
+      stage_end();
+    }
+    int first = C;   // first row that is not finite, of this lane's column
+    // (the last tile's rows have all of R: a zero of T times NaN is NaN)
+    if (__any(!(fabsf(U[MT - 1][0]) < INFINITY))) {
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -189,16 +205,18 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
       first = min(first, __shfl_xor(first, 16));
       first = min(first, __shfl_xor(first, 32));
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < MT; ++t) {
+        U[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (16 * t + 4 * g + r >= first) X[t][r] = 0.0f;
-    }
-    // U = T R: 32 products at a time, of the row tiles they reach
-    f32x4 U[MT];
+      }
 #pragma unroll
-    for (int t = 0; t < MT; ++t) U[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    tri_mma<C, 3>(U, rec + Record<C>::T, X);
+      for (int ks = 0; ks < CS; ++ks) {
+        read_tri<false, C>(tf[ks], rec + Record<C>::T, ks);
+        mma_tri<false, C>(U, tf[ks], ks, to_frag<3>(X[2 * ks], X[2 * ks + 1]));
+      }
+    }
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     if constexpr (KEEP) {
       const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_u(), C, keep.dvp * 4, keep.dvp * 4);
@@ -208,26 +226,33 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
         for (int r = 0; r < 4; ++r)
           store_el<false>(p, ko + (16 * t + r) * keep.dvp * 4, 16 * t + 4 * g + r < first ? U[t][r] : kNaN);
     }
+    // O <- scale from O + P U, and S <- whole S + K^T (to U): the first is not in
+    // the chain and fills its gaps
+    Frag<NI> cf[2][4];
+    read_cols4<NI, C>(cf[0], s_kt, 0, 0);
+    if constexpr (Y && CS > 1) read_tri<false, C>(pf[1], rec + Record<C>::P, 1);
+    float4 to[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) to[t] = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
+    const float whole = dec[C - 1];
     if constexpr (Y) {
-      const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) O[t][r] *= from[t][r];
-      tri_mma<C, NO>(O, rec + Record<C>::P, U);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * t + 4 * g + r;
-          store_el<BF16>(yr, yo + (16 * t + r) * ldy, i < first ? a.scale * O[t][r] : kNaN);
-        }
+      for (int t = 0; t < MT; ++t) from[t] = *reinterpret_cast<const float4*>(dec + 3 * C + 16 * t + 4 * g);
     }
-    const float whole = dec[3 * C];
+    stage_end();
+    if constexpr (Y) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const float ff[4] = {from[t].x, from[t].y, from[t].z, from[t].w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[t][r] *= ff[r];
+      }
+#pragma unroll
+      for (int ks = 0; ks < CS; ++ks) mma_tri<false, C>(O, pf[ks], ks, to_frag<NO>(U[2 * ks], U[2 * ks + 1]));
+    }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const float4 to = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
-      const float tt[4] = {to.x, to.y, to.z, to.w};
+      const float tt[4] = {to[t].x, to[t].y, to[t].z, to[t].w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) U[t][r] *= tt[r];
     }
@@ -235,8 +260,34 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[t][r] *= whole;
+    Frag<3> uf[CS];
 #pragma unroll
-    for (int ks = 0; ks < CS; ++ks) cols_mma<NI, C>(S, s_kt, ks, to_frag<3>(U[2 * ks], U[2 * ks + 1]));
+    for (int ks = 0; ks < CS; ++ks) uf[ks] = to_frag<3>(U[2 * ks], U[2 * ks + 1]);
+    stage_end();
+    constexpr int kGroups = CS * KT / 4;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      if (i + 1 < kGroups) read_cols4<NI, C>(cf[(i + 1) & 1], s_kt, 4 * ((i + 1) % (KT / 4)), (i + 1) / (KT / 4));
+      stage_end();
+      mma_cols4(S, 4 * (i % (KT / 4)), cf[i & 1], uf[i / (KT / 4)]);
+      if constexpr (Y) {
+        if (i == 0) {
+          if (first < C) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (16 * t + 4 * g + r >= first) O[t][r] = kNaN;
+          }
+          const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; r += 2) store_el2<BF16>(yr, yo + (16 * t + r) * ldy, ldy, O[t][r], O[t][r + 1]);
+        }
+      }
+      stage_end();
+    }
     if (first < C) {
 #pragma unroll
       for (int t = 0; t < KT; ++t)

@@ -42,6 +42,9 @@ struct Frag {
 // fewer than three parts round the last one (an error below 2^-16 with two)
 template <int NP>
 __device__ __forceinline__ Frag<NP> to_frag(const float (&x)[8]) {
+  // a product that x is must not go into the differences below unrounded: the
+  // parts are those of x wherever it is split
+#pragma clang fp contract(off)
   union {
     uint32_t w[4];
     bf16x8 v;
@@ -135,22 +138,25 @@ __device__ __forceinline__ Frag<NP> read_cols(const unsigned char* base, int mt,
   return read_frag<NP>(base, mt * (C / 32) + ks, mt);
 }
 
-// s += a x over 32 tokens for the state's KT tiles, four at a time (enough to
-// hide the matrix instructions' latency, and fewer registers than all)
-template <int NP, int C, int KT>
-__device__ __forceinline__ void cols_mma(f32x4 (&s)[KT], const unsigned char* a, int ks, const Frag<3>& x) {
+// The chains' products run in stages whose fragments are read one stage ahead
+// (left to itself the compiler reads a fragment right before its use, and the
+// wave, alone on its SIMD, waits for the LDS each time). A stage ends here.
+__device__ __forceinline__ void stage_end() { __builtin_amdgcn_sched_barrier(0); }
+
+// four of the state's tiles by the fragments of 32 tokens
+template <int NP, int C>
+__device__ __forceinline__ void read_cols4(Frag<NP> (&f)[4], const unsigned char* a, int t0, int ks) {
 #pragma unroll
-  for (int t0 = 0; t0 < KT; t0 += 4) {
-    Frag<NP> f[4];
+  for (int t = 0; t < 4; ++t) f[t] = read_cols<NP, C>(a, t0 + t, ks);
+}
+template <int NP, int KT>
+__device__ __forceinline__ void mma_cols4(f32x4 (&s)[KT], int t0, const Frag<NP> (&f)[4], const Frag<3>& x) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) f[t] = read_cols<NP, C>(a, t0 + t, ks);
+  for (int i = 0; i < NP; ++i)
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
+    for (int j = 0; i + j < 3; ++j)
 #pragma unroll
-      for (int j = 0; i + j < 3; ++j)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) s[t0 + t] = mfma(f[t].p[i], x.p[j], s[t0 + t]);
-  }
+      for (int t = 0; t < 4; ++t) s[t0 + t] = mfma(f[t].p[i], x.p[j], s[t0 + t]);
 }
 
 // ---- staging of token rows -----------------------------------------------------
@@ -305,6 +311,19 @@ __device__ __forceinline__ float value(uint32_t raw) {
   return __uint_as_float(BF16 ? raw << 16 : raw);
 }
 
+// two rows' elements, `ld` bytes apart (bf16: rounded in one instruction)
+template <bool BF16>
+__device__ __forceinline__ void store_el2(Buf r, int o, int ld, float x, float y) {
+  if constexpr (BF16) {
+    const uint32_t w = round2(x, y);
+    __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(w), r, o, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(w >> 16), r, o + ld, 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(x), r, o, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(y), r, o + ld, 0, 0);
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ void store_el(Buf r, int o, float x) {
   if constexpr (BF16) __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(round2(x, x)), r, o, 0, 0);
@@ -326,47 +345,32 @@ __host__ __device__ constexpr int tri_frag(int it, int ks) { return it < 2 ? it 
 template <int C>
 __host__ __device__ constexpr int tri_frag_t(int jt, int ks) { return C == 32 ? jt : jt < 2 ? 2 * jt + ks : 2 + jt; }
 
-// c += a x for a lower triangular a in fragments of NP parts and x in accumulator
-// tiles (or its transpose, an upper one)
-template <int C, int NP>
-__device__ __forceinline__ void tri_mma(f32x4 (&c)[C / 16], const unsigned char* a, const f32x4 (&x)[C / 16]) {
+// the fragments of a lower triangular matrix for the products 32 ks.. (UP: of
+// its transpose), the row tiles that have them, and c += a x with them
+template <bool UP, int C>
+__device__ __forceinline__ bool tri_has(int t, int ks) { return UP ? t <= 2 * ks + 1 : t >= 2 * ks; }
+template <bool UP, int C, int NP>
+__device__ __forceinline__ void read_tri(Frag<NP> (&f)[C / 16], const unsigned char* a, int ks) {
 #pragma unroll
-  for (int ks = 0; ks < C / 32; ++ks) {
-    constexpr int MT = C / 16;
-    const Frag<NP> b = to_frag<NP>(x[2 * ks], x[2 * ks + 1]);
-    Frag<NP> f[MT];
-#pragma unroll
-    for (int t = 2 * ks; t < MT; ++t) f[t] = read_frag<NP>(a, tri_frag<C>(t, ks), 0);
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-#pragma unroll
-      for (int j = 0; i + j < NP; ++j)
-#pragma unroll
-        for (int t = 2 * ks; t < MT; ++t) c[t] = mfma(f[t].p[i], b.p[j], c[t]);
-  }
+  for (int t = 0; t < C / 16; ++t)
+    if (tri_has<UP, C>(t, ks)) f[t] = read_frag<NP>(a, UP ? tri_frag_t<C>(t, ks) : tri_frag<C>(t, ks), 0);
 }
-template <int C, int NP, int NB>
-__device__ __forceinline__ void tri_mma_t(f32x4 (&c)[C / 16], const unsigned char* a, const f32x4 (&x)[C / 16]) {
+template <bool UP, int C, int NP, int NB>
+__device__ __forceinline__ void mma_tri(f32x4 (&c)[C / 16], const Frag<NP> (&f)[C / 16], int ks, const Frag<NB>& b) {
 #pragma unroll
-  for (int ks = C / 32 - 1; ks >= 0; --ks) {
-    constexpr int MT = C / 16;
-    const Frag<NB> b = to_frag<NB>(x[2 * ks], x[2 * ks + 1]);
-    Frag<NP> f[MT];
+  for (int i = 0; i < NP; ++i)
 #pragma unroll
-    for (int t = 0; t <= 2 * ks + 1; ++t) f[t] = read_frag<NP>(a, tri_frag_t<C>(t, ks), 0);
+    for (int j = 0; j < NB && i + j < NP; ++j)
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
-#pragma unroll
-      for (int j = 0; j < NB && i + j < NP; ++j)
-#pragma unroll
-        for (int t = 0; t <= 2 * ks + 1; ++t) c[t] = mfma(f[t].p[i], b.p[j], c[t]);
-  }
+      for (int t = 0; t < C / 16; ++t)
+        if (tri_has<UP, C>(t, ks)) c[t] = mfma(f[t].p[i], b.p[j], c[t]);
 }
 
-// The record of one head's chunk: the parts of T = (I + A)^-1 and of P = M o QK^T
-// (backward: T, its transpose and that of P), then the decays
-//   from[i] = e^{G_i}, to[i] = e^{G_end - G_i}, beta[i], whole = e^{G_end}, bad
-// (1 KB) with bad the first token whose key, decay or strength is not finite (C if none).
+// The record of one head's chunk: the parts of T = (I + A)^-1 and of P = scale
+// M o QK^T (backward: T, its transpose and that of P), then the decays
+//   from[i] = e^{G_i}, to[i] = e^{G_end - G_i}, beta[i], scale from[i]
+// (1 KB). From the first token on whose key, decay or strength is not finite
+// beta is NaN and T the identity.
 template <int C>
 struct Record {
   static constexpr int T = 0;
