@@ -26,7 +26,7 @@ using namespace delta;
 namespace {
 
 // LDS of a chunk: fragments of k (by rows, by columns) and q (by columns) and
-// the decays, two of them where they fit (one more wave copies them); the transposed T and P, which the
+// the decays, two of them where they fit (more waves copy them); the transposed T and P, which the
 // next chunk's replace as soon as they are read.
 template <bool BF16, int KP>
 struct Back : Shape<BF16, KP> {
@@ -41,7 +41,7 @@ struct Back : Shape<BF16, KP> {
 // SUM: only the gradients at the segments' starts, from zero ends (the last
 // segment's from ds_last)
 template <bool BF16, int KP, int NW, bool SUM>
-__global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, int chunks, int groups, DeltaSegs segs, DeltaKeep keep) {
+__global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs a, int chunks, int groups, DeltaSegs segs, DeltaKeep keep) {
   using Z = Back<BF16, KP>;
   constexpr int C = Z::C, NI = Z::NI, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -60,13 +60,13 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
   if (seg > 0 && n0 >= nc) return;
   const bool last = n0 + segs.chunks >= nc;
 
-  if (w == NW) {   // the copying wave
+  if (w >= NW) {   // the copying waves
     auto record = [&](int n) { return a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true, 3); };
-    auto copy_tri = [&](int n) { lds_copy<1>(smem + Z::oTri, record(n) + Record<C>::P, 2 * Z::kTri, 0); };
+    auto copy_tri = [&](int n) { lds_copy<kCopy>(smem + Z::oTri, record(n) + Record<C>::P, 2 * Z::kTri, w - NW); };
     auto copy = [&](int n) {
       unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
-      lds_copy<1>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(true), 3 * Z::kMat, 0);
-      lds_copy<1>(dst + 3 * Z::kMat, record(n) + Record<C>::decays(true, 3), kFrag, 0);
+      lds_copy<kCopy>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(true), 3 * Z::kMat, w - NW);
+      lds_copy<kCopy>(dst + 3 * Z::kMat, record(n) + Record<C>::decays(true, 3), kFrag, w - NW);
     };
     if (n0 < n1) {
       if (Z::kTwo) copy(n1 - 1);
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
       }
       barrier_copied();
       if (Z::kTwo && n > n0) copy(n - 1);
-      barrier_copied();
+      __builtin_amdgcn_s_barrier();   // T and P are read; the copies need not be there yet
       if (n > n0) copy_tri(n - 1);
     }
     return;
@@ -96,6 +96,8 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         D[t][r] = __uint_as_float(load_raw<false>(p, live ? (16 * t + 4 * g + r) * ld + col * 4 : kNowhere));
+#pragma unroll
+    for (int t = 0; t < KT; ++t) asm volatile("" : "+v"(D[t]));   // waited for here, not in every chunk
   }
 
   uint32_t ob[MT][4];
@@ -106,11 +108,12 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
   const unsigned char* s_pt = s_tt + Z::kTri;
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
+    const int o = here(yo);
     const Buf yr = rows_buf(static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) ob[t][r] = load_raw<BF16>(yr, yo + (16 * t + r) * ldy);
+      for (int r = 0; r < 4; ++r) ob[t][r] = load_raw<BF16>(yr, o + (16 * t + r) * ldy);
   };
 
   if (n0 < n1) fetch(n1 - 1);
@@ -132,11 +135,12 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     Frag<3> tf[2][MT];
     if (wave_live) {
       if constexpr (!SUM) {
+        const int o = here(ko);
         const Buf kd = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_d(), keep.dkp, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) store_el<false>(kd, ko + (16 * t + r) * keep.dvp * 4, D[t][r]);
+          for (int r = 0; r < 4; ++r) store_el<false>(kd, o + (16 * t + r) * keep.dvp * 4, D[t][r]);
       }
       // dU = to K D' + P^T dO
 #pragma unroll
@@ -186,6 +190,7 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
     auto read_c = [&](int i) { read_cols4<NI, C>(cf[i & 1], i < kGroups / 2 ? s_kt : s_qt, 4 * (i % (KT / 4)), i % (kGroups / 2) / (KT / 4)); };
     read_c(0);
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
+    const int o1 = here(ko), o2 = here(yo);
     const Buf kr = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_r(C), C, keep.dvp * 4, keep.dvp * 4);
     const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
@@ -196,12 +201,12 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_back_scan(DeltaArgs a, 
       const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w}, ss[4] = {fs.x, fs.y, fs.z, fs.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        if constexpr (!SUM) store_el<false>(kr, ko + (16 * t + r) * keep.dvp * 4, dR[t][r]);
+        if constexpr (!SUM) store_el<false>(kr, o1 + (16 * t + r) * keep.dvp * 4, dR[t][r]);
         dR[t][r] *= bb[r];
       }
       if constexpr (!SUM) {
 #pragma unroll
-        for (int r = 0; r < 4; r += 2) store_el2<BF16>(vr, yo + (16 * t + r) * ldy, ldy, dR[t][r], dR[t][r + 1]);
+        for (int r = 0; r < 4; r += 2) store_el2<BF16>(vr, o2 + (16 * t + r) * ldy, ldy, dR[t][r], dR[t][r + 1]);
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -294,7 +299,7 @@ __device__ __forceinline__ void store_row8(unsigned char* base, const float (&x)
 
 // VEC: whole 16-byte groups of dy are aligned
 template <bool BF16, int KP, bool VEC>
-__global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, DeltaKeep keep) {
+__global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunks, DeltaKeep keep) {
   using Z = Grad<BF16, KP>;
   constexpr int C = Z::C, MT = Z::MT, CS = Z::CS, NI = Z::NI, NW = Z::NW, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
       }
     };
     Eight es_, ed, et[Z::kItems];
-    const int srow = tid >> 2, sc = tid & 3;    // this thread's row of S and D' and eight of its 32 values
+    const int srow = here(tid) >> 2, sc = tid & 3;    // this thread's row of S and D' and eight of its 32 values
     auto fetch = [&](int v0) {
       es_ = load_kept(0, srow, keep.dkp, v0 + 8 * sc);
       ed = load_kept(keep.at_d(), srow, keep.dkp, v0 + 8 * sc);
@@ -472,6 +477,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
       }
     }
     __syncthreads();   // the last step is read
+    const int gg = here(g), mm = here(m);
 #pragma unroll
     for (int j = 0; j < Z::kJobs; ++j) {
       const int job = w + j * NW, mat = job / Z::kTri, f = job % Z::kTri;
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int p = 16 * (2 * st + (e >> 2)) + 4 * g + (e & 3), q = 16 * rt + m;
+          const int p = 16 * (2 * st + (e >> 2)) + 4 * gg + (e & 3), q = 16 * rt + mm;
           const int i = (mat & 1) ? p : q, jj = (mat & 1) ? q : p;
           const float factor = mat < 2 ? a.scale : mat == 3 ? -s_b[i] : 1.0f;
           const bool in = mat < 2 ? jj <= i : jj < i;
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
     // dR.V: every wave C / NW tokens side by side, kLanes lanes a token
     {
       constexpr int kLanes = 64 * NW / C;
-      const int i = tid / kLanes, lv = 4 * (tid % kLanes), ldv = static_cast<int>(a.ldv) * es;
+      const int id = here(tid), i = id / kLanes, lv = 4 * (id % kLanes), ldv = static_cast<int>(a.ldv) * es;
       const Buf vr = rows_buf(static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es, rows, ldv, a.Dv * es);
       float s = 0.0f;
       for (int v = lv; v < a.Dv; v += 4 * kLanes) {
@@ -506,7 +512,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
       }
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor(s, o);
-      if (tid % kLanes == 0) s_rv[i] = s;
+      if (lv == 0) s_rv[i] = s;
     }
     // k and q of this wave's features, as operands over the tokens; their slots
     // are also the values at the accumulators' places
@@ -522,8 +528,8 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
     float kh = 0.0f;   // sum of to k.(U D'^T)
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const float4 fr = *reinterpret_cast<const float4*>(s_from + 16 * t + 4 * g);
-      const float4 to = *reinterpret_cast<const float4*>(s_to + 16 * t + 4 * g);
+      const float4 fr = *reinterpret_cast<const float4*>(s_from + 16 * t + 4 * gg);
+      const float4 to = *reinterpret_cast<const float4*>(s_to + 16 * t + 4 * gg);
       const float ff[4] = {fr.x, fr.y, fr.z, fr.w}, tt[4] = {to.x, to.y, to.z, to.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float kv = value_of(kf[t >> 1], 4 * (t & 1) + r), qv = value_of(qf[t >> 1], 4 * (t & 1) + r);
-        const int i = 16 * t + 4 * g + r;
+        const int i = 16 * t + 4 * gg + r;
         const float row = s_b[i] * F[t][r];
         const float ga = row_sum(qv * E[t][r] - kv * (H[t][r] + row)), ka = row_sum(-kv * F[t][r]);
         H[t][r] -= row;   // dK of the head
@@ -574,7 +580,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
         }
       }
     // dq and dk of the heads that share a key: in LDS until the last one
-    f32x4* sum = reinterpret_cast<f32x4*>(smem + Z::oAcc) + w * 2 * MT * 64 + l;
+    f32x4* sum = reinterpret_cast<f32x4*>(smem + Z::oAcc) + w * 2 * MT * 64 + here(l);
     if (hh > 0) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
@@ -592,7 +598,7 @@ __global__ void __launch_bounds__(4 * KP) k_delta_grad(DeltaArgs a, int chunks, 
       const int c = 16 * w + m, ldo = a.Hk * a.Dk * es;
       const Buf qo = rows_buf(static_cast<char*>(a.dq) + (tok * a.Hk + hk) * a.Dk * es, rows, ldo, a.Dk * es);
       const Buf ko = rows_buf(static_cast<char*>(a.dk) + (tok * a.Hk + hk) * a.Dk * es, rows, ldo, a.Dk * es);
-      const int oo = c < a.Dk ? 4 * g * ldo + c * es : kNowhere;
+      const int oo = here(c < a.Dk ? 4 * g * ldo + c * es : kNowhere);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -678,12 +684,12 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups;
   hipError_t e = hipSuccess;
   if (segs.count > 1) {
-    sum<<<dim3(static_cast<unsigned>(blocks * (segs.count - 1))), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
+    sum<<<dim3(static_cast<unsigned>(blocks * (segs.count - 1))), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
     e = hipGetLastError();
     if (e == hipSuccess) e = launch_delta_join_back(a, segs, stream);
     if (e != hipSuccess) return e;
   }
-  scan<<<dim3(static_cast<unsigned>(blocks * segs.count)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
+  scan<<<dim3(static_cast<unsigned>(blocks * segs.count)), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
   e = hipGetLastError();
   if (e != hipSuccess || a.L == 0) return e;
   // dy is contiguous and 16-byte aligned

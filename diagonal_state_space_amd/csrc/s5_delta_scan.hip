@@ -27,7 +27,7 @@ namespace {
 
 constexpr float kNaN = __builtin_nanf("");
 
-// One more wave copies the chunks. LDS of a chunk: fragments of k (by rows, by columns) and q, T, P and the
+// More waves copy the chunks. LDS of a chunk: fragments of k (by rows, by columns) and q, T, P and the
 // decays (KEEP: without q and P); two of them where they fit, the next chunk
 // on its way while one is worked on.
 // What a pass of the chunks is for: y and the last state; the states at the
@@ -49,7 +49,7 @@ struct Scan : Shape<BF16, KP> {
 };
 
 template <bool BF16, int KP, int NW, Pass PASS>
-__global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int chunks, int groups, DeltaSegs segs, DeltaKeep keep) {
+__global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, int chunks, int groups, DeltaSegs segs, DeltaKeep keep) {
   using Z = Scan<BF16, KP, PASS>;
   constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
   constexpr bool SUM = PASS == kSum || PASS == kSumBack, KEEP = PASS == kKeep, Y = PASS == kOut;
@@ -71,16 +71,16 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
   if (seg > 0 && n0 >= nc) return;
   if (SUM && n0 + segs.chunks >= nc) return;    // no segment follows
 
-  if (w == NW) {   // the copying wave
+  if (w >= NW) {   // the copying waves
     auto copy = [&](int n) {
       unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
       const unsigned char* rec = a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(Z::kBack, NO);
-      lds_copy<1>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack), Z::kFrags, 0);
+      lds_copy<kCopy>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack), Z::kFrags, w - NW);
       if constexpr (Y) {
-        lds_copy<1>(dst + Z::kFrags, rec, Z::kRec, 0);
+        lds_copy<kCopy>(dst + Z::kFrags, rec, Z::kRec, w - NW);
       } else {
-        lds_copy<1>(dst + Z::kFrags, rec + Record<C>::T, Z::kRecT, 0);
-        lds_copy<1>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(Z::kBack, NO), kFrag, 0);
+        lds_copy<kCopy>(dst + Z::kFrags, rec + Record<C>::T, Z::kRecT, w - NW);
+        lds_copy<kCopy>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(Z::kBack, NO), kFrag, w - NW);
       }
     };
     if (Z::kTwo && n0 < n1) copy(n0);
@@ -111,6 +111,8 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
         if constexpr (SUM) S[t][r] = row + segs.dvp == col ? 1.0f : 0.0f;
         else S[t][r] = __uint_as_float(load_raw<false>(p, live ? row * ld + col * 4 : kNowhere));
       }
+#pragma unroll
+    for (int t = 0; t < KT; ++t) asm volatile("" : "+v"(S[t]));   // waited for here, not in every chunk
   }
 
   uint32_t vb[MT][4];
@@ -119,12 +121,13 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
   const int ko = (4 * g * keep.dvp + col) * 4;   // rows behind the kept ones are outside their buffer
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
+    const int o = here(vo);
     const Buf vr = rows_buf(static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es, min(len - n * C, C),
                             ldv, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) vb[t][r] = load_raw<BF16>(vr, vo + (16 * t + r) * ldv);
+      for (int r = 0; r < 4; ++r) vb[t][r] = load_raw<BF16>(vr, o + (16 * t + r) * ldv);
   };
 
   if (n0 < n1) fetch(n0);
@@ -137,46 +140,61 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     const unsigned char *s_kt = s_k + Z::kMat, *s_q = s_k + 2 * Z::kMat, *rec = s_k + Z::kFrags;
     const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - kFrag);
     if constexpr (KEEP) {
+      const int o = here(ko);
       const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C), keep.dkp, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) store_el<false>(p, ko + (16 * t + r) * keep.dvp * 4, S[t][r]);
+        for (int r = 0; r < 4; ++r) store_el<false>(p, o + (16 * t + r) * keep.dvp * 4, S[t][r]);
     }
-    // X = K S and O = Q S
+    // X = K S, R over it and U = T R are the chain; what is not (O = Q S) and the
+    // splitting of the next operand go between, into the gaps of its stages
     f32x4 X[MT], O[MT], U[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) X[t] = O[t] = U[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Frag<NI> kx[2][MT], qx[2][MT];
-    Frag<3> tf[CS][MT];
-    Frag<NO> pf[CS][MT];
-    auto read_x = [&](int ks) {
+    Frag<NI> kx[2][MT], qx[KS / 2][MT];
+    Frag<3> tf[CS][MT], sf[2];
+    Frag<NO> so[KS / 2];
+    auto read_k = [&](int ks) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        kx[ks & 1][t] = read_rows<NI, KS>(s_k, t, ks);
-        if constexpr (Y) qx[ks & 1][t] = read_rows<NI, KS>(s_q, t, ks);
+      for (int t = 0; t < MT; ++t) kx[ks & 1][t] = read_rows<NI, KS>(s_k, t, ks);
+    };
+    auto read_q = [&](int half) {
+      if constexpr (Y) {
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i)
+#pragma unroll
+          for (int t = 0; t < MT; ++t) qx[i][t] = read_rows<NI, KS>(s_q, t, half * (KS / 2) + i);
       }
     };
-    read_x(0);
+    auto mma_q = [&](int half) {
+      if constexpr (Y) {
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) mma(O, qx[i], so[i]);
+      }
+    };
+    read_k(0);
+    sf[0] = to_frag<3>(S[0], S[1]);
     stage_end();
     float4 from[MT], beta[MT];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       if (ks + 1 < KS) {
-        read_x(ks + 1);
+        read_k(ks + 1);
       } else {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           from[t] = *reinterpret_cast<const float4*>(dec + 16 * t + 4 * g);
           beta[t] = *reinterpret_cast<const float4*>(dec + 2 * C + 16 * t + 4 * g);
         }
+        read_q(0);
       }
       stage_end();
-      mma(X, kx[ks & 1], to_frag<3>(S[2 * ks], S[2 * ks + 1]));
-      if constexpr (Y) mma(O, qx[ks & 1], to_frag<NO>(S[2 * ks], S[2 * ks + 1]));
+      mma(X, kx[ks & 1], sf[ks & 1]);
+      if (ks + 1 < KS) sf[(ks + 1) & 1] = to_frag<3>(S[2 * ks + 2], S[2 * ks + 3]);
+      if (Y && ks < KS / 2) so[ks] = to_frag<NO>(S[2 * ks], S[2 * ks + 1]);
       stage_end();
     }
-    // R over X, U = T R
     read_tri<false, C>(tf[0], rec + Record<C>::T, 0);
     stage_end();
 #pragma unroll
@@ -185,15 +203,37 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
 #pragma unroll
       for (int r = 0; r < 4; ++r) X[t][r] = bb[r] * (value<BF16>(vb[t][r]) - ff[r] * X[t][r]);
     }
-    if (n + 1 < n1) fetch(n + 1);
+    mma_q(0);
+    Frag<3> xf[CS];
+    xf[0] = to_frag<3>(X[0], X[1]);
+    stage_end();
+    const float whole = dec[C - 1];
+    float4 to[MT];
 #pragma unroll
     for (int ks = 0; ks < CS; ++ks) {
-      if (ks + 1 < CS) read_tri<false, C>(tf[ks + 1], rec + Record<C>::T, ks + 1);
-      else if constexpr (Y) read_tri<false, C>(pf[0], rec + Record<C>::P, 0);
+      if (ks + 1 < CS) {
+        read_tri<false, C>(tf[ks + 1], rec + Record<C>::T, ks + 1);
+      } else {
+        read_q(1);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) to[t] = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
+      }
       stage_end();
-      mma_tri<false, C>(U, tf[ks], ks, to_frag<3>(X[2 * ks], X[2 * ks + 1]));
+      mma_tri<false, C>(U, tf[ks], ks, xf[ks]);
+      if (ks + 1 < CS) xf[ks + 1] = to_frag<3>(X[2 * ks + 2], X[2 * ks + 3]);
+      if (Y && ks == 0) {
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) so[i] = to_frag<NO>(S[KS + 2 * i], S[KS + 2 * i + 1]);
+      }
+      if (ks == CS - 1) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[t][r] *= whole;
+      }
       stage_end();
     }
+    if (n + 1 < n1) fetch(n + 1);
     int first = C;   // first row that is not finite, of this lane's column
     // (the last tile's rows have all of R: a zero of T times NaN is NaN)
     if (__any(!(fabsf(U[MT - 1][0]) < INFINITY))) {
@@ -219,59 +259,60 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
     }
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     if constexpr (KEEP) {
+      const int o = here(ko);
       const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_u(), C, keep.dvp * 4, keep.dvp * 4);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          store_el<false>(p, ko + (16 * t + r) * keep.dvp * 4, 16 * t + 4 * g + r < first ? U[t][r] : kNaN);
+          store_el<false>(p, o + (16 * t + r) * keep.dvp * 4, 16 * t + 4 * g + r < first ? U[t][r] : kNaN);
     }
-    // O <- scale from O + P U, and S <- whole S + K^T (to U): the first is not in
-    // the chain and fills its gaps
+    // S <- whole S + K^T (to U), and O <- scale from O + P U beside it
     Frag<NI> cf[2][4];
     read_cols4<NI, C>(cf[0], s_kt, 0, 0);
-    if constexpr (Y && CS > 1) read_tri<false, C>(pf[1], rec + Record<C>::P, 1);
-    float4 to[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) to[t] = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
-    const float whole = dec[C - 1];
-    if constexpr (Y) {
-#pragma unroll
-      for (int t = 0; t < MT; ++t) from[t] = *reinterpret_cast<const float4*>(dec + 3 * C + 16 * t + 4 * g);
-    }
     stage_end();
-    if constexpr (Y) {
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const float ff[4] = {from[t].x, from[t].y, from[t].z, from[t].w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) O[t][r] *= ff[r];
-      }
-#pragma unroll
-      for (int ks = 0; ks < CS; ++ks) mma_tri<false, C>(O, pf[ks], ks, to_frag<NO>(U[2 * ks], U[2 * ks + 1]));
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const float tt[4] = {to[t].x, to[t].y, to[t].z, to[t].w};
-#pragma unroll
-      for (int r = 0; r < 4; ++r) U[t][r] *= tt[r];
-    }
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[t][r] *= whole;
+    mma_q(1);
     Frag<3> uf[CS];
 #pragma unroll
-    for (int ks = 0; ks < CS; ++ks) uf[ks] = to_frag<3>(U[2 * ks], U[2 * ks + 1]);
+    for (int ks = 0; ks < CS; ++ks) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 f = to[2 * ks + (e >> 2)];
+        x[e] = U[2 * ks + (e >> 2)][e & 3] * ((e & 3) == 0 ? f.x : (e & 3) == 1 ? f.y : (e & 3) == 2 ? f.z : f.w);
+      }
+      uf[ks] = to_frag<3>(x);
+    }
     stage_end();
     constexpr int kGroups = CS * KT / 4;
+    Frag<NO> pf[CS][MT], ub[CS];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       if (i + 1 < kGroups) read_cols4<NI, C>(cf[(i + 1) & 1], s_kt, 4 * ((i + 1) % (KT / 4)), (i + 1) / (KT / 4));
+      if (Y && i == 0) {
+#pragma unroll
+        for (int ks = 0; ks < CS; ++ks) read_tri<false, C>(pf[ks], rec + Record<C>::P, ks);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) from[t] = *reinterpret_cast<const float4*>(dec + 3 * C + 16 * t + 4 * g);
+      }
       stage_end();
       mma_cols4(S, 4 * (i % (KT / 4)), cf[i & 1], uf[i / (KT / 4)]);
       if constexpr (Y) {
         if (i == 0) {
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const float ff[4] = {from[t].x, from[t].y, from[t].z, from[t].w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) O[t][r] *= ff[r];
+          }
+#pragma unroll
+          for (int ks = 0; ks < CS; ++ks) ub[ks] = to_frag<NO>(U[2 * ks], U[2 * ks + 1]);
+        }
+        if (i == (kGroups > 1 ? 1 : 0)) {
+#pragma unroll
+          for (int ks = 0; ks < CS; ++ks) mma_tri<false, C>(O, pf[ks], ks, ub[ks]);
+        }
+        if (i == kGroups - 1) {
           if (first < C) {
 #pragma unroll
             for (int t = 0; t < MT; ++t)
@@ -279,11 +320,12 @@ __global__ void __launch_bounds__(64 * (NW + 1)) k_delta_scan(DeltaArgs a, int c
               for (int r = 0; r < 4; ++r)
                 if (16 * t + 4 * g + r >= first) O[t][r] = kNaN;
           }
+          const int o = here(yo);
           const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
           for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; r += 2) store_el2<BF16>(yr, yo + (16 * t + r) * ldy, ldy, O[t][r], O[t][r + 1]);
+            for (int r = 0; r < 4; r += 2) store_el2<BF16>(yr, o + (16 * t + r) * ldy, ldy, O[t][r], O[t][r + 1]);
         }
       }
       stage_end();
@@ -409,7 +451,7 @@ hipError_t run(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep,
   const int chunks = (a.L + Z::C - 1) / Z::C;
   const int groups = ((SUM ? segs.ld() : a.Dv) + 16 * NW - 1) / (16 * NW);
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups * (SUM ? segs.count - 1 : segs.count);
-  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + 1)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
+  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
   return hipGetLastError();
 }
 

@@ -184,6 +184,13 @@ __device__ __forceinline__ uint4 load16(Buf r, int o) {
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
 }
 
+// the same offset, of which the compiler makes no table for a loop: sums with it
+// are formed where they are used instead of kept in registers throughout
+__device__ __forceinline__ int here(int o) {
+  asm volatile("" : "+v"(o));
+  return o;
+}
+
 // four tokens `ld` bytes apart, the first at byte `o` (kNowhere: a block of
 // features that do not exist); nd of the eight features exist
 template <bool BF16>
@@ -408,10 +415,11 @@ __device__ __forceinline__ void lds_copy(unsigned char* dst, const unsigned char
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + o), 16, o + l * 16, 0, 0, 0);
 }
 
-// Barriers of kernels whose last wave does nothing but copy the next chunk
+// Barriers of kernels whose last kCopy waves do nothing but copy the next chunk
 // into LDS (the waves that compute then have no such copy in flight, for which
-// the compiler would wait before each of their LDS reads): it arrives when
-// its copies are there, the others when their reads are done.
+// the compiler would wait before each of their LDS reads): they arrive when
+// their copies are there, the others when their reads are done.
+constexpr int kCopy = 4;
 __device__ __forceinline__ void barrier_copied() {
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
   asm volatile("" ::: "memory");
