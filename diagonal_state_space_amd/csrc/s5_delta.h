@@ -46,7 +46,7 @@ struct DeltaArgs {
   void* y;                 // [B, L, Hv, Dv]
   float* s_last;           // [B, Hv, Dk, Dv] or null; may be s0 itself
   void* ws;
-  unsigned char *frags, *recs;   // in ws: operand fragments of k and q, records of the chunks
+  unsigned char *frags, *recs;   // in ws: fragments of k and q by columns (backward), records of the chunks
   // backward only
   const void* dy;
   const float* ds_last;    // or null (zero)

@@ -61,26 +61,53 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
   const bool last = n0 + segs.chunks >= nc;
 
   if (w >= NW) {   // the copying waves
+    const int id = tid - 64 * NW;
+    const bool vec = vectored(a, BF16);
+    Stage<BF16, KP, 64 * kCopy> k, q;
     auto record = [&](int n) { return a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true, 3); };
+    auto load = [&](int n) {
+      const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
+      if constexpr (BF16) {
+        k.load(a, a.k, a.ldk, tok, min(len - n * C, C), hk, id, vec);
+        q.load(a, a.q, a.ldq, tok, min(len - n * C, C), hk, id, vec);
+      }
+    };
     auto copy_tri = [&](int n) { lds_copy<kCopy>(smem + Z::oTri, record(n) + Record<C>::P, 2 * Z::kTri, w - NW); };
     auto copy = [&](int n) {
       unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
-      lds_copy<kCopy>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(true), 3 * Z::kMat, w - NW);
+      if constexpr (BF16) {
+        k.store(dst, dst + Z::kMat, id);
+        q.store(nullptr, dst + 2 * Z::kMat, id);
+      } else {
+        const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(true);
+        lds_copy<kCopy>(dst, fr + Z::k_rows(true), Z::kMat, w - NW);
+        lds_copy<kCopy>(dst + Z::kMat, fr, 2 * Z::kMat, w - NW);
+      }
       lds_copy<kCopy>(dst + 3 * Z::kMat, record(n) + Record<C>::decays(true, 3), kFrag, w - NW);
     };
     if (n0 < n1) {
-      if (Z::kTwo) copy(n1 - 1);
+      load(n1 - 1);
+      if (Z::kTwo) {
+        copy(n1 - 1);
+        if (n1 - 1 > n0) load(n1 - 2);
+      }
       copy_tri(n1 - 1);
     }
     for (int n = n1 - 1; n >= n0; --n) {
-      if constexpr (!Z::kTwo) {
+      if constexpr (Z::kTwo) {
+        barrier_copied();
+        if (n > n0) copy(n - 1);
+        barrier_passed();   // T and P are read; the copies need not be there yet
+        if (n > n0) copy_tri(n - 1);
+        if (n - 1 > n0) load(n - 2);
+      } else {
         barrier_copied();
         copy(n);
+        barrier_copied();
+        if (n > n0) load(n - 1);
+        barrier_passed();
+        if (n > n0) copy_tri(n - 1);
       }
-      barrier_copied();
-      if (Z::kTwo && n > n0) copy(n - 1);
-      __builtin_amdgcn_s_barrier();   // T and P are read; the copies need not be there yet
-      if (n > n0) copy_tri(n - 1);
     }
     return;
   }
@@ -521,8 +548,8 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       const unsigned char* fr = a.frags + static_cast<int64_t>(blockIdx.x) * Z::frags(true);
 #pragma unroll
       for (int s = 0; s < CS; ++s) {
-        kf[s] = read_cols<NI, C>(fr + Z::kMat, w, s);
-        qf[s] = read_cols<NI, C>(fr + 2 * Z::kMat, w, s);
+        kf[s] = read_cols<NI, C>(fr, w, s);
+        qf[s] = read_cols<NI, C>(fr + Z::kMat, w, s);
       }
     }
     float kh = 0.0f;   // sum of to k.(U D'^T)

@@ -8,7 +8,8 @@
 //
 // Both products run on the matrix cores from staged k and q; P comes out
 // transposed, which is the order of its operand fragments, and is stored from
-// the registers. A kernel before this one puts k and q into fragments. The inverse: the 16 x 16 diagonal blocks by substitution, a
+// the registers. float32 k and q are split into fragments by a kernel before
+// this one. The inverse: the 16 x 16 diagonal blocks by substitution, a
 // column a lane; then blocks of 32 and 64 from halves,
 //   [X 0; B Y]^-1 = [X^-1 0; -Y^-1 B X^-1  Y^-1],
 // by float32 matrix instructions, the second factor from the accumulators of
@@ -31,11 +32,11 @@ __device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// k and q of a chunk and key head as operand fragments
-template <bool BF16, int KP, bool BACK>
-__global__ void __launch_bounds__(kThreads) k_delta_frags(DeltaArgs a, int chunks, bool vec) {
-  using Z = Shape<BF16, KP>;
-  constexpr int C = Z::C, es = Z::es;
+// float32 k and q of a chunk and key head as fragments
+template <int KP, bool BACK>
+__global__ void __launch_bounds__(kThreads) k_delta_frags(DeltaArgs a, int chunks) {
+  using Z = Shape<false, KP>;
+  constexpr int C = Z::C;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x;
   const int n = blockIdx.x % chunks, bk = blockIdx.x / chunks;
@@ -43,18 +44,12 @@ __global__ void __launch_bounds__(kThreads) k_delta_frags(DeltaArgs a, int chunk
   const int rows = min(length_of(a, b) - n * C, C);
   if (rows <= 0) return;
   const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-  const int ldk = static_cast<int>(a.ldk) * es, ldq = static_cast<int>(a.ldq) * es;
-  const Buf kr = rows_buf(static_cast<const char*>(a.k) + (tok * a.ldk + static_cast<int64_t>(hk) * a.Dk) * es, rows, ldk, a.Dk * es);
-  const Buf qr = rows_buf(static_cast<const char*>(a.q) + (tok * a.ldq + static_cast<int64_t>(hk) * a.Dk) * es, rows, ldq, a.Dk * es);
-  for (int i = tid; i < (C / 4) * (KP / 8); i += kThreads) {
-    const int tg = i / (KP / 8), dg = i % (KP / 8), nd = a.Dk - 8 * dg;
-    const Parts<BF16> k(load_block<BF16>(kr, block_offset<BF16>(tg, dg, ldk, a.Dk), ldk, nd, vec));
-    const Parts<BF16> q(load_block<BF16>(qr, block_offset<BF16>(tg, dg, ldq, a.Dk), ldq, nd, vec));
-    store_rows<BF16, Z::KS>(smem, k, tg, dg);
-    store_cols<BF16, C>(smem + Z::kMat, k, tg, dg);
-    if constexpr (BACK) store_cols<BF16, C>(smem + 2 * Z::kMat, q, tg, dg);
-    store_rows<BF16, Z::KS>(smem + (BACK ? 3 : 2) * Z::kMat, q, tg, dg);
-  }
+  const bool vec = vectored(a, false);
+  Stage<false, KP, kThreads> x;
+  x.load(a, a.k, a.ldk, tok, rows, hk, tid, vec);
+  x.store(smem + Z::k_rows(BACK), smem, tid);
+  x.load(a, a.q, a.ldq, tok, rows, hk, tid, vec);
+  x.store(smem + Z::q_rows(BACK), BACK ? smem + Z::kMat : nullptr, tid);
   __syncthreads();
   uint4* dst = reinterpret_cast<uint4*>(a.frags + static_cast<int64_t>(blockIdx.x) * Z::frags(BACK));
   for (int i = tid; i < Z::frags(BACK) / 16; i += kThreads) dst[i] = reinterpret_cast<const uint4*>(smem)[i];
@@ -83,9 +78,22 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, int chunks
   if (left <= 0) return;
   const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
 
-  const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(BACK);
-  lds_copy<kWaves>(s_k, fr, Z::kMat, w);
-  lds_copy<kWaves>(s_q, fr + (BACK ? 3 : 2) * Z::kMat, Z::kMat, w);
+  if constexpr (BF16) {
+    const bool vec = vectored(a, true);
+    Stage<BF16, KP, kThreads> k, q;
+    k.load(a, a.k, a.ldk, tok, min(left, C), hk, tid, vec);
+    q.load(a, a.q, a.ldq, tok, min(left, C), hk, tid, vec);
+    // the first of the heads that share a key leaves k and q by columns for the
+    // gradients
+    unsigned char* cols = BACK && h == hk * (a.Hv / a.Hk)
+                              ? a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(BACK) : nullptr;
+    k.store(s_k, cols, tid);
+    q.store(s_q, cols != nullptr ? cols + Z::kMat : nullptr, tid);
+  } else {
+    const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(BACK);
+    lds_copy<kWaves>(s_k, fr + Z::k_rows(BACK), Z::kMat, w);
+    lds_copy<kWaves>(s_q, fr + Z::q_rows(BACK), Z::kMat, w);
+  }
   // sums of g (a wave's 64 lanes hold the chunk)
   if (w == 0) {
     const bool live = l < C && l < left;
@@ -270,20 +278,20 @@ hipError_t run(const DeltaArgs& a, hipStream_t stream) {
   constexpr int C = Z::C;
   constexpr int square = C * (C + 4) * 4, stage = 2 * Z::kMat;
   constexpr int lds = (stage > square ? stage : square) + square + C * 8 + C * 4 + 16;
-  auto* frags = k_delta_frags<BF16, KP, BACK>;
   auto* prep = k_delta_prep<BF16, KP, BACK>;
-  static const hipError_t attr[2] = {
-      hipFuncSetAttribute(reinterpret_cast<const void*>(frags), hipFuncAttributeMaxDynamicSharedMemorySize, Z::frags(BACK)),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(prep), hipFuncAttributeMaxDynamicSharedMemorySize, lds)};
-  for (hipError_t e : attr)
-    if (e != hipSuccess) return e;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(prep), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return attr;
   const int chunks = (a.L + C - 1) / C;
-  const int V = BF16 ? 8 : 4;
-  auto ok = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  const bool vec = a.Dk % V == 0 && a.ldq % V == 0 && a.ldk % V == 0 && ok(a.q) && ok(a.k);
-  frags<<<dim3(static_cast<unsigned>(a.B * a.Hk * chunks)), dim3(kThreads), Z::frags(BACK), stream>>>(a, chunks, vec);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if constexpr (!BF16) {
+    auto* frags = k_delta_frags<KP, BACK>;
+    static const hipError_t frags_attr =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(frags), hipFuncAttributeMaxDynamicSharedMemorySize, Z::frags(BACK));
+    if (frags_attr != hipSuccess) return frags_attr;
+    frags<<<dim3(static_cast<unsigned>(a.B * a.Hk * chunks)), dim3(kThreads), Z::frags(BACK), stream>>>(a, chunks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   prep<<<dim3(static_cast<unsigned>(a.B * a.Hv * chunks)), dim3(kThreads), lds, stream>>>(a, chunks);
   return hipGetLastError();
 }

@@ -72,10 +72,26 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   if (SUM && n0 + segs.chunks >= nc) return;    // no segment follows
 
   if (w >= NW) {   // the copying waves
+    const int id = tid - 64 * NW;
+    const bool vec = vectored(a, BF16);
+    Stage<BF16, KP, 64 * kCopy> k, q;
+    auto load = [&](int n) {
+      const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
+      if constexpr (BF16) k.load(a, a.k, a.ldk, tok, min(len - n * C, C), hk, id, vec);
+      if constexpr (BF16 && Y) q.load(a, a.q, a.ldq, tok, min(len - n * C, C), hk, id, vec);
+    };
     auto copy = [&](int n) {
       unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
       const unsigned char* rec = a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(Z::kBack, NO);
-      lds_copy<kCopy>(dst, a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack), Z::kFrags, w - NW);
+      if constexpr (BF16) {
+        k.store(dst, dst + Z::kMat, id);
+        if constexpr (Y) q.store(dst + 2 * Z::kMat, nullptr, id);
+      } else {
+        const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack);
+        lds_copy<kCopy>(dst, fr + Z::k_rows(Z::kBack), Z::kMat, w - NW);
+        lds_copy<kCopy>(dst + Z::kMat, fr, Z::kMat, w - NW);
+        if constexpr (Y) lds_copy<kCopy>(dst + 2 * Z::kMat, fr + Z::q_rows(Z::kBack), Z::kMat, w - NW);
+      }
       if constexpr (Y) {
         lds_copy<kCopy>(dst + Z::kFrags, rec, Z::kRec, w - NW);
       } else {
@@ -83,14 +99,22 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
         lds_copy<kCopy>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(Z::kBack, NO), kFrag, w - NW);
       }
     };
-    if (Z::kTwo && n0 < n1) copy(n0);
+    if (n0 < n1) load(n0);
+    if (Z::kTwo && n0 < n1) {
+      copy(n0);
+      if (n0 + 1 < n1) load(n0 + 1);
+    }
     for (int n = n0; n < n1; ++n) {
-      if constexpr (!Z::kTwo) {
+      if constexpr (Z::kTwo) {
+        barrier_copied();
+        if (n + 1 < n1) copy(n + 1);
+        if (n + 2 < n1) load(n + 2);
+      } else {
         barrier_copied();
         copy(n);
+        barrier_copied();
+        if (n + 1 < n1) load(n + 1);
       }
-      barrier_copied();
-      if (Z::kTwo && n + 1 < n1) copy(n + 1);
     }
     return;
   }

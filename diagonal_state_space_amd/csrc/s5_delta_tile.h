@@ -390,17 +390,63 @@ struct Record {
 // What the kernels share for an io type and padded features of a key (KP = 64
 // or 128): parts of k and q (NI) and of what leads to y only (NO), tiles of 16
 // and steps of 32 tokens (MT, CS) and features (KT, KS), bytes of the fragments
-// of k or q of a chunk. The fragments of a key head's chunk are k by rows, k by
-// columns, q by rows (backward: q by columns before it).
+// of k or q of a chunk.
 template <bool BF16, int KP>
 struct Shape {
   static constexpr int C = chunk_of<BF16>();
   static constexpr int NI = BF16 ? 1 : 3, NO = BF16 ? 2 : 3;
   static constexpr int KS = KP / 32, KT = KP / 16, MT = C / 16, CS = C / 32;
   static constexpr int kMat = MT * KS * NI * kFrag;
-  static constexpr int frags(bool backward) { return (backward ? 4 : 3) * kMat; }
   static constexpr int es = BF16 ? 2 : 4;
+  // Fragments of a key head's chunk in the workspace: by columns k and (backward)
+  // q, which the gradients read; float32 io also by rows k and q, made by a
+  // kernel of their own. The copying waves of the chains take q and k of bf16 io
+  // from the call's arrays (16 us less for 128 sequence heads of 2048 tokens than
+  // through fragments), but splitting float32 would hold up the waves they share
+  // a SIMD with (5 x 333 tokens of 4 heads: 42 us instead of 36).
+  static constexpr int frags(bool back) { return ((back ? 2 : BF16 ? 0 : 1) + (BF16 ? 0 : 2)) * kMat; }
+  static constexpr int k_rows(bool back) { return (back ? 2 : 1) * kMat; }
+  static constexpr int q_rows(bool back) { return k_rows(back) + kMat; }
 };
+
+// Blocks of a chunk's k and q on their way from memory to fragments in LDS, one
+// or more for each of N threads (`id`).
+template <bool BF16, int KP, int N>
+struct Stage {
+  using Z = Shape<BF16, KP>;
+  static constexpr int kBlocks = (Z::C / 4) * (KP / 8), kJobs = (kBlocks + N - 1) / N;
+  Block<BF16> b[kJobs];
+
+  // tokens [tok, tok + rows) of head `hk`
+  __device__ __forceinline__ void load(const DeltaArgs& a, const void* p, int64_t stride, int64_t tok, int rows, int hk, int id, bool vec) {
+    const int ld = static_cast<int>(stride) * Z::es;
+    const Buf buf = rows_buf(static_cast<const char*>(p) + (tok * stride + static_cast<int64_t>(hk) * a.Dk) * Z::es, rows, ld, a.Dk * Z::es);
+#pragma unroll
+    for (int j = 0; j < kJobs; ++j) {
+      const int i = id + j * N, tg = i / (KP / 8), dg = i % (KP / 8);
+      b[j] = load_block<BF16>(buf, block_offset<BF16>(tg, dg, ld, i < kBlocks ? a.Dk : 0), ld, a.Dk - 8 * dg, vec);
+    }
+  }
+  // fragments by rows and by columns (null: without)
+  __device__ __forceinline__ void store(unsigned char* rows, unsigned char* cols, int id) const {
+#pragma unroll
+    for (int j = 0; j < kJobs; ++j) {
+      const int i = id + j * N, tg = i / (KP / 8), dg = i % (KP / 8);
+      if (i < kBlocks) {
+        const Parts<BF16> p(b[j]);
+        if (rows != nullptr) store_rows<BF16, Z::KS>(rows, p, tg, dg);
+        if (cols != nullptr) store_cols<BF16, Z::C>(cols, p, tg, dg);
+      }
+    }
+  }
+};
+
+// whether whole 16-byte groups of k and q are aligned
+__device__ __forceinline__ bool vectored(const DeltaArgs& a, bool bf16) {
+  const int V = bf16 ? 8 : 4;
+  return a.Dk % V == 0 && a.ldq % V == 0 && a.ldk % V == 0 &&
+         ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k)) & 15u) == 0;
+}
 
 // ---- 1 KB blocks from global memory straight into LDS ------------------------------
 typedef __attribute__((address_space(3))) void lds_void;
@@ -421,7 +467,11 @@ __device__ __forceinline__ void lds_copy(unsigned char* dst, const unsigned char
 // their copies are there, the others when their reads are done.
 constexpr int kCopy = 4;
 __device__ __forceinline__ void barrier_copied() {
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void barrier_passed() {   // the copying waves', with copies under way
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
