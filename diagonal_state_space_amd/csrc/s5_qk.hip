@@ -18,6 +18,7 @@
 // turns dropped, then sine and cosine in float32.
 // The pass is bound by the bytes of q and k in and out.
 #include <algorithm>
+#include <type_traits>
 
 #include "s5_common.h"
 #include "s5_delta.h"
@@ -27,27 +28,10 @@ namespace s5 {
 namespace {
 
 constexpr int kThreads = 256;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr int kMaxTile = 8;        // tokens whose angles a workgroup holds at once
 constexpr int kBackwardBlocks = 1024;
-
-template <bool BF16, int V>
-__device__ __forceinline__ void load_chunk(const void* p, int64_t i, float (&x)[V]) {
-  if constexpr (V == 1) {
-    if constexpr (BF16) x[0] = bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-    else x[0] = static_cast<const float*>(p)[i];
-  } else if constexpr (BF16) {
-    const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(w[j] << 16);
-      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  } else {
-    const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
-  }
-}
 
 template <bool BF16, int V>
 __device__ __forceinline__ void store_chunk(void* p, int64_t i, const float (&x)[V]) {
@@ -58,10 +42,46 @@ __device__ __forceinline__ void store_chunk(void* p, int64_t i, const float (&x)
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      w[j] = f32_to_bf16(x[2 * j]) | (static_cast<uint32_t>(f32_to_bf16(x[2 * j + 1])) << 16);
+      w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * j], x[2 * j + 1]}, bf16x2));
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = uint4{w[0], w[1], w[2], w[3]};
   } else {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = float4{x[0], x[1], x[2], x[3]};
+  }
+}
+
+// a chunk's bits
+template <bool BF16, int V>
+struct Raw {
+  uint32_t w[V == 1 ? 1 : 4];
+};
+
+template <bool BF16, int V>
+__device__ __forceinline__ Raw<BF16, V> load_raw(const void* p, int64_t i) {
+  Raw<BF16, V> r;
+  if constexpr (V == 1) {
+    if constexpr (BF16) r.w[0] = static_cast<const uint16_t*>(p)[i];
+    else r.w[0] = static_cast<const uint32_t*>(p)[i];
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (BF16 ? 2 : 4));
+    r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
+  }
+  return r;
+}
+
+template <bool BF16, int V>
+__device__ __forceinline__ void values(const Raw<BF16, V>& r, float (&x)[V]) {
+  if constexpr (V == 1) {
+    x[0] = __uint_as_float(BF16 ? r.w[0] << 16 : r.w[0]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BF16) {
+        x[2 * j] = __uint_as_float(r.w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(r.w[j] & 0xffff0000u);
+      } else {
+        x[j] = __uint_as_float(r.w[j]);
+      }
+    }
   }
 }
 
@@ -74,7 +94,6 @@ __global__ void __launch_bounds__(kThreads) k_qk(QkArgs a, int G, int tile) {
   const int RP = a.R >> 1;                               // rotated pairs
   const int lane = tid & (G - 1);
   const int slot = tid / G, slots = kThreads / G;        // rows a pass of the workgroup handles
-  const int heads = a.Hq + a.Hk;
   const int chunks = a.D / V;
 
   int c0[U], c1[U];      // the unit's chunks; chunks and beyond: none
@@ -90,11 +109,131 @@ __global__ void __launch_bounds__(kThreads) k_qk(QkArgs a, int G, int tile) {
       c1[j] = u + RP / V;
     }
   }
-  float w[2][U][2][V];   // weights of q and k at this lane's features
-  float dw[2][U][2][V];
+  float dw[2][U][2][V];   // this lane's sums of the weights' gradients
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float* p = m == 0 ? a.wq : a.wk;
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[m][j][h][i] = 0.0f;
+
+  struct Row {
+    Raw<BF16, V> x[U][2], d[U][2];
+  };
+  // row i of q (m = 0) or k of the tile at t0: its token and head, and its bits
+  auto place = [&](int m, int i, int& t, int& hh) {
+    const int heads = m == 0 ? a.Hq : a.Hk;
+    t = i / heads;
+    hh = i - t * heads;
+  };
+  auto load = [&](int m, int64_t t0, int i, Row& row) {
+    int t, hh;
+    place(m, i, t, hh);
+    const int heads = m == 0 ? a.Hq : a.Hk;
+    const int64_t in = (t0 + t) * (m == 0 ? a.ldq : a.ldk) + static_cast<int64_t>(hh) * a.D;
+    const int64_t out = ((t0 + t) * heads + hh) * a.D;
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = h == 0 ? c0[j] : c1[j];
+        if (c < chunks) {
+          row.x[j][h] = load_raw<BF16, V>(m == 0 ? a.q : a.k, in + c * V);
+          if constexpr (GRAD) row.d[j][h] = load_raw<BF16, V>(m == 0 ? a.dq_out : a.dk_out, out + c * V);
+        } else {
+          row.x[j][h] = row.d[j][h] = Raw<BF16, V>{};
+        }
+      }
+  };
+  auto compute = [&](auto m_, int64_t t0, int i, bool live, const Row& row, const float (&w)[U][2][V]) {
+    constexpr int m = decltype(m_)::value;
+    int t, hh;
+    place(m, i, t, hh);
+    float x[U][2][V], d[U][2][V];
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        values<BF16, V>(row.x[j][h], x[j][h]);
+        if constexpr (GRAD) values<BF16, V>(row.d[j][h], d[j][h]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum = fmaf(x[j][h][e], x[j][h][e], sum);
+      }
+    float r = 1.0f;
+    if (a.norm) {
+      for (int o = 1; o < G; o <<= 1) sum += __shfl_xor(sum, o);
+      r = 1.0f / sqrtf(fmaf(sum, a.inv_m, a.eps));
+    }
+    // rotates the values of the unit (forward) or turns them back (gradient)
+    auto rotate = [&](float (&v)[U][2][V]) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int u = lane + j * G;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const int p = u * V + e;
+          if (p < RP) {
+            float2 cs = s_cs[t * RP + p];
+            if constexpr (GRAD) cs.y = -cs.y;
+            float& f0 = v[j][INSIDE ? (2 * e) / V : 0][INSIDE ? (2 * e) % V : e];
+            float& f1 = v[j][INSIDE ? (2 * e + 1) / V : 1][INSIDE ? (2 * e + 1) % V : e];
+            const float v0 = f0, v1 = f1;
+            f0 = v0 * cs.x - v1 * cs.y;
+            f1 = v1 * cs.x + v0 * cs.y;
+          }
+        }
+      }
+    };
+    if constexpr (!GRAD) {
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[j][h][e] *= r * w[j][h][e];
+      rotate(x);
+    } else {
+      rotate(d);
+      float dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float n = x[j][h][e] * r;
+            if (live) dw[m][j][h][e] += d[j][h][e] * n;
+            d[j][h][e] *= w[j][h][e];
+            dot = fmaf(d[j][h][e], n, dot);
+            x[j][h][e] = n;
+          }
+      if (a.norm) {
+        for (int o = 1; o < G; o <<= 1) dot += __shfl_xor(dot, o);
+        dot *= a.inv_m;
+      } else {
+        dot = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[j][h][e] = r * (d[j][h][e] - x[j][h][e] * dot);
+    }
+    if (live) {
+      void* dst = m == 0 ? a.q_out : a.k_out;
+      const int64_t out = ((t0 + t) * (m == 0 ? a.Hq : a.Hk) + hh) * a.D;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (c0[j] < chunks) store_chunk<BF16, V>(dst, out + c0[j] * V, x[j][0]);
+        if (c1[j] < chunks) store_chunk<BF16, V>(dst, out + c1[j] * V, x[j][1]);
+      }
+    }
+  };
+  auto weights = [&](const float* p, float (&w)[U][2][V]) {
 #pragma unroll
     for (int j = 0; j < U; ++j)
 #pragma unroll
@@ -102,13 +241,18 @@ __global__ void __launch_bounds__(kThreads) k_qk(QkArgs a, int G, int tile) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int c = h == 0 ? c0[j] : c1[j];
-          w[m][j][h][i] = p != nullptr && c < chunks ? p[c * V + i] : 1.0f;
-          dw[m][j][h][i] = 0.0f;
+          w[j][h][i] = p != nullptr && c < chunks ? p[c * V + i] : 1.0f;
         }
-  }
+  };
 
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tile; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * tile) {
     const int nt = static_cast<int>(a.T - t0 < tile ? a.T - t0 : tile);
+    const int rq = nt * a.Hq, rk = nt * a.Hk;
+    // every slot has a row in every pass (the last one again where there is none
+    // left), so that the next row's loads need no condition; the first are on
+    // their way while the angles are computed
+    Row row;
+    load(0, t0, min(slot, rq - 1), row);
     __syncthreads();     // the previous tile's angles are read
     for (int i = tid; i < nt * RP; i += kThreads) {
       const int t = i / RP, p = i - t * RP;
@@ -119,104 +263,23 @@ __global__ void __launch_bounds__(kThreads) k_qk(QkArgs a, int G, int tile) {
       s_cs[i] = float2{a.rope_scale * cs, a.rope_scale * sn};
     }
     __syncthreads();
-    const int rows = nt * heads;
-    for (int r0 = 0; r0 < rows; r0 += slots) {
-      const int row = r0 + slot;
-      const bool live = row < rows;
-      const int t = live ? row / heads : 0, hh = live ? row - t * heads : 0;
-      const int m = hh < a.Hq ? 0 : 1;
-      const int64_t in = m == 0 ? (t0 + t) * a.ldq + static_cast<int64_t>(hh) * a.D
-                                : (t0 + t) * a.ldk + static_cast<int64_t>(hh - a.Hq) * a.D;
-      const int64_t out = m == 0 ? ((t0 + t) * a.Hq + hh) * a.D : ((t0 + t) * a.Hk + hh - a.Hq) * a.D;
-      const void* src = m == 0 ? a.q : a.k;
-      float x[U][2][V], d[U][2][V];
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = h == 0 ? c0[j] : c1[j];
-          if (live && c < chunks) {
-            load_chunk<BF16, V>(src, in + c * V, x[j][h]);
-            if constexpr (GRAD) load_chunk<BF16, V>(m == 0 ? a.dq_out : a.dk_out, out + c * V, d[j][h]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[j][h][i] = d[j][h][i] = 0.0f;
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) sum = fmaf(x[j][h][i], x[j][h][i], sum);
-        }
-      float r = 1.0f;
-      if (a.norm) {
-        for (int o = 1; o < G; o <<= 1) sum += __shfl_xor(sum, o);
-        r = 1.0f / sqrtf(fmaf(sum, a.inv_m, a.eps));
-      }
-      // rotates the values of the unit (forward) or turns them back (gradient)
-      auto rotate = [&](float (&v)[U][2][V]) {
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const int u = lane + j * G;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int p = u * V + i;
-            if (p < RP) {
-              float2 cs = s_cs[t * RP + p];
-              if constexpr (GRAD) cs.y = -cs.y;
-              float& e = v[j][INSIDE ? (2 * i) / V : 0][INSIDE ? (2 * i) % V : i];
-              float& f = v[j][INSIDE ? (2 * i + 1) / V : 1][INSIDE ? (2 * i + 1) % V : i];
-              const float e0 = e, f0 = f;
-              e = e0 * cs.x - f0 * cs.y;
-              f = f0 * cs.x + e0 * cs.y;
-            }
-          }
-        }
-      };
-      if constexpr (!GRAD) {
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[j][h][i] *= r * (m == 0 ? w[0][j][h][i] : w[1][j][h][i]);
-        rotate(x);
-      } else {
-        rotate(d);
-        float dot = 0.0f;
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float n = x[j][h][i] * r;
-              const float dn = d[j][h][i] * n;
-              if (m == 0) dw[0][j][h][i] += dn; else dw[1][j][h][i] += dn;
-              const float e = d[j][h][i] * (m == 0 ? w[0][j][h][i] : w[1][j][h][i]);
-              dot = fmaf(e, n, dot);
-              d[j][h][i] = e;
-              x[j][h][i] = n;
-            }
-        if (a.norm) {
-          for (int o = 1; o < G; o <<= 1) dot += __shfl_xor(dot, o);
-          dot *= a.inv_m;
-        } else {
-          dot = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[j][h][i] = r * (d[j][h][i] - x[j][h][i] * dot);
-      }
-      if (live) {
-        void* dst = m == 0 ? a.q_out : a.k_out;
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          if (c0[j] < chunks) store_chunk<BF16, V>(dst, out + c0[j] * V, x[j][0]);
-          if (c1[j] < chunks) store_chunk<BF16, V>(dst, out + c1[j] * V, x[j][1]);
-        }
-      }
+    float w[U][2][V];
+    weights(a.wq, w);
+    for (int r0 = 0; r0 < rq; r0 += slots) {
+      Row next;
+      const int i = r0 + slot;
+      if (r0 + slots < rq) load(0, t0, min(i + slots, rq - 1), next);
+      else load(1, t0, min(slot, rk - 1), next);
+      compute(std::integral_constant<int, 0>{}, t0, min(i, rq - 1), i < rq, row, w);
+      row = next;
+    }
+    weights(a.wk, w);
+    for (int r0 = 0; r0 < rk; r0 += slots) {
+      Row next;
+      const int i = r0 + slot;
+      if (r0 + slots < rk) load(1, t0, min(i + slots, rk - 1), next);
+      compute(std::integral_constant<int, 1>{}, t0, min(i, rk - 1), i < rk, row, w);
+      row = next;
     }
   }
 
