@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 256;
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-constexpr int kMaxTile = 8;        // tokens whose angles a workgroup holds at once
+constexpr int kMaxTile = 16;       // tokens whose angles a workgroup holds at once
 constexpr int kBackwardBlocks = 1024;
 
 template <bool BF16, int V>
@@ -346,11 +346,13 @@ int lanes_of(const QkArgs& a, int V) {
   return G;
 }
 
-// tokens of a tile: up to eight share a workgroup's angles; fewer while that
-// would leave compute units without a workgroup
+// tokens of a tile: as many as share a workgroup's angles, fewer while that would
+// leave a compute unit with less than two workgroups. (40 heads of 128 over 16384
+// tokens: tiles of 4, 8, 16 and 32 tokens take 79, 74, 71 and 97 us, the gradients
+// of 32 heads over 8192 tokens 51, 46, 42 and 42.)
 int tile_of(const QkArgs& a) {
   int tile = kMaxTile;
-  while (tile > 1 && a.T / tile < 1024) tile >>= 1;
+  while (tile > 1 && a.T / tile < 512) tile >>= 1;
   return tile;
 }
 
