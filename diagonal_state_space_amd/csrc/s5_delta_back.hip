@@ -290,9 +290,9 @@ struct Grad : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;
   static constexpr int NW = KP / 16, kThreads = 64 * NW;
   static constexpr int kTri = tri_frags<Z::C>(), kJobs = (4 * kTri + NW - 1) / NW;
-  static constexpr int kTok = 3 * Z::C * 4, kItems = (kTok + kThreads - 1) / kThreads;   // staged rows of 8 of dR, U, dY
-  static constexpr int oR = 0, oU = oR + Z::MT * 3 * kFrag, oY = oU + Z::MT * 3 * kFrag;
-  static constexpr int oS = oY + Z::MT * Z::NI * kFrag, oD = oS + Z::KT * 3 * kFrag, kStage = oD + Z::KT * 3 * kFrag;
+  static constexpr int kItems = 4 * Z::C * 4 / kThreads;    // staged eights of dR, U, dY and V of a thread
+  static constexpr int oR = 0, oU = oR + Z::MT * 3 * kFrag, oY = oU + Z::MT * 3 * kFrag, oV = oY + Z::MT * Z::NI * kFrag;
+  static constexpr int oS = oV + Z::MT * Z::NI * kFrag, oD = oS + Z::KT * 3 * kFrag, kStage = oD + Z::KT * 3 * kFrag;
   static constexpr int kW = 4 * kTri * 3 * kFrag;           // over the stage when that is read
   static constexpr int oG = kStage > kW ? kStage : kW;      // double sums of g
   static constexpr int oB = oG + Z::C * 8;                  // beta, from, to
@@ -324,7 +324,7 @@ __device__ __forceinline__ void store_row8(unsigned char* base, const float (&x)
   }
 }
 
-// VEC: whole 16-byte groups of dy are aligned
+// VEC: whole 16-byte groups of dy and v are aligned
 template <bool BF16, int KP, bool VEC>
 __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunks, DeltaKeep keep) {
   using Z = Grad<BF16, KP>;
@@ -336,14 +336,8 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
   float* s_rv = reinterpret_cast<float*>(smem + Z::oRV);
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = blockIdx.x % chunks, bk = blockIdx.x / chunks;
-  const int b = bk / a.Hk, hk = bk - b * a.Hk;
-  const int left = length_of(a, b) - n * C;
-  if (left <= 0) return;
-  const int rows = min(left, C);
-  const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-  const int group = a.Hv / a.Hk;
-  const int ldy = a.Hv * a.Dv * es, ldw = keep.dvp * 4;
+  const int group = a.Hv / a.Hk, items = a.B * a.Hk * chunks;
+  const int ldy = a.Hv * a.Dv * es, ldv = static_cast<int>(a.ldv) * es, ldw = keep.dvp * 4;
 
   auto value_of = [&](const Frag<NI>& f, int e) {
     float x = static_cast<float>(f.p[0][e]);
@@ -352,32 +346,56 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     return x;
   };
 
-  for (int hh = 0; hh < group; ++hh) {
-    const int h = hk * group + hh;
-    const int64_t bh = static_cast<int64_t>(b) * a.Hv + h, cn = bh * chunks + n;
-    const float* kept = keep.p + cn * keep.size(C);
-    const Buf kb = rows_buf(kept, 1, 0, keep.size(C) * 4);
-    const Buf yr = rows_buf(static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es, rows, ldy, a.Dv * es);
-    float gi = 0.0f;
+  // The workgroup's chunks it, it + gridDim, ... and their heads, one after the
+  // other: the next one's first loads are under way while one is finished.
+  struct Place {
+    int it, hh, b, hk, n, left;
+  };
+  auto advance = [&](Place& p) {
+    if (++p.hh < group) return true;
+    p.hh = 0;
+    for (p.it += gridDim.x; p.it < items; p.it += gridDim.x) {
+      const int bk = p.it / chunks;
+      p.n = p.it - bk * chunks;
+      p.b = bk / a.Hk;
+      p.hk = bk - p.b * a.Hk;
+      p.left = length_of(a, p.b) - p.n * C;
+      if (p.left > 0) return true;
+    }
+    return false;
+  };
 
-    // a row's eight values: of the kept arrays, and of dy as its bits
-    struct Eight {
-      uint4 lo, hi;
-    };
+  // a row's eight values: of the kept arrays, of dy and v as their bits
+  struct Eight {
+    uint4 lo, hi;
+  };
+  auto floats = [](const Eight& x, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = __uint_as_float(word(x.lo, i));
+      f[4 + i] = __uint_as_float(word(x.hi, i));
+    }
+  };
+  Eight es_, ed, et[Z::kItems];
+  float gn = 0.0f, bn = 0.0f;    // the first wave's: g and beta
+  auto fetch = [&](const Place& p, int v0) {
+    const int id = here(tid), h = p.hk * group + p.hh;
+    const int64_t tok = static_cast<int64_t>(p.b) * a.L + p.n * C;
+    const Buf kb = rows_buf(keep.p + ((static_cast<int64_t>(p.b) * a.Hv + h) * chunks + p.n) * keep.size(C), 1, 0, keep.size(C) * 4);
     auto load_kept = [&](int at, int row, int rows, int v) {
       const int o = row < rows && v < keep.dvp ? at * 4 + row * ldw + v * 4 : kNowhere;
       return Eight{load16(kb, o), load16(kb, o + 16)};
     };
-    auto load_dy = [&](int row, int v) {
-      const int o = row * ldy + v * es;
+    auto load_io = [&](Buf r, int ld, int row, int v) {
+      const int o = row * ld + v * es;
       Eight x{};
       if constexpr (VEC) {
-        x.lo = load16(yr, v < a.Dv ? o : kNowhere);
-        if constexpr (!BF16) x.hi = load16(yr, v + 4 < a.Dv ? o + 16 : kNowhere);
+        x.lo = load16(r, v < a.Dv ? o : kNowhere);
+        if constexpr (!BF16) x.hi = load16(r, v + 4 < a.Dv ? o + 16 : kNowhere);
       } else {
         uint32_t e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = load_raw<BF16>(yr, v + i < a.Dv ? o + i * es : kNowhere);
+        for (int i = 0; i < 8; ++i) e[i] = load_raw<BF16>(r, v + i < a.Dv ? o + i * es : kNowhere);
         if constexpr (BF16) {
           x.lo = uint4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
         } else {
@@ -387,44 +405,51 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
       return x;
     };
-    auto floats = [](const Eight& x, float (&f)[8]) {
+    // this thread's row of S and D' and eight of its 32 values; its eights of the rest
+    es_ = load_kept(0, id >> 2, keep.dkp, v0 + 8 * (id & 3));
+    ed = load_kept(keep.at_d(), id >> 2, keep.dkp, v0 + 8 * (id & 3));
+    const int rows = min(p.left, C);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = __uint_as_float(word(x.lo, i));
-        f[4 + i] = __uint_as_float(word(x.hi, i));
+    for (int j = 0; j < Z::kItems; ++j) {
+      const int i = id + j * Z::kThreads, mat = __builtin_amdgcn_readfirstlane(i / (4 * C));
+      const int row = (i >> 2) % C, v = v0 + 8 * (i & 3);
+      if (mat < 2) {
+        et[j] = load_kept(mat == 0 ? keep.at_r(C) : keep.at_u(), row, C, v);
+      } else {
+        const char* src = mat == 2 ? static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es
+                                   : static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es;
+        const int ld = mat == 2 ? ldy : ldv;
+        et[j] = load_io(rows_buf(src, rows, ld, a.Dv * es), ld, row, v);
       }
-    };
-    Eight es_, ed, et[Z::kItems];
-    const int srow = here(tid) >> 2, sc = tid & 3;    // this thread's row of S and D' and eight of its 32 values
-    auto fetch = [&](int v0) {
-      es_ = load_kept(0, srow, keep.dkp, v0 + 8 * sc);
-      ed = load_kept(keep.at_d(), srow, keep.dkp, v0 + 8 * sc);
-#pragma unroll
-      for (int j = 0; j < Z::kItems; ++j) {
-        const int i = tid + j * Z::kThreads;
-        if (i < Z::kTok) {
-          const int mat = __builtin_amdgcn_readfirstlane(i / (4 * C)), row = (i >> 2) % C, v = v0 + 8 * (i & 3);
-          et[j] = mat == 2 ? load_dy(row, v) : load_kept(mat == 0 ? keep.at_r(C) : keep.at_u(), row, C, v);
-        }
-      }
-    };
+    }
+    if (v0 == 0 && w == 0) {
+      const bool in = l < C && l < p.left;
+      gn = in ? a.g[(tok + l) * a.Hv + h] : 0.0f;
+      bn = in ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
+    }
+  };
 
-    f32x4 E[MT], F[MT], H[MT], W[Z::kJobs][2];
+  Place at{static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x), group - 1, 0, 0, 0, 0};
+  if (!advance(at)) return;
+  fetch(at, 0);
+  for (bool more = true; more;) {
+    const int h = at.hk * group + at.hh, left = at.left, rows = min(left, C);
+    const int64_t tok = static_cast<int64_t>(at.b) * a.L + at.n * C;
+    const float gi = gn;
+
+    f32x4 E[MT], F[MT], H[MT], W[Z::kJobs][2], RV = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < MT; ++t) E[t] = F[t] = H[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < Z::kJobs; ++j) W[j][0] = W[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     float sd = 0.0f;   // <D', S>
-    fetch(0);
     __syncthreads();     // the previous head's sums and decays are read
     if (w == 0) {
-      const bool live = l < C && l < left;
-      gi = live ? a.g[(tok + l) * a.Hv + h] : 0.0f;
-      const double s = chunk_sums(gi);
+      const double s = chunk_sums(gn);
       const double end = __shfl(s, C - 1);
       if (l < C) {
         s_g[l] = s;
-        s_b[l] = live ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
+        s_b[l] = bn;
         s_from[l] = expf(static_cast<float>(s));
         s_to[l] = expf(static_cast<float>(end - s));
       }
@@ -433,31 +458,30 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     for (int v0 = 0; v0 < keep.dvp; v0 += 32) {
       __syncthreads();   // the previous step is read
       {
+        const int id = here(tid);
         float x[8], y[8];
         floats(es_, x);
         floats(ed, y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sd = fmaf(x[i], y[i], sd);
-        store_row8<3>(smem + Z::oS, x, srow, sc);
-        store_row8<3>(smem + Z::oD, y, srow, sc);
+        store_row8<3>(smem + Z::oS, x, id >> 2, id & 3);
+        store_row8<3>(smem + Z::oD, y, id >> 2, id & 3);
 #pragma unroll
         for (int j = 0; j < Z::kItems; ++j) {
-          const int i = tid + j * Z::kThreads;
-          if (i < Z::kTok) {
-            const int mat = __builtin_amdgcn_readfirstlane(i / (4 * C)), row = (i >> 2) % C, c = i & 3;
-            if (BF16 && mat == 2) {
-              unsigned char* p = smem + Z::oY + (row >> 4) * kFrag + 8 * (c >> 1);
-              *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1), row & 15, 0)) = uint2{et[j].lo.x, et[j].lo.y};
-              *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1) + 1, row & 15, 0)) = uint2{et[j].lo.z, et[j].lo.w};
-            } else {
-              floats(et[j], x);
-              store_row8<3>(smem + (mat == 0 ? Z::oR : mat == 1 ? Z::oU : Z::oY), x, row, c);
-            }
+          const int i = id + j * Z::kThreads, mat = __builtin_amdgcn_readfirstlane(i / (4 * C));
+          const int row = (i >> 2) % C, c = i & 3;
+          if (BF16 && mat >= 2) {
+            unsigned char* p = smem + (mat == 2 ? Z::oY : Z::oV) + (row >> 4) * kFrag + 8 * (c >> 1);
+            *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1), row & 15, 0)) = uint2{et[j].lo.x, et[j].lo.y};
+            *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1) + 1, row & 15, 0)) = uint2{et[j].lo.z, et[j].lo.w};
+          } else {
+            floats(et[j], x);
+            store_row8<3>(smem + (mat == 0 ? Z::oR : mat == 1 ? Z::oU : mat == 2 ? Z::oY : Z::oV), x, row, c);
           }
         }
       }
       __syncthreads();
-      if (v0 + 32 < keep.dvp) fetch(v0 + 32);
+      if (v0 + 32 < keep.dvp) fetch(at, v0 + 32);
       {
         const Frag<3> sf = read_frag<3>(smem + Z::oS, w, 0);
         {
@@ -476,6 +500,10 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oU, t, 0);
         mma(H, x, read_frag<3>(smem + Z::oD, w, 0));
         __builtin_amdgcn_sched_barrier(0);
+        // dR.V is the diagonal of dR V^T: the last waves' tiles (they have the
+        // fewest other products)
+        const int t = NW - 1 - w;
+        if (t < MT) RV = mma(read_frag<3>(smem + Z::oR, t, 0), read_frag<NI>(smem + Z::oV, t, 0), RV);
       }
       // job: W1, W1 transposed, W2, W2 transposed; the fragment of its operand
 #pragma unroll
@@ -525,27 +553,16 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(smem + (job * 3 + p) * kFrag + l * 16) = fr.p[p];
       }
     }
-    // dR.V: every wave C / NW tokens side by side, kLanes lanes a token
-    {
-      constexpr int kLanes = 64 * NW / C;
-      const int id = here(tid), i = id / kLanes, lv = 4 * (id % kLanes), ldv = static_cast<int>(a.ldv) * es;
-      const Buf vr = rows_buf(static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es, rows, ldv, a.Dv * es);
-      float s = 0.0f;
-      for (int v = lv; v < a.Dv; v += 4 * kLanes) {
-        const uint4 r = load16(kb, (keep.at_r(C) + i * keep.dvp + v) * 4);
+    if (NW - 1 - w < MT) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s = fmaf(__uint_as_float(word(r, e)), value<BF16>(load_raw<BF16>(vr, v + e < a.Dv ? i * ldv + (v + e) * es : kNowhere)), s);
-      }
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor(s, o);
-      if (lv == 0) s_rv[i] = s;
+      for (int r = 0; r < 4; ++r)
+        if (4 * gg + r == mm) s_rv[16 * (NW - 1 - w) + mm] = RV[r];
     }
     // k and q of this wave's features, as operands over the tokens; their slots
     // are also the values at the accumulators' places
     Frag<NI> kf[CS], qf[CS];
     {
-      const unsigned char* fr = a.frags + static_cast<int64_t>(blockIdx.x) * Z::frags(true);
+      const unsigned char* fr = a.frags + static_cast<int64_t>(at.it) * Z::frags(true);
 #pragma unroll
       for (int s = 0; s < CS; ++s) {
         kf[s] = read_cols<NI, C>(fr, w, s);
@@ -567,6 +584,9 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
     }
     __syncthreads();   // W1 and W2 are there
+    Place next = at;
+    more = advance(next);
+    if (more) fetch(next, 0);
     auto triangle = [&](f32x4 (&c)[MT], int mat, const Frag<NI> (&x)[CS]) {
 #pragma unroll
       for (int s = 0; s < CS; ++s) {
@@ -608,14 +628,14 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
     // dq and dk of the heads that share a key: in LDS until the last one
     f32x4* sum = reinterpret_cast<f32x4*>(smem + Z::oAcc) + w * 2 * MT * 64 + here(l);
-    if (hh > 0) {
+    if (at.hh > 0) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         E[t] += sum[t * 64];
         H[t] += sum[(MT + t) * 64];
       }
     }
-    if (hh + 1 < group) {
+    if (at.hh + 1 < group) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         sum[t * 64] = E[t];
@@ -623,8 +643,8 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
     } else {
       const int c = 16 * w + m, ldo = a.Hk * a.Dk * es;
-      const Buf qo = rows_buf(static_cast<char*>(a.dq) + (tok * a.Hk + hk) * a.Dk * es, rows, ldo, a.Dk * es);
-      const Buf ko = rows_buf(static_cast<char*>(a.dk) + (tok * a.Hk + hk) * a.Dk * es, rows, ldo, a.Dk * es);
+      const Buf qo = rows_buf(static_cast<char*>(a.dq) + (tok * a.Hk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
+      const Buf ko = rows_buf(static_cast<char*>(a.dk) + (tok * a.Hk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
       const int oo = here(c < a.Dk ? 4 * g * ldo + c * es : kNowhere);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -668,6 +688,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         a.dbeta[(tok + l) * a.Hv + h] = s_rv[l] + k1;
       }
     }
+    at = next;
   }
 }
 
@@ -720,8 +741,11 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   e = hipGetLastError();
   if (e != hipSuccess || a.L == 0) return e;
   // dy is contiguous and 16-byte aligned
-  auto* grad = a.Dv % (BF16 ? 8 : 4) == 0 ? grad_vec : grad_one;
-  grad<<<dim3(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hk * chunks)), dim3(G::kThreads), G::kLds - (a.Hv == a.Hk ? G::kAcc : 0), stream>>>(a, chunks, keep);
+  constexpr int V = BF16 ? 8 : 4;
+  auto* grad = a.Dv % V == 0 && a.ldv % V == 0 && (reinterpret_cast<uintptr_t>(a.v) & 15u) == 0 ? grad_vec : grad_one;
+  // one workgroup at a time fits a compute unit (KP = 64: two)
+  const int64_t items = static_cast<int64_t>(a.B) * a.Hk * chunks, most = KP == 64 ? 512 : 256;
+  grad<<<dim3(static_cast<unsigned>(items < most ? items : most)), dim3(G::kThreads), G::kLds - (a.Hv == a.Hk ? G::kAcc : 0), stream>>>(a, chunks, keep);
   return hipGetLastError();
 }
 
