@@ -61,7 +61,8 @@ hipError_t launch_delta_tokens(const DeltaArgs& a, hipStream_t stream);
 // What the chains leave for the gradients of a chunk (float32, columns padded
 // with zeros to 16), one after the other for each of [B*Hv][chunks]: the state S
 // at its start and the gradient D' of its end state [dkp][dvp], its writes U and
-// their gradients dR [C][dvp].
+// their gradients dR [C][dvp]. Each is stored as the accumulators' tiles, those
+// of 16 columns one after the other: four rows of a column in 16 bytes.
 struct DeltaKeep {
   float* p;
   int dkp, dvp;

@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
   const int cg = turn % groups, seg = (turn / groups) % count + (SUM ? 1 : 0), bh = turn / (groups * count) * 8 + die;
   if (bh >= a.B * a.Hv) return;
   const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / (a.Hv / a.Hk);
-  const int col = (cg * NW + w) * 16 + m;
-  const bool wave_live = (cg * NW + w) * 16 < a.Dv, live = col < a.Dv;
+  const int wg = cg * NW + w, col = wg * 16 + m;
+  const bool wave_live = wg * 16 < a.Dv, live = col < a.Dv;
   const int len = length_of(a, b);
   const int nc = (len + C - 1) / C;
   const int n0 = seg * segs.chunks, n1 = min(nc, n0 + segs.chunks);
@@ -130,7 +130,6 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
   uint32_t ob[MT][4];
   const int ldy = a.Hv * a.Dv * es;
   const int yo = live ? 4 * g * ldy + col * es : kNowhere;
-  const int ko = (4 * g * keep.dvp + col) * 4;   // rows behind the kept ones are outside their buffer
   const unsigned char* s_tt = smem + Z::oTri;
   const unsigned char* s_pt = s_tt + Z::kTri;
   auto fetch = [&](int n) {
@@ -162,12 +161,10 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     Frag<3> tf[2][MT];
     if (wave_live) {
       if constexpr (!SUM) {
-        const int o = here(ko);
-        const Buf kd = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_d(), keep.dkp, keep.dvp * 4, keep.dvp * 4);
+        const int o = here(16 * l);
+        const Buf kd = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_d() + 16 * wg * keep.dkp, 1, 0, keep.dkp * 64);
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) store_el<false>(kd, o + (16 * t + r) * keep.dvp * 4, D[t][r]);
+        for (int t = 0; t < KT; ++t) store16(kd, o + t * 1024, D[t]);
       }
       // dU = to K D' + P^T dO
 #pragma unroll
@@ -217,8 +214,8 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     auto read_c = [&](int i) { read_cols4<NI, C>(cf[i & 1], i < kGroups / 2 ? s_kt : s_qt, 4 * (i % (KT / 4)), i % (kGroups / 2) / (KT / 4)); };
     read_c(0);
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-    const int o1 = here(ko), o2 = here(yo);
-    const Buf kr = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_r(C), C, keep.dvp * 4, keep.dvp * 4);
+    const int o1 = here(16 * l), o2 = here(yo);
+    const Buf kr = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_r(C) + 16 * wg * C, 1, 0, C * 64);
     const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -226,11 +223,9 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
       const float4 be = *reinterpret_cast<const float4*>(dec + 2 * C + 16 * t + 4 * g);
       const float4 fs = *reinterpret_cast<const float4*>(dec + 3 * C + 16 * t + 4 * g);
       const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w}, ss[4] = {fs.x, fs.y, fs.z, fs.w};
+      if constexpr (!SUM) store16(kr, o1 + t * 1024, dR[t]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if constexpr (!SUM) store_el<false>(kr, o1 + (16 * t + r) * keep.dvp * 4, dR[t][r]);
-        dR[t][r] *= bb[r];
-      }
+      for (int r = 0; r < 4; ++r) dR[t][r] *= bb[r];
       if constexpr (!SUM) {
 #pragma unroll
         for (int r = 0; r < 4; r += 2) store_el2<BF16>(vr, o2 + (16 * t + r) * ldy, ldy, dR[t][r], dR[t][r + 1]);
@@ -319,8 +314,26 @@ __device__ __forceinline__ void store_row8(unsigned char* base, const float (&x)
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const uint4 w = __builtin_bit_cast(uint4, f.p[i]);
-    *reinterpret_cast<uint2*>(p + i * kFrag + slot_of(2 * (c & 1), row & 15, 0)) = uint2{w.x, w.y};
-    *reinterpret_cast<uint2*>(p + i * kFrag + slot_of(2 * (c & 1) + 1, row & 15, 0)) = uint2{w.z, w.w};
+    *reinterpret_cast<uint2*>(p + i * kFrag + slot_of(2 * (c & 1), row & 15, 2 * (c & 1))) = uint2{w.x, w.y};
+    *reinterpret_cast<uint2*>(p + i * kFrag + slot_of(2 * (c & 1) + 1, row & 15, 2 * (c & 1) + 1)) = uint2{w.z, w.w};
+  }
+}
+
+// rows 4 rg.. of the columns 2 cp, 2 cp + 1 of a step, as they are kept, into
+// row fragments
+__device__ __forceinline__ void store_rows4(unsigned char* base, const uint4& lo, const uint4& hi, int rg, int cp) {
+  const int gc = (cp & 7) >> 1;
+  const int o = (rg >> 2) * 3 * kFrag + slot_of(gc, 4 * (rg & 3), gc) + 8 * (cp >> 3) + 4 * (cp & 1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float x = __uint_as_float(word(lo, j)), y = __uint_as_float(word(hi, j));
+    unsigned char* p = base + (o ^ 16 * j);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      *reinterpret_cast<uint32_t*>(p + i * kFrag) = upper(x, y);
+      x -= cut(x);
+      y -= cut(y);
+    }
   }
 }
 
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = a.Hv / a.Hk, items = a.B * a.Hk * chunks;
-  const int ldy = a.Hv * a.Dv * es, ldv = static_cast<int>(a.ldv) * es, ldw = keep.dvp * 4;
+  const int ldy = a.Hv * a.Dv * es, ldv = static_cast<int>(a.ldv) * es;
 
   auto value_of = [&](const Frag<NI>& f, int e) {
     float x = static_cast<float>(f.p[0][e]);
@@ -365,7 +378,8 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     return false;
   };
 
-  // a row's eight values: of the kept arrays, of dy and v as their bits
+  // eight values: four rows of two columns of the kept arrays, a row's of dy and
+  // v as their bits
   struct Eight {
     uint4 lo, hi;
   };
@@ -382,8 +396,10 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     const int id = here(tid), h = p.hk * group + p.hh;
     const int64_t tok = static_cast<int64_t>(p.b) * a.L + p.n * C;
     const Buf kb = rows_buf(keep.p + ((static_cast<int64_t>(p.b) * a.Hv + h) * chunks + p.n) * keep.size(C), 1, 0, keep.size(C) * 4);
-    auto load_kept = [&](int at, int row, int rows, int v) {
-      const int o = row < rows && v < keep.dvp ? at * 4 + row * ldw + v * 4 : kNowhere;
+    // four rows of two columns
+    auto load_kept = [&](int at, int rows, int i) {
+      const int rg = i >> 4, v = v0 + 2 * (i & 15);
+      const int o = 4 * rg < rows && v < keep.dvp ? at * 4 + (v >> 4) * rows * 64 + (rg >> 2) * 1024 + (rg & 3) * 256 + (v & 15) * 16 : kNowhere;
       return Eight{load16(kb, o), load16(kb, o + 16)};
     };
     auto load_io = [&](Buf r, int ld, int row, int v) {
@@ -405,16 +421,15 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
       return x;
     };
-    // this thread's row of S and D' and eight of its 32 values; its eights of the rest
-    es_ = load_kept(0, id >> 2, keep.dkp, v0 + 8 * (id & 3));
-    ed = load_kept(keep.at_d(), id >> 2, keep.dkp, v0 + 8 * (id & 3));
+    es_ = load_kept(0, keep.dkp, id);
+    ed = load_kept(keep.at_d(), keep.dkp, id);
     const int rows = min(p.left, C);
 #pragma unroll
     for (int j = 0; j < Z::kItems; ++j) {
       const int i = id + j * Z::kThreads, mat = __builtin_amdgcn_readfirstlane(i / (4 * C));
       const int row = (i >> 2) % C, v = v0 + 8 * (i & 3);
       if (mat < 2) {
-        et[j] = load_kept(mat == 0 ? keep.at_r(C) : keep.at_u(), row, C, v);
+        et[j] = load_kept(mat == 0 ? keep.at_r(C) : keep.at_u(), C, i % (4 * C));
       } else {
         const char* src = mat == 2 ? static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es
                                    : static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es;
@@ -437,12 +452,11 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     const int64_t tok = static_cast<int64_t>(at.b) * a.L + at.n * C;
     const float gi = gn;
 
-    f32x4 E[MT], F[MT], H[MT], W[Z::kJobs][2], RV = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 E[MT], F[MT], H[MT], W[Z::kJobs][2], RV = {0.0f, 0.0f, 0.0f, 0.0f}, SD = RV;
 #pragma unroll
     for (int t = 0; t < MT; ++t) E[t] = F[t] = H[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < Z::kJobs; ++j) W[j][0] = W[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float sd = 0.0f;   // <D', S>
     __syncthreads();     // the previous head's sums and decays are read
     if (w == 0) {
       const double s = chunk_sums(gn);
@@ -459,51 +473,51 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       __syncthreads();   // the previous step is read
       {
         const int id = here(tid);
-        float x[8], y[8];
-        floats(es_, x);
-        floats(ed, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sd = fmaf(x[i], y[i], sd);
-        store_row8<3>(smem + Z::oS, x, id >> 2, id & 3);
-        store_row8<3>(smem + Z::oD, y, id >> 2, id & 3);
+        store_rows4(smem + Z::oS, es_.lo, es_.hi, id >> 4, id & 15);
+        store_rows4(smem + Z::oD, ed.lo, ed.hi, id >> 4, id & 15);
 #pragma unroll
         for (int j = 0; j < Z::kItems; ++j) {
           const int i = id + j * Z::kThreads, mat = __builtin_amdgcn_readfirstlane(i / (4 * C));
           const int row = (i >> 2) % C, c = i & 3;
           if (BF16 && mat >= 2) {
             unsigned char* p = smem + (mat == 2 ? Z::oY : Z::oV) + (row >> 4) * kFrag + 8 * (c >> 1);
-            *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1), row & 15, 0)) = uint2{et[j].lo.x, et[j].lo.y};
-            *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1) + 1, row & 15, 0)) = uint2{et[j].lo.z, et[j].lo.w};
+            *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1), row & 15, 2 * (c & 1))) = uint2{et[j].lo.x, et[j].lo.y};
+            *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1) + 1, row & 15, 2 * (c & 1) + 1)) = uint2{et[j].lo.z, et[j].lo.w};
+          } else if (mat < 2) {
+            store_rows4(smem + (mat == 0 ? Z::oR : Z::oU), et[j].lo, et[j].hi, (i >> 4) % (C / 4), i & 15);
           } else {
+            float x[8];
             floats(et[j], x);
-            store_row8<3>(smem + (mat == 0 ? Z::oR : mat == 1 ? Z::oU : mat == 2 ? Z::oY : Z::oV), x, row, c);
+            store_row8<3>(smem + (mat == 2 ? Z::oY : Z::oV), x, row, c);
           }
         }
       }
       __syncthreads();
       if (v0 + 32 < keep.dvp) fetch(at, v0 + 32);
       {
-        const Frag<3> sf = read_frag<3>(smem + Z::oS, w, 0);
+        const Frag<3> sf = read_frag<3>(smem + Z::oS, w, l >> 4);
         {
           Frag<NI> y[MT];
 #pragma unroll
-          for (int t = 0; t < MT; ++t) y[t] = read_frag<NI>(smem + Z::oY, t, 0);
+          for (int t = 0; t < MT; ++t) y[t] = read_frag<NI>(smem + Z::oY, t, l >> 4);
           mma(E, y, sf);
         }
         __builtin_amdgcn_sched_barrier(0);   // one product's fragments at a time: more would spill
         Frag<3> x[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oR, t, 0);
+        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oR, t, l >> 4);
         mma(F, x, sf);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oU, t, 0);
-        mma(H, x, read_frag<3>(smem + Z::oD, w, 0));
+        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oU, t, l >> 4);
+        const Frag<3> df = read_frag<3>(smem + Z::oD, w, l >> 4);
+        mma(H, x, df);
+        SD = mma(df, sf, SD);   // <D', S> is the sum of its diagonal
         __builtin_amdgcn_sched_barrier(0);
         // dR.V is the diagonal of dR V^T: the last waves' tiles (they have the
         // fewest other products)
         const int t = NW - 1 - w;
-        if (t < MT) RV = mma(read_frag<3>(smem + Z::oR, t, 0), read_frag<NI>(smem + Z::oV, t, 0), RV);
+        if (t < MT) RV = mma(read_frag<3>(smem + Z::oR, t, l >> 4), read_frag<NI>(smem + Z::oV, t, l >> 4), RV);
       }
       // job: W1, W1 transposed, W2, W2 transposed; the fragment of its operand
 #pragma unroll
@@ -514,17 +528,17 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
           const int st = C == 32 ? 0 : (mat & 1) ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
           // tiles of the products (accumulator rows): 2 st, 2 st + 1; the row tile: columns
           if (mat == 0) {
-            const Frag<NI> c = read_frag<NI>(smem + Z::oY, rt, 0);
-            Frag<3> p[2] = {read_frag<3>(smem + Z::oU, 2 * st, 0), read_frag<3>(smem + Z::oU, 2 * st + 1, 0)};
+            const Frag<NI> c = read_frag<NI>(smem + Z::oY, rt, l >> 4);
+            Frag<3> p[2] = {read_frag<3>(smem + Z::oU, 2 * st, l >> 4), read_frag<3>(smem + Z::oU, 2 * st + 1, l >> 4)};
             mma(W[j], p, c);
           } else if (mat == 1) {
-            const Frag<3> c = read_frag<3>(smem + Z::oU, rt, 0);
-            Frag<NI> p[2] = {read_frag<NI>(smem + Z::oY, 2 * st, 0), read_frag<NI>(smem + Z::oY, 2 * st + 1, 0)};
+            const Frag<3> c = read_frag<3>(smem + Z::oU, rt, l >> 4);
+            Frag<NI> p[2] = {read_frag<NI>(smem + Z::oY, 2 * st, l >> 4), read_frag<NI>(smem + Z::oY, 2 * st + 1, l >> 4)};
             mma(W[j], p, c);
           } else {
             const unsigned char *s1 = smem + (mat == 2 ? Z::oU : Z::oR), *s2 = smem + (mat == 2 ? Z::oR : Z::oU);
-            const Frag<3> c = read_frag<3>(s2, rt, 0);
-            Frag<3> p[2] = {read_frag<3>(s1, 2 * st, 0), read_frag<3>(s1, 2 * st + 1, 0)};
+            const Frag<3> c = read_frag<3>(s2, rt, l >> 4);
+            Frag<3> p[2] = {read_frag<3>(s1, 2 * st, l >> 4), read_frag<3>(s1, 2 * st + 1, l >> 4)};
             mma(W[j], p, c);
           }
         }
@@ -569,7 +583,10 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         qf[s] = read_cols<NI, C>(fr + Z::kMat, w, s);
       }
     }
-    float kh = 0.0f;   // sum of to k.(U D'^T)
+    float sd = 0.0f, kh = 0.0f;   // <D', S> and the sum of to k.(U D'^T)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (4 * gg + r == mm) sd = SD[r];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const float4 fr = *reinterpret_cast<const float4*>(s_from + 16 * t + 4 * gg);

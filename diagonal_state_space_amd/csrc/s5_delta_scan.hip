@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   const int cg = turn % groups, seg = (turn / groups) % count, bh = turn / (groups * count) * 8 + die;
   if (bh >= a.B * a.Hv) return;
   const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / (a.Hv / a.Hk);
-  const int col = (cg * NW + w) * 16 + m;
-  const bool wave_live = (cg * NW + w) * 16 < (SUM ? segs.ld() : a.Dv), live = col < a.Dv;
+  const int wg = cg * NW + w, col = wg * 16 + m;
+  const bool wave_live = wg * 16 < (SUM ? segs.ld() : a.Dv), live = col < a.Dv;
   const int len = length_of(a, b);
   const int nc = (len + C - 1) / C;
   const int n0 = seg * segs.chunks, n1 = min(nc, n0 + segs.chunks);
@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   uint32_t vb[MT][4];
   const int ldv = static_cast<int>(a.ldv) * es, ldy = a.Hv * a.Dv * es;
   const int vo = live ? 4 * g * ldv + col * es : kNowhere, yo = live ? 4 * g * ldy + col * es : kNowhere;
-  const int ko = (4 * g * keep.dvp + col) * 4;   // rows behind the kept ones are outside their buffer
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     const int o = here(vo);
@@ -164,12 +163,10 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
     const unsigned char *s_kt = s_k + Z::kMat, *s_q = s_k + 2 * Z::kMat, *rec = s_k + Z::kFrags;
     const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - kFrag);
     if constexpr (KEEP) {
-      const int o = here(ko);
-      const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C), keep.dkp, keep.dvp * 4, keep.dvp * 4);
+      const int o = here(16 * l);
+      const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + 16 * wg * keep.dkp, 1, 0, keep.dkp * 64);
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) store_el<false>(p, o + (16 * t + r) * keep.dvp * 4, S[t][r]);
+      for (int t = 0; t < KT; ++t) store16(p, o + t * 1024, S[t]);
     }
     // X = K S, R over it and U = T R are the chain; what is not (O = Q S) and the
     // splitting of the next operand go between, into the gaps of its stages
@@ -283,13 +280,17 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
     }
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     if constexpr (KEEP) {
-      const int o = here(ko);
-      const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_u(), C, keep.dvp * 4, keep.dvp * 4);
+      const int o = here(16 * l);
+      const Buf p = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_u() + 16 * wg * C, 1, 0, C * 64);
+      if (first < C) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          store_el<false>(p, o + (16 * t + r) * keep.dvp * 4, 16 * t + 4 * g + r < first ? U[t][r] : kNaN);
+          for (int r = 0; r < 4; ++r)
+            if (16 * t + 4 * g + r >= first) U[t][r] = kNaN;
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) store16(p, o + t * 1024, U[t]);
     }
     // S <- whole S + K^T (to U), and O <- scale from O + P U beside it
     Frag<NI> cf[2][4];

@@ -184,6 +184,10 @@ __device__ __forceinline__ uint4 load16(Buf r, int o) {
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
 }
 
+__device__ __forceinline__ void store16(Buf r, int o, f32x4 x) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned, x), r, o, 0, 0);
+}
+
 // the same offset, of which the compiler makes no table for a loop: sums with it
 // are formed where they are used instead of kept in registers throughout
 __device__ __forceinline__ int here(int o) {
