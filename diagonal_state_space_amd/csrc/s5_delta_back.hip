@@ -285,49 +285,58 @@ struct Grad : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;
   static constexpr int NW = KP / 16, kThreads = 64 * NW;
   static constexpr int kTri = tri_frags<Z::C>(), kJobs = (4 * kTri + NW - 1) / NW;
-  static constexpr int kItems = 4 * Z::C * 4 / kThreads;    // staged eights of dR, U, dY and V of a thread
+  static constexpr int kItems = 4 * Z::MT / NW;   // staged tiles of dR, U, dY and V of a wave
+  // whether all waves' j-th jobs are of W2, or of W1
+  static constexpr bool all_w2(int j) { return (j + 1) * NW <= 2 * kTri; }
+  static constexpr bool all_w1(int j) { return j * NW >= 2 * kTri; }
   static constexpr int oR = 0, oU = oR + Z::MT * 3 * kFrag, oY = oU + Z::MT * 3 * kFrag, oV = oY + Z::MT * Z::NI * kFrag;
   static constexpr int oS = oV + Z::MT * Z::NI * kFrag, oD = oS + Z::KT * 3 * kFrag, kStage = oD + Z::KT * 3 * kFrag;
   static constexpr int kW = 4 * kTri * 3 * kFrag;           // over the stage when that is read
   static constexpr int oG = kStage > kW ? kStage : kW;      // double sums of g
   static constexpr int oB = oG + Z::C * 8;                  // beta, from, to
   static constexpr int oRed = oB + 3 * Z::C * 4;            // [NW][2][C] row sums
-  static constexpr int oSum = oRed + NW * 2 * Z::C * 4;     // [NW][2] sums
-  static constexpr int oRV = oSum + NW * 2 * 4;             // [C] dR.V
+  static constexpr int oRV = oRed + NW * 2 * Z::C * 4;      // [C] dR.V
   static constexpr int oAcc = oRV + Z::C * 4;               // [NW][2 MT][64] dq and dk, where heads share a key
   static constexpr int kAcc = NW * 2 * Z::MT * kFrag, kLds = oAcc + kAcc;
 };
 
-// sum over the 16 lanes of a row (in all of them)
-__device__ __forceinline__ float row_sum(float x) {
-  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xf, 0xf, true));   // row_ror:8
-  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x124, 0xf, 0xf, true));
-  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x122, 0xf, 0xf, true));
-  return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x121, 0xf, 0xf, true));
+// Sums of N values each over the 16 lanes of a row: halves of the values and of
+// the lanes are exchanged four times, after which lane m has N/16 of the sums,
+// from index m N/16 on.
+template <int CTRL>
+__device__ __forceinline__ float from_lane(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
 }
-
-// eight values of row `row` (features 8c.. of a step of 32) into row fragments
-template <int NP>
-__device__ __forceinline__ void store_row8(unsigned char* base, const float (&x)[8], int row, int c) {
-  const Frag<NP> f = to_frag<NP>(x);
-  unsigned char* p = base + (row >> 4) * NP * kFrag + 8 * (c >> 1);
+template <int CTRL, int H, int N>
+__device__ __forceinline__ void fold(float (&x)[N], bool upper) {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const uint4 w = __builtin_bit_cast(uint4, f.p[i]);
-    *reinterpret_cast<uint2*>(p + i * kFrag + slot_of(2 * (c & 1), row & 15, 2 * (c & 1))) = uint2{w.x, w.y};
-    *reinterpret_cast<uint2*>(p + i * kFrag + slot_of(2 * (c & 1) + 1, row & 15, 2 * (c & 1) + 1)) = uint2{w.z, w.w};
+  for (int i = 0; i < H; ++i) {
+    const float a = x[i], b = x[i + H];
+    x[i] = (upper ? b : a) + from_lane<CTRL>(upper ? a : b);
   }
 }
+template <int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], int m) {
+  fold<0x140, N / 2>(x, m & 8);    // row_mirror
+  fold<0x141, N / 4>(x, m & 4);    // row_half_mirror
+  fold<0x4e, N / 8>(x, m & 2);     // quad_perm 2, 3, 0, 1
+  fold<0xb1, N / 16>(x, m & 1);    // quad_perm 1, 0, 3, 2
+}
 
-// rows 4 rg.. of the columns 2 cp, 2 cp + 1 of a step, as they are kept, into
-// row fragments
-__device__ __forceinline__ void store_rows4(unsigned char* base, const uint4& lo, const uint4& hi, int rg, int cp) {
-  const int gc = (cp & 7) >> 1;
-  const int o = (rg >> 2) * 3 * kFrag + slot_of(gc, 4 * (rg & 3), gc) + 8 * (cp >> 3) + 4 * (cp & 1);
+// Places of a lane's values in row fragments: of rows l/16 * 4.. of the columns
+// 2 cp, 2 cp + 1 (cp = l%16) of a step, as they are kept, and of the columns
+// 8 (l%4).. of row l/4. A wave has 16 rows of either.
+__device__ __forceinline__ int kept_place(int l) {
+  const int cp = l & 15, gc = (cp & 7) >> 1;
+  return slot_of(gc, 4 * (l >> 4), gc) + 8 * (cp >> 3) + 4 * (cp & 1);
+}
+__device__ __forceinline__ int row_place(int l) { return slot_of(2 * (l & 1), l >> 2, 2 * (l & 1)) + 8 * ((l >> 1) & 1); }
+
+__device__ __forceinline__ void store_kept(unsigned char* tile, int place, const uint4& lo, const uint4& hi) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float x = __uint_as_float(word(lo, j)), y = __uint_as_float(word(hi, j));
-    unsigned char* p = base + (o ^ 16 * j);
+    unsigned char* p = tile + (place ^ 16 * j);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       *reinterpret_cast<uint32_t*>(p + i * kFrag) = upper(x, y);
@@ -336,6 +345,45 @@ __device__ __forceinline__ void store_rows4(unsigned char* base, const uint4& lo
     }
   }
 }
+// NI = 1: the bits of eight bf16, else two times four floats
+template <int NI>
+__device__ __forceinline__ void store_row8(unsigned char* tile, int place, const uint4& lo, const uint4& hi) {
+  // the second four: the next slot group, whose rows are exchanged by one more
+  unsigned char *p = tile + place, *q = tile + ((place + 256) ^ 16);
+  if constexpr (NI == 1) {
+    *reinterpret_cast<uint2*>(p) = uint2{lo.x, lo.y};
+    *reinterpret_cast<uint2*>(q) = uint2{lo.z, lo.w};
+  } else {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __uint_as_float(word(lo, i));
+      x[4 + i] = __uint_as_float(word(hi, i));
+    }
+    const Frag<NI> f = to_frag<NI>(x);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint4 w = __builtin_bit_cast(uint4, f.p[i]);
+      *reinterpret_cast<uint2*>(p + i * kFrag) = uint2{w.x, w.y};
+      *reinterpret_cast<uint2*>(q + i * kFrag) = uint2{w.z, w.w};
+    }
+  }
+}
+
+// One of the C x C products' operand fragments: W1 = dY U^T (mat 0) and
+// transposed (1), W2 = dR U^T (2, 3); the larger products first. Fragment f has
+// the row tile rt and the products of 32 from tile 2 st on.
+template <int C>
+struct Job {
+  static constexpr int kTri = tri_frags<C>();
+  int q, mat, f, rt, st;
+  __device__ __forceinline__ explicit Job(int n) : q(n), mat(n < 2 * kTri ? 2 + n / kTri : n / kTri - 2), f(n % kTri) {
+    rt = C == 32 ? f : (mat & 1) ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : (f >> 1) + 1);
+    st = C == 32 ? 0 : (mat & 1) ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
+  }
+  __device__ __forceinline__ bool ours() const { return q < 4 * kTri; }
+  __device__ __forceinline__ bool w2() const { return q < 2 * kTri; }
+};
 
 // VEC: whole 16-byte groups of dy and v are aligned
 template <bool BF16, int KP, bool VEC>
@@ -345,12 +393,10 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
   extern __shared__ __align__(16) unsigned char smem[];
   double* s_g = reinterpret_cast<double*>(smem + Z::oG);
   float *s_b = reinterpret_cast<float*>(smem + Z::oB), *s_from = s_b + C, *s_to = s_from + C;
-  float *s_red = reinterpret_cast<float*>(smem + Z::oRed), *s_sum = reinterpret_cast<float*>(smem + Z::oSum);
-  float* s_rv = reinterpret_cast<float*>(smem + Z::oRV);
+  float *s_red = reinterpret_cast<float*>(smem + Z::oRed), *s_rv = reinterpret_cast<float*>(smem + Z::oRV);
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = a.Hv / a.Hk, items = a.B * a.Hk * chunks;
-  const int ldy = a.Hv * a.Dv * es, ldv = static_cast<int>(a.ldv) * es;
 
   auto value_of = [&](const Frag<NI>& f, int e) {
     float x = static_cast<float>(f.p[0][e]);
@@ -378,32 +424,32 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     return false;
   };
 
-  // eight values: four rows of two columns of the kept arrays, a row's of dy and
-  // v as their bits
+  // A step's values of a thread, eight of each: rows of S and D' (tile w); then
+  // 16 rows of a wave at a time of dR, U, dY and V (tile w + j NW of all four)
   struct Eight {
     uint4 lo, hi;
   };
-  auto floats = [](const Eight& x, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = __uint_as_float(word(x.lo, i));
-      f[4 + i] = __uint_as_float(word(x.hi, i));
-    }
-  };
+  constexpr int kFirstIo = 2 * MT;   // tile numbers of dY and V
+  auto all_kept = [](int j) { return (j + 1) * NW <= kFirstIo; };
+  auto all_io = [](int j) { return j * NW >= kFirstIo; };
   Eight es_, ed, et[Z::kItems];
   float gn = 0.0f, bn = 0.0f;    // the first wave's: g and beta
+  const int lane_kept = g * 256 + (m & 7) * 32, lane_s = lane_kept + (m >> 3) * keep.dkp * 64, lane_r = lane_kept + (m >> 3) * C * 64;
   auto fetch = [&](const Place& p, int v0) {
-    const int id = here(tid), h = p.hk * group + p.hh;
+    const int h = p.hk * group + p.hh;
     const int64_t tok = static_cast<int64_t>(p.b) * a.L + p.n * C;
-    const Buf kb = rows_buf(keep.p + ((static_cast<int64_t>(p.b) * a.Hv + h) * chunks + p.n) * keep.size(C), 1, 0, keep.size(C) * 4);
-    // four rows of two columns
-    auto load_kept = [&](int at, int rows, int i) {
-      const int rg = i >> 4, v = v0 + 2 * (i & 15);
-      const int o = 4 * rg < rows && v < keep.dvp ? at * 4 + (v >> 4) * rows * 64 + (rg >> 2) * 1024 + (rg & 3) * 256 + (v & 15) * 16 : kNowhere;
-      return Eight{load16(kb, o), load16(kb, o + 16)};
+    const float* kept = keep.p + ((static_cast<int64_t>(p.b) * a.Hv + h) * chunks + p.n) * keep.size(C);
+    // four rows of two columns of the array at `at`, tile t of its `rows` rows:
+    // what does not exist is outside the buffer
+    auto load_kept = [&](int at, int rows, int t, int o) {
+      const Buf b = rows_buf(kept + at + v0 * rows + t * 256, 16 * t < rows ? 1 : 0, 0, (v0 + 16 < keep.dvp ? rows * 64 : 0) + 1024);
+      return Eight{load16(b, o), load16(b, o + 16)};
     };
-    auto load_io = [&](Buf r, int ld, int row, int v) {
-      const int o = row * ld + v * es;
+    auto load_io = [&](bool second, int t) {
+      const int64_t ld = second ? a.ldv : a.Hv * a.Dv;
+      const char* src = static_cast<const char*>(second ? a.v : a.dy) + ((tok + 16 * t) * ld + static_cast<int64_t>(h) * a.Dv) * es;
+      const int ldb = static_cast<int>(ld) * es, v = v0 + 8 * (l & 3), o = (l >> 2) * ldb + v * es;
+      const Buf r = rows_buf(src, min(p.left, C) - 16 * t, ldb, a.Dv * es);
       Eight x{};
       if constexpr (VEC) {
         x.lo = load16(r, v < a.Dv ? o : kNowhere);
@@ -421,21 +467,13 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
       return x;
     };
-    es_ = load_kept(0, keep.dkp, id);
-    ed = load_kept(keep.at_d(), keep.dkp, id);
-    const int rows = min(p.left, C);
+    es_ = load_kept(0, keep.dkp, w, lane_s);
+    ed = load_kept(keep.at_d(), keep.dkp, w, lane_s);
 #pragma unroll
     for (int j = 0; j < Z::kItems; ++j) {
-      const int i = id + j * Z::kThreads, mat = __builtin_amdgcn_readfirstlane(i / (4 * C));
-      const int row = (i >> 2) % C, v = v0 + 8 * (i & 3);
-      if (mat < 2) {
-        et[j] = load_kept(mat == 0 ? keep.at_r(C) : keep.at_u(), C, i % (4 * C));
-      } else {
-        const char* src = mat == 2 ? static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es
-                                   : static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es;
-        const int ld = mat == 2 ? ldy : ldv;
-        et[j] = load_io(rows_buf(src, rows, ld, a.Dv * es), ld, row, v);
-      }
+      const int t = w + j * NW;
+      if (all_kept(j) || (!all_io(j) && t < kFirstIo)) et[j] = load_kept(t < MT ? keep.at_r(C) : keep.at_u(), C, t % MT, lane_r);
+      else et[j] = load_io(t >= kFirstIo + MT, t % MT);
     }
     if (v0 == 0 && w == 0) {
       const bool in = l < C && l < p.left;
@@ -443,6 +481,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       bn = in ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
     }
   };
+  const int kept_at = kept_place(l), row_at = row_place(l);
 
   Place at{static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x), group - 1, 0, 0, 0, 0};
   if (!advance(at)) return;
@@ -468,125 +507,127 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         s_to[l] = expf(static_cast<float>(end - s));
       }
     }
+    // k and q of this wave's features, as operands over the tokens; their slots
+    // are also the values at the accumulators' places
+    Frag<NI> kf[CS], qf[CS];
+    int v0 = 0;
 #pragma clang loop unroll(disable)
-    for (int v0 = 0; v0 < keep.dvp; v0 += 32) {
+    do {
       __syncthreads();   // the previous step is read
       {
-        const int id = here(tid);
-        store_rows4(smem + Z::oS, es_.lo, es_.hi, id >> 4, id & 15);
-        store_rows4(smem + Z::oD, ed.lo, ed.hi, id >> 4, id & 15);
+        store_kept(smem + Z::oS + w * 3 * kFrag, here(kept_at), es_.lo, es_.hi);
+        store_kept(smem + Z::oD + w * 3 * kFrag, here(kept_at), ed.lo, ed.hi);
 #pragma unroll
         for (int j = 0; j < Z::kItems; ++j) {
-          const int i = id + j * Z::kThreads, mat = __builtin_amdgcn_readfirstlane(i / (4 * C));
-          const int row = (i >> 2) % C, c = i & 3;
-          if (BF16 && mat >= 2) {
-            unsigned char* p = smem + (mat == 2 ? Z::oY : Z::oV) + (row >> 4) * kFrag + 8 * (c >> 1);
-            *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1), row & 15, 2 * (c & 1))) = uint2{et[j].lo.x, et[j].lo.y};
-            *reinterpret_cast<uint2*>(p + slot_of(2 * (c & 1) + 1, row & 15, 2 * (c & 1) + 1)) = uint2{et[j].lo.z, et[j].lo.w};
-          } else if (mat < 2) {
-            store_rows4(smem + (mat == 0 ? Z::oR : Z::oU), et[j].lo, et[j].hi, (i >> 4) % (C / 4), i & 15);
-          } else {
-            float x[8];
-            floats(et[j], x);
-            store_row8<3>(smem + (mat == 2 ? Z::oY : Z::oV), x, row, c);
-          }
+          const int t = w + j * NW;
+          if (all_kept(j) || (!all_io(j) && t < kFirstIo)) store_kept(smem + (t < MT ? Z::oR : Z::oU) + (t % MT) * 3 * kFrag, here(kept_at), et[j].lo, et[j].hi);
+          else store_row8<NI>(smem + (t < kFirstIo + MT ? Z::oY : Z::oV) + (t % MT) * NI * kFrag, here(row_at), et[j].lo, et[j].hi);
         }
       }
       __syncthreads();
-      if (v0 + 32 < keep.dvp) fetch(at, v0 + 32);
+      v0 += 32;
+      if (v0 < keep.dvp) {
+        fetch(at, v0);
+      } else {
+        const unsigned char* fr = a.frags + static_cast<int64_t>(at.it) * Z::frags(true);
+#pragma unroll
+        for (int s = 0; s < CS; ++s) {
+          kf[s] = read_cols<NI, C>(fr, w, s);
+          qf[s] = read_cols<NI, C>(fr + Z::kMat, w, s);
+        }
+      }
       {
-        const Frag<3> sf = read_frag<3>(smem + Z::oS, w, l >> 4);
+        const Frag<3> sf = read_frag<3>(smem + Z::oS, w, g);
         {
           Frag<NI> y[MT];
 #pragma unroll
-          for (int t = 0; t < MT; ++t) y[t] = read_frag<NI>(smem + Z::oY, t, l >> 4);
+          for (int t = 0; t < MT; ++t) y[t] = read_frag<NI>(smem + Z::oY, t, g);
           mma(E, y, sf);
         }
         __builtin_amdgcn_sched_barrier(0);   // one product's fragments at a time: more would spill
         Frag<3> x[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oR, t, l >> 4);
+        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oR, t, g);
         mma(F, x, sf);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oU, t, l >> 4);
-        const Frag<3> df = read_frag<3>(smem + Z::oD, w, l >> 4);
+        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oU, t, g);
+        const Frag<3> df = read_frag<3>(smem + Z::oD, w, g);
         mma(H, x, df);
         SD = mma(df, sf, SD);   // <D', S> is the sum of its diagonal
         __builtin_amdgcn_sched_barrier(0);
         // dR.V is the diagonal of dR V^T: the last waves' tiles (they have the
         // fewest other products)
         const int t = NW - 1 - w;
-        if (t < MT) RV = mma(read_frag<3>(smem + Z::oR, t, l >> 4), read_frag<NI>(smem + Z::oV, t, l >> 4), RV);
+        if (t < MT) RV = mma(read_frag<3>(smem + Z::oR, t, g), read_frag<NI>(smem + Z::oV, t, g), RV);
       }
-      // job: W1, W1 transposed, W2, W2 transposed; the fragment of its operand
 #pragma unroll
       for (int j = 0; j < Z::kJobs; ++j) {
-        const int job = w + j * NW, mat = job / Z::kTri, f = job % Z::kTri;
-        if (job < 4 * Z::kTri) {
-          const int rt = C == 32 ? f : (mat & 1) ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : (f >> 1) + 1);
-          const int st = C == 32 ? 0 : (mat & 1) ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
+        const Job<C> job(w + j * NW);
+        if (job.ours()) {
           // tiles of the products (accumulator rows): 2 st, 2 st + 1; the row tile: columns
-          if (mat == 0) {
-            const Frag<NI> c = read_frag<NI>(smem + Z::oY, rt, l >> 4);
-            Frag<3> p[2] = {read_frag<3>(smem + Z::oU, 2 * st, l >> 4), read_frag<3>(smem + Z::oU, 2 * st + 1, l >> 4)};
+          if (Z::all_w2(j) || (!Z::all_w1(j) && job.w2())) {
+            const unsigned char *s1 = smem + (job.mat == 2 ? Z::oU : Z::oR), *s2 = smem + (job.mat == 2 ? Z::oR : Z::oU);
+            const Frag<3> c = read_frag<3>(s2, job.rt, g);
+            Frag<3> p[2] = {read_frag<3>(s1, 2 * job.st, g), read_frag<3>(s1, 2 * job.st + 1, g)};
             mma(W[j], p, c);
-          } else if (mat == 1) {
-            const Frag<3> c = read_frag<3>(smem + Z::oU, rt, l >> 4);
-            Frag<NI> p[2] = {read_frag<NI>(smem + Z::oY, 2 * st, l >> 4), read_frag<NI>(smem + Z::oY, 2 * st + 1, l >> 4)};
+          } else if (job.mat == 0) {
+            const Frag<NI> c = read_frag<NI>(smem + Z::oY, job.rt, g);
+            Frag<3> p[2] = {read_frag<3>(smem + Z::oU, 2 * job.st, g), read_frag<3>(smem + Z::oU, 2 * job.st + 1, g)};
             mma(W[j], p, c);
           } else {
-            const unsigned char *s1 = smem + (mat == 2 ? Z::oU : Z::oR), *s2 = smem + (mat == 2 ? Z::oR : Z::oU);
-            const Frag<3> c = read_frag<3>(s2, rt, l >> 4);
-            Frag<3> p[2] = {read_frag<3>(s1, 2 * st, l >> 4), read_frag<3>(s1, 2 * st + 1, l >> 4)};
+            const Frag<3> c = read_frag<3>(smem + Z::oU, job.rt, g);
+            Frag<NI> p[2] = {read_frag<NI>(smem + Z::oY, 2 * job.st, g), read_frag<NI>(smem + Z::oY, 2 * job.st + 1, g)};
             mma(W[j], p, c);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-    }
+    } while (v0 < keep.dvp);
     __syncthreads();   // the last step is read
-    const int gg = here(g), mm = here(m);
 #pragma unroll
     for (int j = 0; j < Z::kJobs; ++j) {
-      const int job = w + j * NW, mat = job / Z::kTri, f = job % Z::kTri;
-      if (job < 4 * Z::kTri) {
-        const int rt = C == 32 ? f : (mat & 1) ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : (f >> 1) + 1);
-        const int st = C == 32 ? 0 : (mat & 1) ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1);
+      const Job<C> job(w + j * NW);
+      if (job.ours()) {
+        // element e: product p of the fragment, row q; rows i and j of M are q and
+        // p, or p and q in the transposed ones
+        const bool up = job.mat & 1;
+        const int gg = here(g), diff = up ? m - 4 * gg : 4 * gg - m, p0 = 32 * job.st, q0 = 16 * job.rt;
+        const int most = (job.mat == 0 || job.mat == 1 ? 0 : -1);   // p - q (up: q - p) at most
+        const double gq = s_g[q0 + m], sign = up ? -1.0 : 1.0;
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int p = 16 * (2 * st + (e >> 2)) + 4 * gg + (e & 3), q = 16 * rt + mm;
-          const int i = (mat & 1) ? p : q, jj = (mat & 1) ? q : p;
-          const float factor = mat < 2 ? a.scale : mat == 3 ? -s_b[i] : 1.0f;
-          const bool in = mat < 2 ? jj <= i : jj < i;
-          x[e] = in ? factor * decay_exp(s_g[i] - s_g[jj]) * W[j][e >> 2][e & 3] : 0.0f;
+          const int o = p0 + 16 * (e >> 2) + (e & 3);
+          const float f = decay_exp(sign * (gq - s_g[o + 4 * gg])) * W[j][e >> 2][e & 3];
+          x[e] = diff <= (up ? most + o - q0 : most - o + q0) ? f : 0.0f;
+        }
+        if (job.w2()) {
+          if (up) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= -s_b[p0 + 16 * (e >> 2) + 4 * gg + (e & 3)];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= a.scale;
         }
         const Frag<3> fr = to_frag<3>(x);
+        unsigned char* to = smem + (job.mat * Z::kTri + job.f) * 3 * kFrag + here(16 * l);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(smem + (job * 3 + p) * kFrag + l * 16) = fr.p[p];
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(to + p * kFrag) = fr.p[p];
       }
     }
+    const int gg = here(g), mm = here(m);
     if (NW - 1 - w < MT) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (4 * gg + r == mm) s_rv[16 * (NW - 1 - w) + mm] = RV[r];
     }
-    // k and q of this wave's features, as operands over the tokens; their slots
-    // are also the values at the accumulators' places
-    Frag<NI> kf[CS], qf[CS];
-    {
-      const unsigned char* fr = a.frags + static_cast<int64_t>(at.it) * Z::frags(true);
+    // <D', S> whole + sum of to k.(U D'^T): this lane's part
+    float ends = 0.0f;
 #pragma unroll
-      for (int s = 0; s < CS; ++s) {
-        kf[s] = read_cols<NI, C>(fr, w, s);
-        qf[s] = read_cols<NI, C>(fr + Z::kMat, w, s);
-      }
-    }
-    float sd = 0.0f, kh = 0.0f;   // <D', S> and the sum of to k.(U D'^T)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (4 * gg + r == mm) sd = SD[r];
+    for (int r = 0; r < 4; ++r) ends = 4 * gg + r == mm ? SD[r] : ends;
+    ends *= s_from[C - 1];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const float4 fr = *reinterpret_cast<const float4*>(s_from + 16 * t + 4 * gg);
@@ -597,7 +638,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         E[t][r] *= a.scale * ff[r];
         F[t][r] *= ff[r];
         H[t][r] *= tt[r];
-        kh = fmaf(value_of(kf[t >> 1], 4 * (t & 1) + r), H[t][r], kh);
+        ends = fmaf(value_of(kf[t >> 1], 4 * (t & 1) + r), H[t][r], ends);
       }
     }
     __syncthreads();   // W1 and W2 are there
@@ -629,20 +670,32 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     __builtin_amdgcn_sched_barrier(0);
     triangle(H, 3, kf);    // dKcol
     __builtin_amdgcn_sched_barrier(0);
+    {
+      // rows of dG and k.Hrow: this wave's features
+      float x[8 * MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < MT; ++t) {
+        const float4 be = *reinterpret_cast<const float4*>(s_b + 16 * t + 4 * gg);
+        const float bb[4] = {be.x, be.y, be.z, be.w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float kv = value_of(kf[t >> 1], 4 * (t & 1) + r), qv = value_of(qf[t >> 1], 4 * (t & 1) + r);
-        const int i = 16 * t + 4 * gg + r;
-        const float row = s_b[i] * F[t][r];
-        const float ga = row_sum(qv * E[t][r] - kv * (H[t][r] + row)), ka = row_sum(-kv * F[t][r]);
-        H[t][r] -= row;   // dK of the head
-        if (m == 0) {
-          s_red[2 * w * C + i] = ga;
-          s_red[(2 * w + 1) * C + i] = ka;
+        for (int r = 0; r < 4; ++r) {
+          const float kv = value_of(kf[t >> 1], 4 * (t & 1) + r), qv = value_of(qf[t >> 1], 4 * (t & 1) + r);
+          const float row = bb[r] * F[t][r];
+          x[4 * t + r] = qv * E[t][r] - kv * (H[t][r] + row);
+          x[4 * MT + 4 * t + r] = -kv * F[t][r];
+          H[t][r] -= row;   // dK of the head
         }
       }
+      ends += __shfl_xor(ends, 16);
+      ends += __shfl_xor(ends, 32);
+      x[4 * MT - 1] += gg == 3 ? ends : 0.0f;   // to the last token's dG
+      row_sums(x, mm);
+      // lane m has the sums from index m MT/2 on: of dG in the first eight lanes
+      float* to = s_red + (2 * w + (mm >> 3)) * C + 4 * gg;
+      const int i = (mm & 7) * (MT / 2);
+#pragma unroll
+      for (int j = 0; j < MT / 2; ++j) to[16 * (i >> 2) + (i & 3) + j] = x[j];
+    }
     // dq and dk of the heads that share a key: in LDS until the last one
     f32x4* sum = reinterpret_cast<f32x4*>(smem + Z::oAcc) + w * 2 * MT * 64 + here(l);
     if (at.hh > 0) {
@@ -659,41 +712,28 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         sum[(MT + t) * 64] = H[t];
       }
     } else {
-      const int c = 16 * w + m, ldo = a.Hk * a.Dk * es;
+      const int c = 16 * w + m, ldo = here_s(a.Hk * a.Dk * es);
       const Buf qo = rows_buf(static_cast<char*>(a.dq) + (tok * a.Hk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
       const Buf ko = rows_buf(static_cast<char*>(a.dk) + (tok * a.Hk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
       const int oo = here(c < a.Dk ? 4 * g * ldo + c * es : kNowhere);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          store_el<BF16>(qo, oo + (16 * t + r) * ldo, E[t][r]);
-          store_el<BF16>(ko, oo + (16 * t + r) * ldo, H[t][r]);
+        for (int r = 0; r < 4; r += 2) {
+          store_el2<BF16>(qo, oo + (16 * t + r) * ldo, ldo, E[t][r], E[t][r + 1]);
+          store_el2<BF16>(ko, oo + (16 * t + r) * ldo, ldo, H[t][r], H[t][r + 1]);
         }
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      sd += __shfl_xor(sd, o);
-      kh += __shfl_xor(kh, o);
-    }
-    if (l == 0) {
-      s_sum[w] = sd;
-      s_sum[NW + w] = kh;
     }
     __syncthreads();
     if (w == 0) {
-      float g1 = 0.0f, k1 = 0.0f, s1 = 0.0f, h1 = 0.0f;
+      float g1 = 0.0f, k1 = 0.0f;
       const int i = l < C ? l : 0;
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
         g1 += s_red[2 * x * C + i];
         k1 += s_red[(2 * x + 1) * C + i];
-        s1 += s_sum[x];
-        h1 += s_sum[NW + x];
       }
-      const float whole = expf(static_cast<float>(s_g[C - 1]));
       double dg = l < C ? g1 : 0.0f;
-      if (l == C - 1) dg += static_cast<double>(whole) * s1 + h1;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const double down = __shfl_down(dg, o);

@@ -195,6 +195,11 @@ __device__ __forceinline__ int here(int o) {
   return o;
 }
 
+__device__ __forceinline__ int here_s(int o) {
+  asm volatile("" : "+s"(o));
+  return o;
+}
+
 // four tokens `ld` bytes apart, the first at byte `o` (kNowhere: a block of
 // features that do not exist); nd of the eight features exist
 template <bool BF16>
