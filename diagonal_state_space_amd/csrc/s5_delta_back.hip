@@ -32,7 +32,7 @@ template <bool BF16, int KP>
 struct Back : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;
   static constexpr int kTri = tri_frags<Z::C>() * 3 * kFrag;
-  static constexpr int kBuf = 3 * Z::kMat + kFrag;
+  static constexpr int oV = 3 * Z::kMat + kFrag, kBuf = oV + (BF16 ? ValueStage::kBytes : 0);
   static constexpr bool kTwo = 2 * kBuf + 2 * kTri <= kMaxLds;
   static constexpr int oTri = (kTwo ? 2 : 1) * kBuf;
   static constexpr int kLds = oTri + 2 * kTri;
@@ -62,12 +62,15 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
 
   if (w >= NW) {   // the copying waves
     const int id = tid - 64 * NW;
-    const bool vec = vectored(a, BF16);
+    const bool vec = vectored(a, BF16), vecy = a.Dv % 8 == 0;
     Stage<BF16, KP, 64 * kCopy> k, q;
+    ValueStage y;
     auto record = [&](int n) { return a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true, 3); };
     auto load = [&](int n) {
       const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
       if constexpr (BF16) {
+        y.load(static_cast<const char*>(a.dy) + ((tok * a.Hv + h) * a.Dv + cg * 16 * NW) * es, a.Hv * a.Dv * es, min(len - n * C, C),
+               a.Dv - cg * 16 * NW, id, vecy);
         k.load(a, a.k, a.ldk, tok, min(len - n * C, C), hk, id, vec);
         q.load(a, a.q, a.ldq, tok, min(len - n * C, C), hk, id, vec);
       }
@@ -76,6 +79,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     auto copy = [&](int n) {
       unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
       if constexpr (BF16) {
+        y.store(dst + Z::oV, id);
         k.store(dst, dst + Z::kMat, id);
         q.store(nullptr, dst + 2 * Z::kMat, id);
       } else {
@@ -97,9 +101,9 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
       if constexpr (Z::kTwo) {
         barrier_copied();
         if (n > n0) copy(n - 1);
+        if (n - 1 > n0) load(n - 2);
         barrier_passed();   // T and P are read; the copies need not be there yet
         if (n > n0) copy_tri(n - 1);
-        if (n - 1 > n0) load(n - 2);
       } else {
         barrier_copied();
         copy(n);
@@ -127,11 +131,14 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     for (int t = 0; t < KT; ++t) asm volatile("" : "+v"(D[t]));   // waited for here, not in every chunk
   }
 
-  uint32_t ob[MT][4];
   const int ldy = a.Hv * a.Dv * es;
   const int yo = live ? 4 * g * ldy + col * es : kNowhere;
+  // whole 16-byte groups of bf16: lane l/2's row, its columns from 8 (l%2) on
+  const bool vecy = BF16 && a.Dv % 8 == 0;
+  const int vo = 16 * wg + 8 * (l & 1) < a.Dv ? (l >> 1) * ldy + (16 * wg + 8 * (l & 1)) * es : kNowhere;
   const unsigned char* s_tt = smem + Z::oTri;
   const unsigned char* s_pt = s_tt + Z::kTri;
+  uint32_t ob[MT][4];   // float32: the next chunk's dO
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     const int o = here(yo);
@@ -142,23 +149,24 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
       for (int r = 0; r < 4; ++r) ob[t][r] = load_raw<BF16>(yr, o + (16 * t + r) * ldy);
   };
 
-  if (n0 < n1) fetch(n1 - 1);
+  if (!BF16 && n0 < n1) fetch(n1 - 1);
   for (int n = n1 - 1; n >= n0; --n) {
     if constexpr (!Z::kTwo) barrier_read();   // the previous chunk is read
     barrier_read();                           // the chunk is there, the previous one read
-    f32x4 dO[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dO[t][r] = value<BF16>(ob[t][r]);
-    if (n > n0) fetch(n - 1);
-
-    const unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
+    unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
     const unsigned char *s_kt = s_k + Z::kMat, *s_qt = s_k + 2 * Z::kMat;
     const float* dec = reinterpret_cast<const float*>(s_k + 3 * Z::kMat);
-    f32x4 dU[MT], dR[MT];
+    f32x4 dO[MT], dU[MT], dR[MT];
+    Frag<NI> dy[CS];   // bf16: dO as it is
     Frag<NI> kx[2][MT];
     Frag<3> tf[2][MT];
+    if constexpr (!BF16) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dO[t][r] = value<BF16>(ob[t][r]);
+      if (n > n0) fetch(n - 1);
+    }
     if (wave_live) {
       if constexpr (!SUM) {
         const int o = here(16 * l);
@@ -184,6 +192,10 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
 #pragma unroll
           for (int t = 0; t < MT; ++t) to[t] = *reinterpret_cast<const float4*>(dec + C + 16 * t + 4 * g);
           read_tri<true, C>(tf[0], s_pt, 0);
+          if constexpr (BF16) {
+#pragma unroll
+            for (int s = 0; s < CS; ++s) dy[s] = read_cols<NI, C>(s_k + Z::oV, w, s);
+          }
         }
         stage_end();
         mma(dU, kx[ks & 1], to_frag<3>(D[2 * ks], D[2 * ks + 1]));
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
         if (i + 1 < 2 * CS) read_tri<true, C>(tf[(i + 1) & 1], i + 1 < CS ? s_pt : s_tt, (i + 1) % CS);
         stage_end();
         const int ks = i % CS;
-        if (i < CS) mma_tri<true, C>(dU, tf[i & 1], ks, to_frag<NI>(dO[2 * ks], dO[2 * ks + 1]));
+        if (i < CS) mma_tri<true, C>(dU, tf[i & 1], ks, BF16 ? dy[ks] : to_frag<NI>(dO[2 * ks], dO[2 * ks + 1]));
         else mma_tri<true, C>(dR, tf[i & 1], ks, to_frag<3>(dU[2 * ks], dU[2 * ks + 1]));
         stage_end();
       }
@@ -214,26 +226,37 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     auto read_c = [&](int i) { read_cols4<NI, C>(cf[i & 1], i < kGroups / 2 ? s_kt : s_qt, 4 * (i % (KT / 4)), i % (kGroups / 2) / (KT / 4)); };
     read_c(0);
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-    const int o1 = here(16 * l), o2 = here(yo);
+    const int o1 = here(16 * l);
     const Buf kr = rows_buf(keep.p + (static_cast<int64_t>(bh) * chunks + n) * keep.size(C) + keep.at_r(C) + 16 * wg * C, 1, 0, C * 64);
-    const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const float4 f = *reinterpret_cast<const float4*>(dec + 16 * t + 4 * g);
       const float4 be = *reinterpret_cast<const float4*>(dec + 2 * C + 16 * t + 4 * g);
-      const float4 fs = *reinterpret_cast<const float4*>(dec + 3 * C + 16 * t + 4 * g);
-      const float ff[4] = {f.x, f.y, f.z, f.w}, bb[4] = {be.x, be.y, be.z, be.w}, ss[4] = {fs.x, fs.y, fs.z, fs.w};
+      const float bb[4] = {be.x, be.y, be.z, be.w};
       if constexpr (!SUM) store16(kr, o1 + t * 1024, dR[t]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) dR[t][r] *= bb[r];
-      if constexpr (!SUM) {
+    }
+    if constexpr (!SUM) {
+      const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
+      if (vecy) {
+        store_values(s_k + Z::oV + w * ValueStage::kWave, vr, here(vo), ldy, dR);
+      } else {
+        const int o2 = here(yo);
 #pragma unroll
-        for (int r = 0; r < 4; r += 2) store_el2<BF16>(vr, o2 + (16 * t + r) * ldy, ldy, dR[t][r], dR[t][r + 1]);
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) store_el2<BF16>(vr, o2 + (16 * t + r) * ldy, ldy, dR[t][r], dR[t][r + 1]);
       }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const float4 f = *reinterpret_cast<const float4*>(dec + 16 * t + 4 * g);
+      const float4 fs = *reinterpret_cast<const float4*>(dec + 3 * C + 16 * t + 4 * g);
+      const float ff[4] = {f.x, f.y, f.z, f.w}, ss[4] = {fs.x, fs.y, fs.z, fs.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         dR[t][r] *= -ff[r];
-        dO[t][r] *= ss[r];
+        dO[t][r] = ss[r] * (BF16 ? element(dy[t >> 1], t & 1, r) : dO[t][r]);
       }
     }
     const float whole = dec[C - 1];

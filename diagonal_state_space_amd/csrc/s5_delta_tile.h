@@ -450,6 +450,52 @@ struct Stage {
   }
 };
 
+// The same for 64 columns of y's gradient in bf16, as fragments by columns: those
+// are the accumulators' order, and operands as they are. Loaded element by
+// element by the waves that need them, and v's gradient stored that way, the
+// backward chain of 64 heads of 2048 tokens took 187 us instead of 169; float32
+// in this way took longer (14 -> 21 us for 8 heads of 777 tokens): its chunks are
+// shorter than the loads take.
+struct ValueStage {
+  static constexpr int C = chunk_of<true>(), kWave = 32 * C, kBytes = 4 * kWave;
+  Block<true> b;
+
+  // rows [0, rows) of `ld` bytes from p, `dims` features from there on
+  __device__ __forceinline__ void load(const void* p, int ld, int rows, int dims, int id, bool vec) {
+    const int tg = id / 8, dg = id % 8;
+    b = load_block<true>(rows_buf(p, rows, ld, dims * 2), block_offset<true>(tg, dg, ld, id < 2 * C ? dims : 0), ld, dims - 8 * dg, vec);
+  }
+  __device__ __forceinline__ void store(unsigned char* dst, int id) const {
+    if (id < 2 * C) store_cols<true, C>(dst, Parts<true>(b), id / 8, id % 8);
+  }
+};
+
+// element of row 4 (l/16) + r of tile t (0, 1) of such a fragment
+template <int NP>
+__device__ __forceinline__ float element(const Frag<NP>& f, int t, int r) {
+  const uint32_t w = word(__builtin_bit_cast(uint4, f.p[0]), 2 * t + (r >> 1));
+  return __uint_as_float((r & 1) ? w & 0xffff0000u : w << 16);
+}
+
+// A wave's 16 columns of v's gradient through its 2 KB of the LDS to rows of `ld`
+// bytes in 16-byte groups (o: this lane's byte of row l/2).
+template <int MT>
+__device__ __forceinline__ void store_values(unsigned char* mine, Buf r, int o, int ld, const f32x4 (&x)[MT]) {
+  const int l = threadIdx.x & 63, g = l >> 4, m = l & 15;
+  unsigned char* p = mine + 4 * g * 32 + m * 2;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      unsigned char* q = p + (16 * t + i) * 32;
+      const uint32_t w = round2(x[t][i], x[t][i + 1]);
+      *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(w);
+      *reinterpret_cast<uint16_t*>(q + 32) = static_cast<uint16_t>(w >> 16);
+    }
+#pragma unroll
+  for (int j = 0; j < MT / 2; ++j) store16(r, o + j * 32 * ld, *reinterpret_cast<const f32x4*>(mine + j * 1024 + l * 16));
+}
+
 // whether whole 16-byte groups of k and q are aligned
 __device__ __forceinline__ bool vectored(const DeltaArgs& a, bool bf16) {
   const int V = bf16 ? 8 : 4;
