@@ -141,10 +141,18 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
 
   uint32_t vb[MT][4];
   const int ldv = static_cast<int>(a.ldv) * es, ldy = a.Hv * a.Dv * es;
+  // byte of the first of this lane's elements in rows of `ld` bytes: bf16's y pass
+  // has no register to keep it in, and one that is spilled is waited for with the
+  // stores
   const int vo = live ? 4 * g * ldv + col * es : kNowhere, yo = live ? 4 * g * ldy + col * es : kNowhere;
+  auto place = [&](int kept, int ld) {
+    if constexpr (!BF16 || !Y) return here(kept);
+    const int i = here(l), c = 16 * wg + (i & 15);
+    return c < a.Dv ? 4 * (i >> 4) * ld + c * es : kNowhere;
+  };
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
-    const int o = here(vo);
+    const int o = place(vo, ldv);
     const Buf vr = rows_buf(static_cast<const char*>(a.v) + (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es, min(len - n * C, C),
                             ldv, a.Dv * es);
 #pragma unroll
@@ -154,6 +162,16 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   };
 
   if (n0 < n1) fetch(n0);
+  if constexpr (Y && BF16) {
+    // Stores of nothing, as many as a chunk's of y: the compiler then counts that
+    // a chunk's v may be waited for without the stores of the chunk before, which
+    // were issued after its loads.
+    stage_end();
+    const Buf none = rows_buf(a.y, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) store_el2<BF16>(none, here(kNowhere), 4, 0.0f, 0.0f);
+    stage_end();
+  }
   for (int n = n0; n < n1; ++n) {
     if constexpr (!Z::kTwo) barrier_read();   // the previous chunk is read
     barrier_read();                           // the chunk is there, the previous one read
@@ -345,7 +363,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
               for (int r = 0; r < 4; ++r)
                 if (16 * t + 4 * g + r >= first) O[t][r] = kNaN;
           }
-          const int o = here(yo);
+          const int o = place(yo, ldy);
           const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
           for (int t = 0; t < MT; ++t)
