@@ -448,12 +448,12 @@ def _on(t, stream):
         raise ValueError(f"the tensors must be on a GPU device, got {t.device}")
     if stream is None and t.device.index == torch.cuda.current_device():
         return None
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
     import contextlib
     c = contextlib.ExitStack()
     c.enter_context(torch.cuda.device(t.device))
     if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
         c.enter_context(torch.cuda.stream(stream))
     return c
 

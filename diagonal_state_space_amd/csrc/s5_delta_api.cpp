@@ -53,9 +53,11 @@ s5_status delta_sizes(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, 
   constexpr int64_t kMost = int64_t{1} << 22;   // a chunk's rows stay below 2^30 bytes
   if (ldq > kMost || ldk > kMost || ldv > kMost || Hv * Dv > kMost || Hk * Dk > kMost) return S5_ERR_UNSUPPORTED;
   if (B > 0 && (L > INT32_MAX / B || Hv * Dv > INT32_MAX / B)) return S5_ERR_UNSUPPORTED;
-  // workgroups of 256 threads, one for each chunk of 32 or 64 steps and head
-  constexpr int64_t kGroups = (int64_t{1} << 24) - 1;
-  if (B > 0 && (Hv > kGroups / B / 16 || (L + 31) / 32 > kGroups / (B * Hv))) return S5_ERR_UNSUPPORTED;
+  // A launch has fewer than 2^32 threads: 256 for each chunk of 32 or 64 steps and
+  // head, and for each head up to 8 column groups of 512 (the chains) or 16 of 256
+  // (the single step)
+  constexpr int64_t kChunks = (int64_t{1} << 24) - 1, kHeads = (int64_t{1} << 19) - 1;
+  if (B > 0 && (Hv > kHeads / B || (L + 31) / 32 > kChunks / (B * Hv))) return S5_ERR_UNSUPPORTED;
   return S5_OK;
 }
 

@@ -388,17 +388,25 @@ s5_status s5_glu(int64_t T, int64_t H, s5_dtype io, int variant, const void* y, 
  * All other arrays contiguous and 16-byte aligned (g, beta, lengths: to their
  * element). The fields of the other direction are ignored. The current device
  * is the arrays'. Nothing is allocated: the calls can be captured in a graph.
- * Precision: the state, sums and decays are float32, products with float32
- * values as exact as float32 products (on the matrix cores as three bf16
- * parts), so for bf16 io only the outputs of type io are rounded to bf16.
+ * Precision: the state and sums are float32 (the sums of g float64), products
+ * with float32 values as exact as float32 products (on the matrix cores as
+ * three bf16 parts), so for bf16 io only the outputs of type io are rounded to
+ * bf16; what leads to y of bf16 io and nowhere else takes two parts (2^-16).
+ * A chunk's writes are solved for at once, with sums in the order of a
+ * triangular system's inverse: keys close to one another with beta near 2
+ * amplify roundings as they do token by token, by up to the chunk's length.
  * The result of a call does not depend on the launch order (no atomics).
+ * Values that are not finite: a key, decay, strength or (in its column) value
+ * makes NaN of y from its step on and of the last state, a query of its step's
+ * y; what comes before keeps its bits. The gradients of a sequence with one may
+ * be NaN throughout.
  * Errors: S5_ERR_INVALID_ARGUMENT (null pointer, wrong size field, negative
  * B or L, heads or features < 1, Hv not a multiple of Hk, a token stride below
  * the row, a scale that is not finite, workspace too small, an output
  * overlapping an input or another output), S5_ERR_UNSUPPORTED (io, feature
- * limits, a token stride or Hv*Dv above 2^22 elements, B*L or B*Hv*Dv above
- * INT32_MAX, B*Hv times the 32-step chunks of L above 2^24 - 1, misalignment),
- * S5_ERR_HIP.
+ * limits, a token stride, Hk*Dk or Hv*Dv above 2^22 elements, B*L or B*Hv*Dv
+ * above INT32_MAX, B*Hv above 2^19 - 1 or, times the 32-step chunks of L, above
+ * 2^24 - 1, misalignment), S5_ERR_HIP.
  */
 #define S5_DELTA_MAX_DK 128
 #define S5_DELTA_MAX_DV 512

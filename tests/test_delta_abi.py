@@ -37,6 +37,8 @@ COMMON = [
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(g=None), INVALID), (dict(beta=None), INVALID),
     (dict(q=at(0) + 1), UNSUPPORTED), (dict(s0=at(5) + 8), UNSUPPORTED), (dict(lengths=at(6) + 2), UNSUPPORTED),
     (dict(Hk=1 << 28, Hv=1 << 28, q_stride=1 << 40), UNSUPPORTED),
+    # 2^19 heads of all sequences: with the 8 column groups of 512 threads that Dv may have, half of a launch's 2^32 threads
+    (dict(B=1 << 17, L=1, workspace_bytes=1 << 40), UNSUPPORTED),
 ]
 
 
@@ -134,3 +136,21 @@ def test_tensors_off_the_gpu_are_refused():
         s5.gated_delta(q, q, q, q[..., 0], q[..., 0])
     with pytest.raises(ValueError):
         s5.gated_delta_step(q[:, 0], q[:, 0], q[:, 0], q[:, 0, :, 0], q[:, 0, :, 0], q)
+
+
+def test_stream_of_another_device_is_refused_first():
+    """A stream that is not of the tensors' device: refused before the current device is changed."""
+    import types
+
+    import torch
+    t = types.SimpleNamespace(device=torch.device("cuda", 0))
+    calls = []
+    real = torch.cuda.device
+    torch.cuda.device = lambda d: calls.append(d)
+    current, torch.cuda.current_device = torch.cuda.current_device, lambda: 0
+    try:
+        with pytest.raises(ValueError):
+            s5._on(t, types.SimpleNamespace(device=torch.device("cuda", 1)))
+    finally:
+        torch.cuda.device, torch.cuda.current_device = real, current
+    assert calls == []
