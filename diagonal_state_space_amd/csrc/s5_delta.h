@@ -76,7 +76,8 @@ struct DeltaKeep {
 // that run side by side: their states from a zero start, with the product of
 // their transitions, are found first and joined in order. Of every [B*Hv]
 // [segment]: [dkp][dvp + dkp] floats, the state from zero (after the join the
-// state at the segment's end) and the transition; backward also [dkp][dvp], the
+// state at the segment's end; of the last segment the sequence's start) and the
+// transition; backward also [dkp][dvp], the
 // gradient of the state at the segment's start.
 struct DeltaSegs {
   float *p, *back;

@@ -122,11 +122,12 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   f32x4 S[KT];
   {
     // the start: the call's, the end of the segment before, or (a segment's
-    // sums) zero and the identity
-    const bool first = seg == 0;
-    const int ld = (first ? a.Dv : segs.ld()) * 4;
-    const Buf p = first ? rows_buf(a.s0 + static_cast<int64_t>(bh) * a.Dk * a.Dv, a.s0 != nullptr ? a.Dk : 0, ld, ld)
-                        : rows_buf(segs.p + segs.at(bh, seg - 1), segs.dkp, ld, ld);
+    // sums) zero and the identity. Of several segments the first one's is the
+    // join's copy behind the others: the last segment may have overwritten s0.
+    const bool given = nc <= segs.chunks;
+    const int ld = (given ? a.Dv : segs.ld()) * 4;
+    const Buf p = given ? rows_buf(a.s0 + static_cast<int64_t>(bh) * a.Dk * a.Dv, a.s0 != nullptr ? a.Dk : 0, ld, ld)
+                        : rows_buf(segs.p + segs.at(bh, seg > 0 ? seg - 1 : segs.count - 1), segs.dkp, ld, ld);
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
 }
 
 // Joins the segments: with the states B and transitions M of their sums, the
-// state at the end of segment s is M_s S + B_s (forward, written over B_s), the
+// state at the end of segment s is M_s S + B_s (forward, written over B_s; the
+// start is copied to the last segment's place, which has no sums), the
 // gradient at its start M_s^T D + B_s (backward). A workgroup has 16 columns of
 // a head, a wave the row tiles w, w + 4; the next segment's M and B are on
 // their way while one is multiplied (float32 matrix instructions).
@@ -447,9 +449,12 @@ __global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, DeltaSegs segs,
     const int lds = BACK ? ldb : a.Dv * 4;
     const Buf p = BACK ? rows_buf(segs.back + segs.at_back(bh, last), segs.dkp, lds, lds)
                        : rows_buf(a.s0 + static_cast<int64_t>(bh) * a.Dk * a.Dv, a.s0 != nullptr ? a.Dk : 0, lds, lds);
+    const Buf copy = rows_buf(segs.p + segs.at(bh, segs.count - 1), segs.dkp, ld, ld);
     for (int i = tid; i < 16 * KT * 16; i += 256) {
       const int row = i >> 4, c = (blockIdx.x % tiles) * 16 + (i & 15);
-      s_x[row * LD + (i & 15)] = __uint_as_float(load_raw<false>(p, BACK || c < a.Dv ? row * lds + c * 4 : kNowhere));
+      const float x = __uint_as_float(load_raw<false>(p, BACK || c < a.Dv ? row * lds + c * 4 : kNowhere));
+      s_x[row * LD + (i & 15)] = x;
+      if constexpr (!BACK) store_el<false>(copy, row * ld + c * 4, x);
     }
   }
   for (int s = from; s != to; s += step) {

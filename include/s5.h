@@ -396,10 +396,10 @@ s5_status s5_glu(int64_t T, int64_t H, s5_dtype io, int variant, const void* y, 
  * triangular system's inverse: keys close to one another with beta near 2
  * amplify roundings as they do token by token, by up to the chunk's length.
  * The result of a call does not depend on the launch order (no atomics).
- * Values that are not finite: a key, decay, strength or (in its column) value
- * makes NaN of y from its step on and of the last state, a query of its step's
- * y; what comes before keeps its bits. The gradients of a sequence with one may
- * be NaN throughout.
+ * Values that are not finite: a key, decay (but -inf), strength or (in its
+ * column) value makes NaN of y from its step on and of the last state, a query
+ * of its step's y; what comes before keeps its bits. The gradients of a
+ * sequence with one may be NaN throughout.
  * Errors: S5_ERR_INVALID_ARGUMENT (null pointer, wrong size field, negative
  * B or L, heads or features < 1, Hv not a multiple of Hk, a token stride below
  * the row, a scale that is not finite, workspace too small, an output

@@ -200,6 +200,22 @@ def test_state_in_place_and_scale():
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_state_in_place_of_segments(io):
+    """The last segment writes the state that the first one starts from; one of
+    the sequences ends inside the first segment."""
+    import diagonal_state_space_amd as s5
+    x = delta_inputs(2, 2500, 1, 1, 100, 33, io, seed=11, decay=(1e-4, 1e-2))
+    d = to_gpu(x, io)
+    lengths = torch.tensor([2500, 70], dtype=torch.int32, device="cuda")
+    y, s = s5.gated_delta(**d, final_state=True, lengths=lengths)
+    keep = d["s0"].clone()
+    y2, s2 = s5.gated_delta(**{**d, "s0": keep}, s_last=keep, lengths=lengths)
+    assert s2 is keep and torch.equal(s2, s) and torch.equal(y2, y)
+    yr, sr = orc.gated_delta(**x, lengths=lengths.cpu().numpy())
+    check("state", s, sr, delta_bound(2500))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 1, 1, 1, 1), (3, 2, 4, 128, 128), (2, 1, 3, 100, 33), (5, 2, 2, 64, 96),
                                    (1, 4, 8, 17, 160), (130, 1, 2, 32, 512)], ids=lambda s: "x".join(map(str, s)))
 def test_step(shape, io):
