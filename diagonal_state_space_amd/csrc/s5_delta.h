@@ -55,8 +55,8 @@ struct DeltaArgs {
   float* ds0;              // or null
 };
 
-// one token after the other, the state in registers
-hipError_t launch_delta_tokens(const DeltaArgs& a, hipStream_t stream);
+// one token of each sequence, the state (s0 = s_last) in place
+hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
 
 // What the chains leave for the gradients of a chunk (float32, columns padded
 // with zeros to 16), one after the other for each of [B*Hv][chunks]: the state S
@@ -87,18 +87,14 @@ struct DeltaSegs {
   __host__ __device__ int64_t at_back(int64_t bh, int seg) const { return (bh * count + seg) * dkp * dvp; }
 };
 
-// the chunked form: preparation of all chunks, then the chunks in order (with
-// `keep` no outputs but S and U for the backward pass)
-// finds the workspace's parts and gives the bytes of fragments, records and segments
+// The chunked form: preparation of all chunks, then the chunks in order (with
+// `keep` no outputs but S and U for the backward pass). delta_work finds the
+// workspace's parts and gives the bytes of fragments, records and segments.
 int64_t delta_work(DeltaArgs& a, DeltaSegs& segs, bool backward);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep* keep, hipStream_t stream);
 // the gradients at the segments' starts from those of their sums
 hipError_t launch_delta_join_back(const DeltaArgs& a, const DeltaSegs& segs, hipStream_t stream);
-// finds the workspace's parts and gives the bytes of fragments, records and segments
-int64_t delta_work(DeltaArgs& a, DeltaSegs& segs, bool backward);
-hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
-hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaKeep* keep, hipStream_t stream);
 
 // whole sequences; bytes of workspace they need
 int64_t delta_workspace(const DeltaArgs& a, bool backward);

@@ -302,7 +302,7 @@ s5_status s5_gated_delta_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int
   a.s0 = s;
   a.y = y;
   a.s_last = s;
-  return s5::launch_delta_tokens(a, stream) == hipSuccess ? S5_OK : S5_ERR_HIP;
+  return s5::launch_delta_step(a, stream) == hipSuccess ? S5_OK : S5_ERR_HIP;
 }
 
 s5_status s5_qk_workspace(const s5_qk_desc* desc, int64_t* bytes) {

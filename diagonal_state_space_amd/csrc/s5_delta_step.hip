@@ -1,13 +1,15 @@
-// The gated delta rule token by token, the state in registers: a single token
-// for each sequence (the state read and written once).
+// One token of the gated delta rule for each sequence, the state in registers:
+// read once, written once.
 //
 //   Sd = a S,  u = beta (v - Sd^T k),  S <- Sd + k u^T,  y = scale S^T q
 // Both products with the old state come from one pass over it, since
 //   S_new^T q = a S^T q + (k.q) u.
 //
-// A workgroup holds kCols columns of one head's state: 32 column lanes of V
-// columns..., every thread the same columns of each kRows-th row, all loaded
-// before the first use. Columns are independent, so workgroups are as well.
+// The state's bytes bound it. A workgroup has 32 columns of one head's state, so
+// that a row's piece is a cache line of 128 bytes; each thread has four columns
+// of every 32nd row (four 16-byte loads, all under way before the first use),
+// or, where rows are not of whole 16-byte groups, one column of every 8th.
+// 128 sequences of 32 heads of 128 x 128 (537 MB): 104 us, 5.2 TB/s, as a copy.
 #include "s5_common.h"
 #include "s5_delta.h"
 
@@ -28,7 +30,7 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
 
 // V: columns of a thread, 4 with 16-byte rows of the state, else 1
 template <bool BF16, int V>
-__global__ void __launch_bounds__(kThreads) k_delta_tokens(DeltaArgs a) {
+__global__ void __launch_bounds__(kThreads) k_delta_step(DeltaArgs a) {
   constexpr int CL = kCols / V;              // column lanes
   constexpr int RG = kThreads / CL;          // rows side by side
   constexpr int NR = kMaxDk / RG;            // rows of a thread
@@ -43,11 +45,6 @@ __global__ void __launch_bounds__(kThreads) k_delta_tokens(DeltaArgs a) {
   const int hk = h / (a.Hv / a.Hk);
   const int col = ct * kCols + cl * V;
   const bool has = col < a.Dv;               // V = 4: Dv % 4 == 0, all or none
-  int len = a.L;
-  if (a.lengths) {
-    len = a.lengths[b];
-    len = len < 0 ? 0 : len > a.L ? a.L : len;
-  }
 
   const int64_t base = static_cast<int64_t>(bh) * a.Dk * a.Dv + col;
   float S[NR][V];
@@ -56,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_tokens(DeltaArgs a) {
     const int row = i * RG + rg;
 #pragma unroll
     for (int c = 0; c < V; ++c) S[i][c] = 0.0f;
-    if (a.s0 && has && row < a.Dk) {
+    if (has && row < a.Dk) {
       const float* p = a.s0 + base + static_cast<int64_t>(row) * a.Dv;
       if constexpr (V == 4) {
         const float4 r = *reinterpret_cast<const float4*>(p);
@@ -67,78 +64,74 @@ __global__ void __launch_bounds__(kThreads) k_delta_tokens(DeltaArgs a) {
     }
   }
 
-  for (int t = 0; t < len; ++t) {
-    const int64_t tok = static_cast<int64_t>(b) * a.L + t;
-    __syncthreads();                         // the previous token's k, q and sums are read
-    if (tid < kMaxDk) {
-      s_k[tid] = tid < a.Dk ? load1<BF16>(a.k, tok * a.ldk + static_cast<int64_t>(hk) * a.Dk + tid) : 0.0f;
-    } else if (tid < 2 * kMaxDk) {
-      const int j = tid - kMaxDk;
-      s_q[j] = j < a.Dk ? load1<BF16>(a.q, tok * a.ldq + static_cast<int64_t>(hk) * a.Dk + j) : 0.0f;
-    }
-    float v[V];
+  if (tid < kMaxDk) {
+    s_k[tid] = tid < a.Dk ? load1<BF16>(a.k, b * a.ldk + static_cast<int64_t>(hk) * a.Dk + tid) : 0.0f;
+  } else if (tid < 2 * kMaxDk) {
+    const int j = tid - kMaxDk;
+    s_q[j] = j < a.Dk ? load1<BF16>(a.q, b * a.ldq + static_cast<int64_t>(hk) * a.Dk + j) : 0.0f;
+  }
+  float v[V];
 #pragma unroll
-    for (int c = 0; c < V; ++c)
-      v[c] = has ? load1<BF16>(a.v, tok * a.ldv + static_cast<int64_t>(h) * a.Dv + col + c) : 0.0f;
-    const float decay = expf(a.g[tok * a.Hv + h]), beta = a.beta[tok * a.Hv + h];
-    __syncthreads();
-    float kk[NR], pk[V], pq[V], kq = 0.0f;
+  for (int c = 0; c < V; ++c)
+    v[c] = has ? load1<BF16>(a.v, b * a.ldv + static_cast<int64_t>(h) * a.Dv + col + c) : 0.0f;
+  const float decay = expf(a.g[b * a.Hv + h]), beta = a.beta[b * a.Hv + h];
+  __syncthreads();
+  float kk[NR], pk[V], pq[V], kq = 0.0f;
 #pragma unroll
-    for (int c = 0; c < V; ++c) pk[c] = pq[c] = 0.0f;
+  for (int c = 0; c < V; ++c) pk[c] = pq[c] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      kk[i] = s_k[i * RG + rg];
-      const float qq = s_q[i * RG + rg];
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        pk[c] = fmaf(S[i][c], kk[i], pk[c]);
-        pq[c] = fmaf(S[i][c], qq, pq[c]);
-      }
-    }
-    for (int j = tid & 63; j < kMaxDk; j += 64) kq = fmaf(s_k[j], s_q[j], kq);
-    for (int o = 1; o < 64; o <<= 1) kq += __shfl_xor(kq, o);
-#pragma unroll
-    for (int o = CL; o < 64; o <<= 1)
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        pk[c] += __shfl_xor(pk[c], o);
-        pq[c] += __shfl_xor(pq[c], o);
-      }
-    if ((tid & 63) < CL) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        s_red[wave][0][cl * V + c] = pk[c];
-        s_red[wave][1][cl * V + c] = pq[c];
-      }
-    }
-    __syncthreads();
-    float u[V], y[V];
+  for (int i = 0; i < NR; ++i) {
+    kk[i] = s_k[i * RG + rg];
+    const float qq = s_q[i * RG + rg];
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      float sk = 0.0f, sq = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        sk += s_red[w][0][cl * V + c];
-        sq += s_red[w][1][cl * V + c];
-      }
-      u[c] = beta * (v[c] - decay * sk);
-      y[c] = a.scale * fmaf(kq, u[c], decay * sq);
+      pk[c] = fmaf(S[i][c], kk[i], pk[c]);
+      pq[c] = fmaf(S[i][c], qq, pq[c]);
     }
+  }
+  for (int j = tid & 63; j < kMaxDk; j += 64) kq = fmaf(s_k[j], s_q[j], kq);
+  for (int o = 1; o < 64; o <<= 1) kq += __shfl_xor(kq, o);
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
+  for (int o = CL; o < 64; o <<= 1)
 #pragma unroll
-      for (int c = 0; c < V; ++c) S[i][c] = fmaf(kk[i], u[c], decay * S[i][c]);
-    if (rg == 0 && has) {
-      const int64_t o = (tok * a.Hv + h) * a.Dv + col;
+    for (int c = 0; c < V; ++c) {
+      pk[c] += __shfl_xor(pk[c], o);
+      pq[c] += __shfl_xor(pq[c], o);
+    }
+  if ((tid & 63) < CL) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        if constexpr (BF16) static_cast<uint16_t*>(a.y)[o + c] = f32_to_bf16(y[c]);
-        else static_cast<float*>(a.y)[o + c] = y[c];
-      }
+    for (int c = 0; c < V; ++c) {
+      s_red[wave][0][cl * V + c] = pk[c];
+      s_red[wave][1][cl * V + c] = pq[c];
+    }
+  }
+  __syncthreads();
+  float u[V], y[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) {
+    float sk = 0.0f, sq = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      sk += s_red[w][0][cl * V + c];
+      sq += s_red[w][1][cl * V + c];
+    }
+    u[c] = beta * (v[c] - decay * sk);
+    y[c] = a.scale * fmaf(kq, u[c], decay * sq);
+  }
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int c = 0; c < V; ++c) S[i][c] = fmaf(kk[i], u[c], decay * S[i][c]);
+  if (rg == 0 && has) {
+    const int64_t o = static_cast<int64_t>(bh) * a.Dv + col;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      if constexpr (BF16) static_cast<uint16_t*>(a.y)[o + c] = f32_to_bf16(y[c]);
+      else static_cast<float*>(a.y)[o + c] = y[c];
     }
   }
 
-  if (a.s_last && has) {
+  if (has) {
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const int row = i * RG + rg;
@@ -153,16 +146,16 @@ __global__ void __launch_bounds__(kThreads) k_delta_tokens(DeltaArgs a) {
 
 }  // namespace
 
-hipError_t launch_delta_tokens(const DeltaArgs& a, hipStream_t stream) {
+hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream) {
   const int64_t blocks = static_cast<int64_t>(a.B) * a.Hv * ((a.Dv + kCols - 1) / kCols);
   const bool vec = a.Dv % 4 == 0;   // the states are 16-byte aligned
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   if (a.bf16_io) {
-    if (vec) k_delta_tokens<true, 4><<<grid, block, 0, stream>>>(a);
-    else k_delta_tokens<true, 1><<<grid, block, 0, stream>>>(a);
+    if (vec) k_delta_step<true, 4><<<grid, block, 0, stream>>>(a);
+    else k_delta_step<true, 1><<<grid, block, 0, stream>>>(a);
   } else {
-    if (vec) k_delta_tokens<false, 4><<<grid, block, 0, stream>>>(a);
-    else k_delta_tokens<false, 1><<<grid, block, 0, stream>>>(a);
+    if (vec) k_delta_step<false, 4><<<grid, block, 0, stream>>>(a);
+    else k_delta_step<false, 1><<<grid, block, 0, stream>>>(a);
   }
   return hipGetLastError();
 }
