@@ -93,6 +93,7 @@ struct DeltaSegs {
 int64_t delta_work(DeltaArgs& a, DeltaSegs& segs, bool backward);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep* keep, hipStream_t stream);
+bool narrow_groups(const DeltaArgs& a, const DeltaSegs& segs);
 // the gradients at the segments' starts from those of their sums
 hipError_t launch_delta_join_back(const DeltaArgs& a, const DeltaSegs& segs, hipStream_t stream);
 

@@ -28,11 +28,11 @@ namespace {
 // LDS of a chunk: fragments of k (by rows, by columns) and q (by columns) and
 // the decays, two of them where they fit (more waves copy them); the transposed T and P, which the
 // next chunk's replace as soon as they are read.
-template <bool BF16, int KP>
+template <bool BF16, int KP, int NW>
 struct Back : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;
   static constexpr int kTri = tri_frags<Z::C>() * 3 * kFrag;
-  static constexpr int oV = 3 * Z::kMat + kFrag, kBuf = oV + (BF16 ? ValueStage::kBytes : 0);
+  static constexpr int oV = 3 * Z::kMat + kFrag, kBuf = oV + (BF16 ? ValueStage<NW>::kBytes : 0);
   static constexpr bool kTwo = 2 * kBuf + 2 * kTri <= kMaxLds;
   static constexpr int oTri = (kTwo ? 2 : 1) * kBuf;
   static constexpr int kLds = oTri + 2 * kTri;
@@ -42,7 +42,7 @@ struct Back : Shape<BF16, KP> {
 // segment's from ds_last)
 template <bool BF16, int KP, int NW, bool SUM>
 __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs a, int chunks, int groups, DeltaSegs segs, DeltaKeep keep) {
-  using Z = Back<BF16, KP>;
+  using Z = Back<BF16, KP, NW>;
   constexpr int C = Z::C, NI = Z::NI, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     const int id = tid - 64 * NW;
     const bool vec = vectored(a, BF16), vecy = a.Dv % 8 == 0;
     Stage<BF16, KP, 64 * kCopy> k, q;
-    ValueStage y;
+    ValueStage<NW> y;
     auto record = [&](int n) { return a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true, 3); };
     auto load = [&](int n) {
       const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     if constexpr (!SUM) {
       const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
       if (vecy) {
-        store_values(s_k + Z::oV + w * ValueStage::kWave, vr, here(vo), ldy, dR);
+        store_values(s_k + Z::oV + w * ValueStage<NW>::kWave, vr, here(vo), ldy, dR);
       } else {
         const int o2 = here(yo);
 #pragma unroll
@@ -783,50 +783,54 @@ int64_t keep_of(DeltaArgs& a, DeltaSegs& segs, DeltaKeep& k) {
   return head + chunks * k.size(C) * 4;
 }
 
+// the chain's passes, for all segments or for their sums
+template <bool BF16, int KP, int NW, bool SUM>
+hipError_t chain(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep, hipStream_t stream) {
+  using Z = Back<BF16, KP, NW>;
+  auto* kern = k_delta_back_scan<BF16, KP, NW, SUM>;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
+  if (attr != hipSuccess) return attr;
+  const int chunks = (a.L + Z::C - 1) / Z::C, groups = (a.Dv + 16 * NW - 1) / (16 * NW);
+  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups * (SUM ? segs.count - 1 : segs.count);
+  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
+  return hipGetLastError();
+}
+
+template <bool BF16, int KP, bool VEC>
+hipError_t grad(const DeltaArgs& a, const DeltaKeep& keep, hipStream_t stream) {
+  using G = Grad<BF16, KP>;
+  auto* kern = k_delta_grad<BF16, KP, VEC>;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds);
+  if (attr != hipSuccess) return attr;
+  const int chunks = (a.L + G::C - 1) / G::C;
+  // one workgroup at a time fits a compute unit (KP = 64: two)
+  const int64_t items = static_cast<int64_t>(a.B) * a.Hk * chunks, most = KP == 64 ? 512 : 256;
+  kern<<<dim3(static_cast<unsigned>(items < most ? items : most)), dim3(G::kThreads), G::kLds - (a.Hv == a.Hk ? G::kAcc : 0), stream>>>(a, chunks, keep);
+  return hipGetLastError();
+}
+
 template <bool BF16, int KP>
 hipError_t run(DeltaArgs a, hipStream_t stream) {
-  constexpr int NW = 4, C = chunk_of<BF16>();
-  using Z = Back<BF16, KP>;
-  using G = Grad<BF16, KP>;
-  auto* scan = k_delta_back_scan<BF16, KP, NW, false>;
-  auto* sum = k_delta_back_scan<BF16, KP, NW, true>;
-  auto* grad_vec = k_delta_grad<BF16, KP, true>;
-  auto* grad_one = k_delta_grad<BF16, KP, false>;
-  static const hipError_t attr[4] = {
-      hipFuncSetAttribute(reinterpret_cast<const void*>(scan), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(sum), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(grad_vec), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds),
-      hipFuncSetAttribute(reinterpret_cast<const void*>(grad_one), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds)};
-  for (hipError_t e : attr)
-    if (e != hipSuccess) return e;
-  const int chunks = (a.L + C - 1) / C;
-  const int groups = (a.Dv + 16 * NW - 1) / (16 * NW);
   DeltaKeep keep{};
   DeltaSegs segs{};
   keep_of(a, segs, keep);
-  if (a.L > 0) {
-    hipError_t e = launch_delta_prep(a, true, stream);
-    if (e == hipSuccess) e = launch_delta_scan(a, segs, &keep, stream);
-    if (e != hipSuccess) return e;
-  }
-  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups;
   hipError_t e = hipSuccess;
-  if (segs.count > 1) {
-    sum<<<dim3(static_cast<unsigned>(blocks * (segs.count - 1))), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
-    e = hipGetLastError();
-    if (e == hipSuccess) e = launch_delta_join_back(a, segs, stream);
-    if (e != hipSuccess) return e;
+  if (a.L > 0) {
+    e = launch_delta_prep(a, true, stream);
+    if (e == hipSuccess) e = launch_delta_scan(a, segs, &keep, stream);
   }
-  scan<<<dim3(static_cast<unsigned>(blocks * segs.count)), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
-  e = hipGetLastError();
+  if (e == hipSuccess && segs.count > 1) {
+    e = narrow_groups(a, segs) ? chain<BF16, KP, 2, true>(a, segs, keep, stream) : chain<BF16, KP, 4, true>(a, segs, keep, stream);
+    if (e == hipSuccess) e = launch_delta_join_back(a, segs, stream);
+  }
+  if (e == hipSuccess) e = narrow_groups(a, segs) ? chain<BF16, KP, 2, false>(a, segs, keep, stream) : chain<BF16, KP, 4, false>(a, segs, keep, stream);
   if (e != hipSuccess || a.L == 0) return e;
   // dy is contiguous and 16-byte aligned
   constexpr int V = BF16 ? 8 : 4;
-  auto* grad = a.Dv % V == 0 && a.ldv % V == 0 && (reinterpret_cast<uintptr_t>(a.v) & 15u) == 0 ? grad_vec : grad_one;
-  // one workgroup at a time fits a compute unit (KP = 64: two)
-  const int64_t items = static_cast<int64_t>(a.B) * a.Hk * chunks, most = KP == 64 ? 512 : 256;
-  grad<<<dim3(static_cast<unsigned>(items < most ? items : most)), dim3(G::kThreads), G::kLds - (a.Hv == a.Hk ? G::kAcc : 0), stream>>>(a, chunks, keep);
-  return hipGetLastError();
+  const bool vec = a.Dv % V == 0 && a.ldv % V == 0 && (reinterpret_cast<uintptr_t>(a.v) & 15u) == 0;
+  return vec ? grad<BF16, KP, true>(a, keep, stream) : grad<BF16, KP, false>(a, keep, stream);
 }
 
 }  // namespace

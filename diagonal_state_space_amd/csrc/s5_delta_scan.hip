@@ -487,9 +487,8 @@ __global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, DeltaSegs segs,
   }
 }
 
-template <bool BF16, int KP, Pass PASS>
+template <bool BF16, int KP, int NW, Pass PASS>
 hipError_t run(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep, hipStream_t stream) {
-  constexpr int NW = 4;
   using Z = Scan<BF16, KP, PASS>;
   constexpr bool SUM = PASS == kSum || PASS == kSumBack;
   auto* kern = k_delta_scan<BF16, KP, NW, PASS>;
@@ -505,8 +504,12 @@ hipError_t run(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep,
 
 template <Pass PASS>
 hipError_t dispatch(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep, hipStream_t stream) {
-  if (a.bf16_io) return a.Dk > 64 ? run<true, 128, PASS>(a, segs, keep, stream) : run<true, 64, PASS>(a, segs, keep, stream);
-  return a.Dk > 64 ? run<false, 128, PASS>(a, segs, keep, stream) : run<false, 64, PASS>(a, segs, keep, stream);
+  if (narrow_groups(a, segs)) {
+    if (a.bf16_io) return a.Dk > 64 ? run<true, 128, 2, PASS>(a, segs, keep, stream) : run<true, 64, 2, PASS>(a, segs, keep, stream);
+    return a.Dk > 64 ? run<false, 128, 2, PASS>(a, segs, keep, stream) : run<false, 64, 2, PASS>(a, segs, keep, stream);
+  }
+  if (a.bf16_io) return a.Dk > 64 ? run<true, 128, 4, PASS>(a, segs, keep, stream) : run<true, 64, 4, PASS>(a, segs, keep, stream);
+  return a.Dk > 64 ? run<false, 128, 4, PASS>(a, segs, keep, stream) : run<false, 64, 4, PASS>(a, segs, keep, stream);
 }
 
 template <bool BACK>
@@ -519,6 +522,10 @@ hipError_t join(const DeltaArgs& a, const DeltaSegs& segs, hipStream_t stream) {
 }
 
 }  // namespace
+
+bool narrow_groups(const DeltaArgs& a, const DeltaSegs& segs) {
+  return static_cast<int64_t>(a.B) * a.Hv * segs.count * ((segs.dvp + 31) / 32) <= 256;
+}
 
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep* keep, hipStream_t stream) {
   const DeltaKeep none{};

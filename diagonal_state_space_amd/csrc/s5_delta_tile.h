@@ -450,23 +450,24 @@ struct Stage {
   }
 };
 
-// The same for 64 columns of y's gradient in bf16, as fragments by columns: those
+// The same for 16 NW columns of y's gradient in bf16, as fragments by columns: those
 // are the accumulators' order, and operands as they are. Loaded element by
 // element by the waves that need them, and v's gradient stored that way, the
 // backward chain of 64 heads of 2048 tokens took 187 us instead of 169; float32
 // in this way took longer (14 -> 21 us for 8 heads of 777 tokens): its chunks are
 // shorter than the loads take.
+template <int NW>
 struct ValueStage {
-  static constexpr int C = chunk_of<true>(), kWave = 32 * C, kBytes = 4 * kWave;
+  static constexpr int C = chunk_of<true>(), kWave = 32 * C, kBytes = NW * kWave, kBlocks = C / 4 * 2 * NW;
   Block<true> b;
 
   // rows [0, rows) of `ld` bytes from p, `dims` features from there on
   __device__ __forceinline__ void load(const void* p, int ld, int rows, int dims, int id, bool vec) {
-    const int tg = id / 8, dg = id % 8;
-    b = load_block<true>(rows_buf(p, rows, ld, dims * 2), block_offset<true>(tg, dg, ld, id < 2 * C ? dims : 0), ld, dims - 8 * dg, vec);
+    const int tg = id / (2 * NW), dg = id % (2 * NW);
+    b = load_block<true>(rows_buf(p, rows, ld, dims * 2), block_offset<true>(tg, dg, ld, id < kBlocks ? dims : 0), ld, dims - 8 * dg, vec);
   }
   __device__ __forceinline__ void store(unsigned char* dst, int id) const {
-    if (id < 2 * C) store_cols<true, C>(dst, Parts<true>(b), id / 8, id % 8);
+    if (id < kBlocks) store_cols<true, C>(dst, Parts<true>(b), id / (2 * NW), id % (2 * NW));
   }
 };
 
