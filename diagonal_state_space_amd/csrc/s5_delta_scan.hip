@@ -410,7 +410,9 @@ __global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, DeltaSegs segs,
   __shared__ float s_x[16 * KT * LD];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tiles = segs.dvp / 16, bh = blockIdx.x / tiles, col = (blockIdx.x % tiles) * 16 + m;
+  // a head's workgroups on one die: they read the same transitions
+  const int tiles = segs.dvp / 16, turn = blockIdx.x >> 3, bh = turn / tiles * 8 + (blockIdx.x & 7), col0 = turn % tiles * 16, col = col0 + m;
+  if (bh >= a.B * a.Hv) return;
   const int nc = (length_of(a, bh / a.Hv) + C - 1) / C;
   const int last = nc > 0 ? (nc - 1) / segs.chunks : 0;   // the last segment there is
   const int ld = segs.ld() * 4, ldb = BACK ? segs.dvp * 4 : ld;
@@ -418,9 +420,11 @@ __global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, DeltaSegs segs,
   const int from = BACK ? last - 1 : 0, to = BACK ? 0 : last, step = BACK ? -1 : 1;
   if (BACK ? from <= to : from >= to) return;
 
-  float4 A[DT][KT];
-  float B[DT][4];
-  auto fetch = [&](int s) {
+  struct Segment {
+    float4 A[DT][KT];
+    float B[DT][4];
+  };
+  auto fetch = [&](Segment& x, int s) {
     const Buf mat = rows_buf(segs.p + segs.at(bh, s), segs.dkp, ld, ld);
     const Buf vec = BACK ? rows_buf(segs.back + segs.at_back(bh, s), segs.dkp, ldb, ldb) : mat;
 #pragma unroll
@@ -431,49 +435,57 @@ __global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, DeltaSegs segs,
         const bool in = 16 * t < segs.dkp && 16 * k < segs.dkp;
         if constexpr (BACK) {
           const int o = (16 * k + 4 * g) * ld + (segs.dvp + 16 * t + m) * 4;
-          A[d][k] = float4{__uint_as_float(load_raw<false>(mat, in ? o : kNowhere)), __uint_as_float(load_raw<false>(mat, in ? o + ld : kNowhere)),
-                           __uint_as_float(load_raw<false>(mat, in ? o + 2 * ld : kNowhere)), __uint_as_float(load_raw<false>(mat, in ? o + 3 * ld : kNowhere))};
+          x.A[d][k] = float4{__uint_as_float(load_raw<false>(mat, in ? o : kNowhere)), __uint_as_float(load_raw<false>(mat, in ? o + ld : kNowhere)),
+                             __uint_as_float(load_raw<false>(mat, in ? o + 2 * ld : kNowhere)), __uint_as_float(load_raw<false>(mat, in ? o + 3 * ld : kNowhere))};
         } else {
           const uint4 v = load16(mat, in ? (16 * t + m) * ld + (segs.dvp + 16 * k + 4 * g) * 4 : kNowhere);
-          A[d][k] = float4{__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+          x.A[d][k] = float4{__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) B[d][r] = __uint_as_float(load_raw<false>(vec, (16 * t + 4 * g + r) * ldb + col * 4));
+      for (int r = 0; r < 4; ++r) x.B[d][r] = __uint_as_float(load_raw<false>(vec, (16 * t + 4 * g + r) * ldb + col * 4));
     }
   };
 
-  fetch(from);
+  Segment even, odd;
+  fetch(even, from);
+  if (from + step != to) fetch(odd, from + step);
   {
     // the first segment's start (backward: the gradient that its sums ended with)
     const int lds = BACK ? ldb : a.Dv * 4;
     const Buf p = BACK ? rows_buf(segs.back + segs.at_back(bh, last), segs.dkp, lds, lds)
                        : rows_buf(a.s0 + static_cast<int64_t>(bh) * a.Dk * a.Dv, a.s0 != nullptr ? a.Dk : 0, lds, lds);
     const Buf copy = rows_buf(segs.p + segs.at(bh, segs.count - 1), segs.dkp, ld, ld);
-    for (int i = tid; i < 16 * KT * 16; i += 256) {
-      const int row = i >> 4, c = (blockIdx.x % tiles) * 16 + (i & 15);
-      const float x = __uint_as_float(load_raw<false>(p, BACK || c < a.Dv ? row * lds + c * 4 : kNowhere));
-      s_x[row * LD + (i & 15)] = x;
-      if constexpr (!BACK) store_el<false>(copy, row * ld + c * 4, x);
+    const int c0 = col0 + (tid & 15);
+    float x[KT];   // all under way before the first is waited for
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+      x[i] = __uint_as_float(load_raw<false>(p, BACK || c0 < a.Dv ? (16 * i + (tid >> 4)) * lds + c0 * 4 : kNowhere));
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      const int row = 16 * i + (tid >> 4);
+      s_x[row * LD + (tid & 15)] = x[i];
+      if constexpr (!BACK) store_el<false>(copy, row * ld + c0 * 4, x[i]);
     }
   }
-  for (int s = from; s != to; s += step) {
+  auto join = [&](Segment& x, int s) {
     __syncthreads();
     f32x4 acc[DT];
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[d][r] = B[d][r];
+      for (int r = 0; r < 4; ++r) acc[d][r] = x.B[d][r];
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        const float* x = s_x + (16 * k + 4 * g) * LD + m;
-        acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[d][k].x, x[0], acc[d], 0, 0, 0);
-        acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[d][k].y, x[LD], acc[d], 0, 0, 0);
-        acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[d][k].z, x[2 * LD], acc[d], 0, 0, 0);
-        acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[d][k].w, x[3 * LD], acc[d], 0, 0, 0);
-      }
+    for (int k = 0; k < KT; ++k) {
+      const float* v = s_x + (16 * k + 4 * g) * LD + m;
+      const float vv[4] = {v[0], v[LD], v[2 * LD], v[3 * LD]};
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          acc[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(r == 0 ? x.A[d][k].x : r == 1 ? x.A[d][k].y : r == 2 ? x.A[d][k].z : x.A[d][k].w, vv[r], acc[d], 0, 0, 0);
     }
-    if (s + step != to) fetch(s + step);
+    if ((to - s) * step > 2) fetch(x, s + 2 * step);
     __syncthreads();
     const Buf out = BACK ? rows_buf(segs.back + segs.at_back(bh, s), segs.dkp, ldb, ldb) : rows_buf(segs.p + segs.at(bh, s), segs.dkp, ld, ld);
 #pragma unroll
@@ -484,6 +496,13 @@ __global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, DeltaSegs segs,
         s_x[row * LD + m] = acc[d][r];
         store_el<false>(out, row * ldb + col * 4, acc[d][r]);
       }
+  };
+  for (int s = from; s != to;) {
+    join(even, s);
+    s += step;
+    if (s == to) break;
+    join(odd, s);
+    s += step;
   }
 }
 
@@ -514,7 +533,7 @@ hipError_t dispatch(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& 
 
 template <bool BACK>
 hipError_t join(const DeltaArgs& a, const DeltaSegs& segs, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (segs.dvp / 16)));
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * (segs.dvp / 16)));
   const int C = a.bf16_io ? chunk_of<true>() : chunk_of<false>();
   if (a.Dk > 64) k_delta_join<8, BACK><<<grid, dim3(256), 0, stream>>>(a, segs, C);
   else k_delta_join<4, BACK><<<grid, dim3(256), 0, stream>>>(a, segs, C);
