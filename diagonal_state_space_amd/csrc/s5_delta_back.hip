@@ -47,9 +47,9 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int die = blockIdx.x & 7, turn = blockIdx.x >> 3;
   const int count = SUM ? segs.count - 1 : segs.count;   // sums: segments 1, 2, ...
-  const int cg = turn % groups, seg = (turn / groups) % count + (SUM ? 1 : 0), bh = turn / (groups * count) * 8 + die;
+  const int turn = blockIdx.x >> 3, cg = turn % groups, unit = turn / groups * 8 + (blockIdx.x & 7);
+  const int bh = unit / count, seg = unit - bh * count + (SUM ? 1 : 0);
   if (bh >= a.B * a.Hv) return;
   const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / (a.Hv / a.Hk);
   const int wg = cg * NW + w, col = wg * 16 + m;
@@ -792,7 +792,7 @@ hipError_t chain(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& kee
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
   if (attr != hipSuccess) return attr;
   const int chunks = (a.L + Z::C - 1) / Z::C, groups = (a.Dv + 16 * NW - 1) / (16 * NW);
-  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups * (SUM ? segs.count - 1 : segs.count);
+  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv * (SUM ? segs.count - 1 : segs.count) + 7) / 8 * 8 * groups;
   kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
   return hipGetLastError();
 }
@@ -816,16 +816,17 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   DeltaKeep keep{};
   DeltaSegs segs{};
   keep_of(a, segs, keep);
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
   hipError_t e = hipSuccess;
   if (a.L > 0) {
     e = launch_delta_prep(a, true, stream);
     if (e == hipSuccess) e = launch_delta_scan(a, segs, &keep, stream);
   }
   if (e == hipSuccess && segs.count > 1) {
-    e = narrow_groups(a, segs) ? chain<BF16, KP, 2, true>(a, segs, keep, stream) : chain<BF16, KP, 4, true>(a, segs, keep, stream);
+    e = narrow_groups(heads * (segs.count - 1), a.Dv) ? chain<BF16, KP, 2, true>(a, segs, keep, stream) : chain<BF16, KP, 4, true>(a, segs, keep, stream);
     if (e == hipSuccess) e = launch_delta_join_back(a, segs, stream);
   }
-  if (e == hipSuccess) e = narrow_groups(a, segs) ? chain<BF16, KP, 2, false>(a, segs, keep, stream) : chain<BF16, KP, 4, false>(a, segs, keep, stream);
+  if (e == hipSuccess) e = narrow_groups(heads * segs.count, a.Dv) ? chain<BF16, KP, 2, false>(a, segs, keep, stream) : chain<BF16, KP, 4, false>(a, segs, keep, stream);
   if (e != hipSuccess || a.L == 0) return e;
   // dy is contiguous and 16-byte aligned
   constexpr int V = BF16 ? 8 : 4;

@@ -56,11 +56,11 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // workgroups go round the eight dies one by one: the column groups of a head
-  // follow each other on one die, whose L2 then holds what they share
-  const int die = blockIdx.x & 7, turn = blockIdx.x >> 3;
+  // workgroups go round the eight dies one by one: the column groups of a
+  // segment follow each other on one die, whose L2 then holds what they share
   const int count = SUM ? segs.count - 1 : segs.count;
-  const int cg = turn % groups, seg = (turn / groups) % count, bh = turn / (groups * count) * 8 + die;
+  const int turn = blockIdx.x >> 3, cg = turn % groups, unit = turn / groups * 8 + (blockIdx.x & 7);
+  const int bh = unit / count, seg = unit - bh * count;
   if (bh >= a.B * a.Hv) return;
   const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / (a.Hv / a.Hk);
   const int wg = cg * NW + w, col = wg * 16 + m;
@@ -516,14 +516,15 @@ hipError_t run(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep,
   if (attr != hipSuccess) return attr;
   const int chunks = (a.L + Z::C - 1) / Z::C;
   const int groups = ((SUM ? segs.ld() : a.Dv) + 16 * NW - 1) / (16 * NW);
-  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv + 7) / 8 * 8 * groups * (SUM ? segs.count - 1 : segs.count);
+  const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv * (SUM ? segs.count - 1 : segs.count) + 7) / 8 * 8 * groups;
   kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
   return hipGetLastError();
 }
 
 template <Pass PASS>
 hipError_t dispatch(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep, hipStream_t stream) {
-  if (narrow_groups(a, segs)) {
+  constexpr bool SUM = PASS == kSum || PASS == kSumBack;
+  if (narrow_groups(static_cast<int64_t>(a.B) * a.Hv * (SUM ? segs.count - 1 : segs.count), SUM ? segs.ld() : segs.dvp)) {
     if (a.bf16_io) return a.Dk > 64 ? run<true, 128, 2, PASS>(a, segs, keep, stream) : run<true, 64, 2, PASS>(a, segs, keep, stream);
     return a.Dk > 64 ? run<false, 128, 2, PASS>(a, segs, keep, stream) : run<false, 64, 2, PASS>(a, segs, keep, stream);
   }
@@ -541,10 +542,6 @@ hipError_t join(const DeltaArgs& a, const DeltaSegs& segs, hipStream_t stream) {
 }
 
 }  // namespace
-
-bool narrow_groups(const DeltaArgs& a, const DeltaSegs& segs) {
-  return static_cast<int64_t>(a.B) * a.Hv * segs.count * ((segs.dvp + 31) / 32) <= 256;
-}
 
 hipError_t launch_delta_scan(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep* keep, hipStream_t stream) {
   const DeltaKeep none{};
