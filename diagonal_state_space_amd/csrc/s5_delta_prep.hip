@@ -312,21 +312,31 @@ namespace {
 
 // Segments of a call: none where the chain's workgroups (64 columns of a head
 // each) fill half of the compute units or the sequence is short; otherwise as
-// many as the estimate below favours. Microseconds of one chunk, measured with
-// one workgroup on a compute unit at 128 x 128 bf16 (see the scan kernel): a pass
-// for the states 3.1, with outputs 3.9, a segment's join 1.5.
-int segments_of(int64_t heads, int groups, int sum_groups, int chunks) {
-  constexpr double kSum = 3.1, kOut = 3.9, kJoin = 1.5, kUnits = 256.0;
-  if (heads * groups >= 128 || chunks < 16) return 1;
-  auto rounds = [&](double wgs) { return wgs <= kUnits ? 1.0 : wgs / kUnits; };
-  double best = chunks * kOut;
+// many as the estimate below favours, in microseconds as measured (128 or 64
+// features of a key): a chunk's pass for outputs and for a segment's sums with a
+// workgroup on few units (with one on each they take 1.35 times as long), a
+// segment's join. Over 160 calls (1 to 48 heads of 1024 to 8192 steps, 64 and 128
+// features, both types) its choice took 0.6 % longer than the best of eleven
+// numbers on average and 13 % at most; one head of 8192 steps, 128 x 128, bf16:
+// 384 us in one piece, 107 in 16.
+int segments_of(int64_t heads, int dvp, int dkp, int chunks, bool bf16) {
+  const bool wide = dkp > 64;
+  const double out = bf16 ? (wide ? 2.8 : 2.2) : (wide ? 3.1 : 1.5), sum = bf16 ? (wide ? 2.1 : 1.65) : (wide ? 1.6 : 1.1);
+  const double join = wide ? 2.5 : 0.45;
+  constexpr double kStart = 2.0;   // a workgroup's first loads
+  if (heads * ((dvp + 63) / 64) >= kUnits / 2 || chunks < 16) return 1;
+  auto rounds = [](int64_t chains, int columns) {
+    const int64_t wgs = chains * (narrow_groups(chains, columns) ? (columns + 31) / 32 : (columns + 63) / 64);
+    const int64_t whole = (wgs + kUnits - 1) / kUnits;
+    return static_cast<double>(whole) * (1.0 + 0.35 * static_cast<double>(wgs < kUnits ? wgs : kUnits) / kUnits);
+  };
+  double best = chunks * out * rounds(heads, dvp);
   int count = 1;
-  for (int n = 3; n <= 32 && n * 4 <= chunks; ++n) {
+  for (int n = 2; n <= 32 && n * 2 <= chunks; ++n) {
     const int each = (chunks + n - 1) / n;
     if ((chunks + each - 1) / each != n) continue;
-    const double t = each * kSum * rounds(static_cast<double>(heads) * sum_groups * (n - 1)) +
-                     each * kOut * rounds(static_cast<double>(heads) * groups * n) + n * kJoin + 8.0;
-    if (t < 0.9 * best) {
+    const double t = (each * sum + kStart) * rounds(heads * (n - 1), dvp + dkp) + (each * out + kStart) * rounds(heads * n, dvp) + n * join;
+    if (t < (count == 1 ? 0.95 : 1.0) * best) {
       best = t;
       count = n;
     }
@@ -345,7 +355,7 @@ int64_t work(DeltaArgs& a, DeltaSegs& segs, bool backward) {
   a.recs = a.frags + frags;
   segs.dkp = (a.Dk + 15) & ~15;
   segs.dvp = (a.Dv + 15) & ~15;
-  segs.count = segments_of(heads, (segs.dvp + 63) / 64, (segs.dvp + segs.dkp + 63) / 64, chunks);
+  segs.count = segments_of(heads, segs.dvp, segs.dkp, chunks, BF16);
   segs.chunks = segs.count > 1 ? (chunks + segs.count - 1) / segs.count : chunks;
   segs.p = reinterpret_cast<float*>(a.recs + recs);
   const int64_t states = segs.count > 1 ? segs.at(heads, 0) : 0;
