@@ -17,6 +17,12 @@
 //           end state: whole <D', S> + sum to k.(U D'^T);  dg = sums of dG from the end
 // (M< is M without its diagonal; . are dot products of a token's rows.) Every
 // term of dG is a row of a product that is there anyway.
+//
+// What bounds them (128 x 128 bf16, 64 value heads of 2048 steps): the chain as the
+// forward one, 158 us; the rest, 189 us, by its instructions and phases (one
+// workgroup on a compute unit: vector instructions 34 % of the cycles, matrix
+// instructions 28 %) next to the 540 MB of states, writes and their gradients
+// that it reads (2.9 TB/s).
 #include "s5_delta_tile.h"
 
 namespace s5 {

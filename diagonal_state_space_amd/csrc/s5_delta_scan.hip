@@ -9,10 +9,17 @@
 // Every result is the next product's operand as it lies in the accumulators
 // (the fragments' product order is that of two tiles), so the chain runs
 // without an exchange or a barrier. What the waves share - k, its transpose,
-// q, T and P of the chunk - is staged in LDS once for the workgroup, fetched
-// into registers one chunk ahead.
+// q, T and P of the chunk - is staged in LDS once for the workgroup, by waves
+// that do nothing else, a chunk ahead.
 // The state's chain is exact to float32 (three bf16 parts); what only reaches
 // y of bf16 io takes two parts.
+//
+// What bounds it: the chain itself, with one wave on a SIMD (the LDS has room for
+// one workgroup on a compute unit). Of 7550 cycles for a chunk of 64 steps (128 x
+// 128 bf16, outputs) matrix instructions take 3500 and vector instructions, four
+// cycles each and most of them splits into parts, 2900; neither can start
+// before the other's results. 64 heads of 2048 steps: outputs 110 us, states and
+// U for the gradients 91; 128 heads: 117.
 //
 // A value that is not finite must not reach earlier steps through a zero of T
 // or P: rows from the first such one on are taken out of R for this column and
