@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
   auto all_kept = [](int j) { return (j + 1) * NW <= kFirstIo; };
   auto all_io = [](int j) { return j * NW >= kFirstIo; };
   Eight es_, ed, et[Z::kItems];
-  float gn = 0.0f, bn = 0.0f;    // the first wave's: g and beta
+  float gn = 0.0f, bn = 0.0f;    // the first two waves': g and beta
   const int lane_kept = g * 256 + (m & 7) * 32, lane_s = lane_kept + (m >> 3) * keep.dkp * 64, lane_r = lane_kept + (m >> 3) * C * 64;
   auto fetch = [&](const Place& p, int v0) {
     const int h = p.hk * group + p.hh;
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       if (all_kept(j) || (!all_io(j) && t < kFirstIo)) et[j] = load_kept(t < MT ? keep.at_r(C) : keep.at_u(), C, t % MT, lane_r);
       else et[j] = load_io(t >= kFirstIo + MT, t % MT);
     }
-    if (v0 == 0 && w == 0) {
+    if (v0 == 0 && w < 2) {
       const bool in = l < C && l < p.left;
       gn = in ? a.g[(tok + l) * a.Hv + h] : 0.0f;
       bn = in ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
@@ -514,7 +514,20 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
 
   Place at{static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x), group - 1, 0, 0, 0, 0};
   if (!advance(at)) return;
+  // sums of g and the decays that come from them: the second wave's, while the
+  // first one finishes the head before
+  auto decays = [&] {
+    const double s = chunk_sums(gn);
+    const double end = __shfl(s, C - 1);
+    if (l < C) {
+      s_g[l] = s;
+      s_b[l] = bn;
+      s_from[l] = expf(static_cast<float>(s));
+      s_to[l] = expf(static_cast<float>(end - s));
+    }
+  };
   fetch(at, 0);
+  if (w == 1) decays();
   for (bool more = true; more;) {
     const int h = at.hk * group + at.hh, left = at.left, rows = min(left, C);
     const int64_t tok = static_cast<int64_t>(at.b) * a.L + at.n * C;
@@ -525,24 +538,12 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     for (int t = 0; t < MT; ++t) E[t] = F[t] = H[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < Z::kJobs; ++j) W[j][0] = W[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    __syncthreads();     // the previous head's sums and decays are read
-    if (w == 0) {
-      const double s = chunk_sums(gn);
-      const double end = __shfl(s, C - 1);
-      if (l < C) {
-        s_g[l] = s;
-        s_b[l] = bn;
-        s_from[l] = expf(static_cast<float>(s));
-        s_to[l] = expf(static_cast<float>(end - s));
-      }
-    }
     // k and q of this wave's features, as operands over the tokens; their slots
     // are also the values at the accumulators' places
     Frag<NI> kf[CS], qf[CS];
     int v0 = 0;
 #pragma clang loop unroll(disable)
-    do {
-      __syncthreads();   // the previous step is read
+    while (true) {
       {
         store_kept(smem + Z::oS + w * 3 * kFrag, here(kept_at), es_.lo, es_.hi);
         store_kept(smem + Z::oD + w * 3 * kFrag, here(kept_at), ed.lo, ed.hi);
@@ -612,8 +613,9 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-    } while (v0 < keep.dvp);
-    __syncthreads();   // the last step is read
+      __syncthreads();   // the step is read
+      if (v0 >= keep.dvp) break;
+    }
 #pragma unroll
     for (int j = 0; j < Z::kJobs; ++j) {
       const Job<C> job(w + j * NW);
@@ -753,7 +755,8 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
           store_el2<BF16>(ko, oo + (16 * t + r) * ldo, ldo, H[t][r], H[t][r + 1]);
         }
     }
-    __syncthreads();
+    __syncthreads();   // the sums are there, the fragments and decays read
+    if (w == 1 && more) decays();
     if (w == 0) {
       float g1 = 0.0f, k1 = 0.0f;
       const int i = l < C ? l : 0;
@@ -762,12 +765,9 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
         g1 += s_red[2 * x * C + i];
         k1 += s_red[(2 * x + 1) * C + i];
       }
-      double dg = l < C ? g1 : 0.0f;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double down = __shfl_down(dg, o);
-        if (l + o < 64) dg += down;
-      }
+      // sums from the end: the lanes the other way round
+      const int r = C - 1 - l;
+      const double sums = lane_sums(l < C ? __shfl(g1, r & 63) : 0.0f), dg = __shfl(sums, r & 63);
       if (l < C && l < left) {
         // a decay that clears the state hides what it multiplied
         a.dg[(tok + l) * a.Hv + h] = gi < kLeastDecay ? 0.0f : static_cast<float>(dg);

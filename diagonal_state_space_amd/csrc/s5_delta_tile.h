@@ -542,18 +542,28 @@ __device__ __forceinline__ void barrier_read() {
 // it in the place of -inf, without -inf - (-inf)
 constexpr float kLeastDecay = -110.0f;
 
-// inclusive sums of g over a wave's lanes (one chunk), float64: their
-// differences stay exact to float32 however fast a head forgets
-__device__ __forceinline__ double chunk_sums(float g) {
-  const int l = threadIdx.x & 63;
-  double s = g < kLeastDecay ? kLeastDecay : g;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double up = __shfl_up(s, o);
-    if (l >= o) s += up;
-  }
+// inclusive sums over a wave's lanes: within rows of 16, then the last lane of
+// a row to the next one and of the first half to the second
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lane_before(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);   // 0 where there is none
+}
+__device__ __forceinline__ double lane_sums(double s) {
+  s += lane_before<0x111, 0xf>(s);   // row_shr 1, 2, 4, 8
+  s += lane_before<0x112, 0xf>(s);
+  s += lane_before<0x114, 0xf>(s);
+  s += lane_before<0x118, 0xf>(s);
+  s += lane_before<0x142, 0xa>(s);   // row_bcast 15, 31
+  s += lane_before<0x143, 0xc>(s);
   return s;
 }
+
+// inclusive sums of g over a wave's lanes (one chunk), float64: their
+// differences stay exact to float32 however fast a head forgets
+__device__ __forceinline__ double chunk_sums(float g) { return lane_sums(g < kLeastDecay ? kLeastDecay : g); }
 
 // e^x for the factors M_ij <= 1 of products: the hardware's exponential of
 // x log2(e), off by up to (1 + |x|) 2^-24 of e^x and so by less than 2^-23 of
