@@ -299,12 +299,13 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
 }
 
 // ---- the gradients without a chain ------------------------------------------------
-// One wave per 16 features of a key. The products over the value features run
-// in steps of 32: S, D', U, dR and dY are split into parts and put into row
-// fragments in LDS once for the workgroup, the next step's loads on their way
-// meanwhile; each wave has its features' rows of E = dY S^T, F = dR S^T and
-// H = U D'^T for all tokens, and a share of the C x C products W1 = dY U^T and
-// W2 = dR U^T. These are computed both ways round, since a product comes out
+// One wave per 32 features of a key and half of the chunk's tokens (16 features
+// and all tokens read more of the LDS, which bounds the products: 185 -> XXX us).
+// The products over the value features run in steps of 32: S, D', U, dR and dY
+// are split into parts and put into row fragments in LDS once for the
+// workgroup, the next step's loads on their way meanwhile; each wave has its
+// part of E = dY S^T, F = dR S^T and H = U D'^T, and a share of the C x C
+// products W1 = dY U^T and W2 = dR U^T. These are computed both ways round, since a product comes out
 // with the rows of its first factor where an operand has its products: the
 // result masked, decayed and split is an operand's fragment as it lies. Then
 // the products over tokens go on in E, F and H.
@@ -323,9 +324,11 @@ struct Grad : Shape<BF16, KP> {
   static constexpr int kW = 4 * kTri * 3 * kFrag;           // over the stage when that is read
   static constexpr int oG = kStage > kW ? kStage : kW;      // double sums of g
   static constexpr int oB = oG + Z::C * 8;                  // beta, from, to
-  static constexpr int oRed = oB + 3 * Z::C * 4;            // [NW][2][C] row sums
-  static constexpr int oRV = oRed + NW * 2 * Z::C * 4;      // [C] dR.V
-  static constexpr int oAcc = oRV + Z::C * 4;               // [NW][2 MT][64] dq and dk, where heads share a key
+  static constexpr int TT = Z::MT / 2;                      // token tiles of a wave
+  static constexpr int oRed = oB + 3 * Z::C * 4;            // [NW / 2][2][C] row sums
+  static constexpr int oRV = oRed + NW * Z::C * 4;          // [C] dR.V
+  static constexpr int oEnd = oRV + Z::C * 4;               // [NW] the waves' parts of the last token's dG
+  static constexpr int oAcc = oEnd + NW * 4;                // [NW][2 MT][64] dq and dk, where heads share a key
   static constexpr int kAcc = NW * 2 * Z::MT * kFrag, kLds = oAcc + kAcc;
 };
 
@@ -418,13 +421,14 @@ struct Job {
 template <bool BF16, int KP, bool VEC>
 __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunks, DeltaKeep keep) {
   using Z = Grad<BF16, KP>;
-  constexpr int C = Z::C, MT = Z::MT, CS = Z::CS, NI = Z::NI, NW = Z::NW, es = Z::es;
+  constexpr int C = Z::C, MT = Z::MT, CS = Z::CS, NI = Z::NI, NW = Z::NW, TT = Z::TT, es = Z::es;
   extern __shared__ __align__(16) unsigned char smem[];
   double* s_g = reinterpret_cast<double*>(smem + Z::oG);
   float *s_b = reinterpret_cast<float*>(smem + Z::oB), *s_from = s_b + C, *s_to = s_from + C;
-  float *s_red = reinterpret_cast<float*>(smem + Z::oRed), *s_rv = reinterpret_cast<float*>(smem + Z::oRV);
+  float *s_red = reinterpret_cast<float*>(smem + Z::oRed), *s_rv = reinterpret_cast<float*>(smem + Z::oRV), *s_end = reinterpret_cast<float*>(smem + Z::oEnd);
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int f0 = w & ~1, th = w & 1, t0 = th * TT;   // feature tiles f0, f0 + 1, token tiles from t0 on
   const int group = a.Hv / a.Hk, items = a.B * a.Hk * chunks;
 
   auto value_of = [&](const Frag<NI>& f, int e) {
@@ -533,14 +537,13 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     const int64_t tok = static_cast<int64_t>(at.b) * a.L + at.n * C;
     const float gi = gn;
 
-    f32x4 E[MT], F[MT], H[MT], W[Z::kJobs][2], RV = {0.0f, 0.0f, 0.0f, 0.0f}, SD = RV;
+    f32x4 E[2][TT], F[2][TT], H[2][TT], W[Z::kJobs][2], RV = {0.0f, 0.0f, 0.0f, 0.0f}, SD = RV;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) E[t] = F[t] = H[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) E[f][t] = F[f][t] = H[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < Z::kJobs; ++j) W[j][0] = W[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // k and q of this wave's features, as operands over the tokens; their slots
-    // are also the values at the accumulators' places
-    Frag<NI> kf[CS], qf[CS];
     int v0 = 0;
 #pragma clang loop unroll(disable)
     while (true) {
@@ -556,40 +559,39 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
       __syncthreads();
       v0 += 32;
-      if (v0 < keep.dvp) {
-        fetch(at, v0);
-      } else {
-        const unsigned char* fr = a.frags + static_cast<int64_t>(at.it) * Z::frags(true);
-#pragma unroll
-        for (int s = 0; s < CS; ++s) {
-          kf[s] = read_cols<NI, C>(fr, w, s);
-          qf[s] = read_cols<NI, C>(fr + Z::kMat, w, s);
-        }
-      }
+      if (v0 < keep.dvp) fetch(at, v0);
       {
-        const Frag<3> sf = read_frag<3>(smem + Z::oS, w, g);
+        const Frag<3> sf[2] = {read_frag<3>(smem + Z::oS, f0, g), read_frag<3>(smem + Z::oS, f0 + 1, g)};
         {
-          Frag<NI> y[MT];
+          Frag<NI> y[TT];
 #pragma unroll
-          for (int t = 0; t < MT; ++t) y[t] = read_frag<NI>(smem + Z::oY, t, g);
-          mma(E, y, sf);
+          for (int t = 0; t < TT; ++t) y[t] = read_frag<NI>(smem + Z::oY, t0 + t, g);
+          mma(E[0], y, sf[0]);
+          mma(E[1], y, sf[1]);
         }
         __builtin_amdgcn_sched_barrier(0);   // one product's fragments at a time: more would spill
-        Frag<3> x[MT];
+        Frag<3> x[TT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oR, t, g);
-        mma(F, x, sf);
+        for (int t = 0; t < TT; ++t) x[t] = read_frag<3>(smem + Z::oR, t0 + t, g);
+        mma(F[0], x, sf[0]);
+        mma(F[1], x, sf[1]);
+        // dR.V is the diagonal of dR V^T: tile t0 + r of it by the r-th last wave of
+        // this half (they have the fewest other products)
+        const int r = (NW - 2 - f0) / 2;
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          if (t == r) RV = mma(x[t], read_frag<NI>(smem + Z::oV, t0 + t, g), RV);
+        __builtin_amdgcn_sched_barrier(0);
+        const Frag<3> df[2] = {read_frag<3>(smem + Z::oD, f0, g), read_frag<3>(smem + Z::oD, f0 + 1, g)};
+        // <D', S> is the sum of the diagonal of D' S^T
+        if (th == 0) SD = mma(df[0], sf[0], SD);
+        else SD = mma(df[1], sf[1], SD);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) x[t] = read_frag<3>(smem + Z::oU, t, g);
-        const Frag<3> df = read_frag<3>(smem + Z::oD, w, g);
-        mma(H, x, df);
-        SD = mma(df, sf, SD);   // <D', S> is the sum of its diagonal
+        for (int t = 0; t < TT; ++t) x[t] = read_frag<3>(smem + Z::oU, t0 + t, g);
+        mma(H[0], x, df[0]);
+        mma(H[1], x, df[1]);
         __builtin_amdgcn_sched_barrier(0);
-        // dR.V is the diagonal of dR V^T: the last waves' tiles (they have the
-        // fewest other products)
-        const int t = NW - 1 - w;
-        if (t < MT) RV = mma(read_frag<3>(smem + Z::oR, t, g), read_frag<NI>(smem + Z::oV, t, g), RV);
       }
 #pragma unroll
       for (int j = 0; j < Z::kJobs; ++j) {
@@ -616,6 +618,20 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       __syncthreads();   // the step is read
       if (v0 >= keep.dvp) break;
     }
+    // k and q of this wave's features, as operands over the tokens; their slots
+    // are also the values at the accumulators' places
+    Frag<NI> kf[2][CS], qf[2][CS];
+    {
+      const unsigned char* fr = a.frags + static_cast<int64_t>(at.it) * Z::frags(true);
+#pragma unroll
+      for (int s = 0; s < CS; ++s)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          kf[f][s] = read_cols<NI, C>(fr, f0 + f, s);
+          qf[f][s] = read_cols<NI, C>(fr + Z::kMat, f0 + f, s);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);   // under way while W1 and W2 are finished
 #pragma unroll
     for (int j = 0; j < Z::kJobs; ++j) {
       const Job<C> job(w + j * NW);
@@ -649,48 +665,66 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
     }
     const int gg = here(g), mm = here(m);
-    if (NW - 1 - w < MT) {
+    if ((NW - 2 - f0) / 2 < TT) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (4 * gg + r == mm) s_rv[16 * (NW - 1 - w) + mm] = RV[r];
+        if (4 * gg + r == mm) s_rv[16 * (t0 + (NW - 2 - f0) / 2) + mm] = RV[r];
     }
     // <D', S> whole + sum of to k.(U D'^T): this lane's part
     float ends = 0.0f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) ends = 4 * gg + r == mm ? SD[r] : ends;
     ends *= s_from[C - 1];
+    // this wave's tokens among the products of its fragments: one of two, or a half
+    // of one
+    auto own = [&](const Frag<NI> (&x)[CS]) {
+      Frag<NI> y;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const float4 fr = *reinterpret_cast<const float4*>(s_from + 16 * t + 4 * gg);
-      const float4 to = *reinterpret_cast<const float4*>(s_to + 16 * t + 4 * gg);
+      for (int p = 0; p < NI; ++p) {
+        const uint4 u = __builtin_bit_cast(uint4, x[0].p[p]), z = __builtin_bit_cast(uint4, x[CS - 1].p[p]);
+        y.p[p] = __builtin_bit_cast(bf16x8, CS == 2 ? uint4{th == 0 ? u.x : z.x, th == 0 ? u.y : z.y, th == 0 ? u.z : z.z, th == 0 ? u.w : z.w}
+                                                    : uint4{th == 0 ? u.x : u.z, th == 0 ? u.y : u.w, 0, 0});
+      }
+      return y;
+    };
+    const Frag<NI> kown[2] = {own(kf[0]), own(kf[1])};
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float4 fr = *reinterpret_cast<const float4*>(s_from + 16 * (t0 + t) + 4 * gg);
+      const float4 to = *reinterpret_cast<const float4*>(s_to + 16 * (t0 + t) + 4 * gg);
       const float ff[4] = {fr.x, fr.y, fr.z, fr.w}, tt[4] = {to.x, to.y, to.z, to.w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        E[t][r] *= a.scale * ff[r];
-        F[t][r] *= ff[r];
-        H[t][r] *= tt[r];
-        ends = fmaf(value_of(kf[t >> 1], 4 * (t & 1) + r), H[t][r], ends);
-      }
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          E[f][t][r] *= a.scale * ff[r];
+          F[f][t][r] *= ff[r];
+          H[f][t][r] *= tt[r];
+          ends = fmaf(value_of(kown[f], 4 * t + r), H[f][t][r], ends);
+        }
     }
     __syncthreads();   // W1 and W2 are there
     Place next = at;
     more = advance(next);
     if (more) fetch(next, 0);
-    auto triangle = [&](f32x4 (&c)[MT], int mat, const Frag<NI> (&x)[CS]) {
+    // the wave's row tiles of a C x C matrix times k or q over all tokens
+    auto triangle = [&](f32x4 (&c)[2][TT], int mat, const Frag<NI> (&x)[2][CS]) {
 #pragma unroll
       for (int s = 0; s < CS; ++s) {
-        Frag<3> f[MT];
+        if (CS == 2 && ((mat & 1) ? th > s : th < s)) continue;   // zeros
+        Frag<3> f[TT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-          if ((mat & 1) ? t <= 2 * s + 1 : t >= 2 * s)
-            f[t] = read_frag<3>(smem, mat * Z::kTri + ((mat & 1) ? tri_frag_t<C>(t, s) : tri_frag<C>(t, s)), 0);
+        for (int t = 0; t < TT; ++t)
+          f[t] = read_frag<3>(smem, mat * Z::kTri + ((mat & 1) ? tri_frag_t<C>(t0 + t, s) : tri_frag<C>(t0 + t, s)), 0);
 #pragma unroll
         for (int i = 0; i < 3; ++i)
 #pragma unroll
           for (int j = 0; j < NI && i + j < 3; ++j)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-              if ((mat & 1) ? t <= 2 * s + 1 : t >= 2 * s) c[t] = mfma(f[t].p[i], x[s].p[j], c[t]);
+            for (int t = 0; t < TT; ++t) {
+              c[0][t] = mfma(f[t].p[i], x[0][s].p[j], c[0][t]);
+              c[1][t] = mfma(f[t].p[i], x[1][s].p[j], c[1][t]);
+            }
       }
     };
     triangle(E, 0, kf);    // dQ
@@ -703,68 +737,98 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     __builtin_amdgcn_sched_barrier(0);
     {
       // rows of dG and k.Hrow: this wave's features
-      float x[8 * MT];
+      const Frag<NI> qown[2] = {own(qf[0]), own(qf[1])};
+      float x[8 * TT];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const float4 be = *reinterpret_cast<const float4*>(s_b + 16 * t + 4 * gg);
+      for (int t = 0; t < TT; ++t) {
+        const float4 be = *reinterpret_cast<const float4*>(s_b + 16 * (t0 + t) + 4 * gg);
         const float bb[4] = {be.x, be.y, be.z, be.w};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float kv = value_of(kf[t >> 1], 4 * (t & 1) + r), qv = value_of(qf[t >> 1], 4 * (t & 1) + r);
-          const float row = bb[r] * F[t][r];
-          x[4 * t + r] = qv * E[t][r] - kv * (H[t][r] + row);
-          x[4 * MT + 4 * t + r] = -kv * F[t][r];
-          H[t][r] -= row;   // dK of the head
+          float dg = 0.0f, hk = 0.0f;
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const float kv = value_of(kown[f], 4 * t + r), qv = value_of(qown[f], 4 * t + r);
+            const float row = bb[r] * F[f][t][r];
+            dg += qv * E[f][t][r] - kv * (H[f][t][r] + row);
+            hk -= kv * F[f][t][r];
+            H[f][t][r] -= row;   // dK of the head
+          }
+          x[4 * t + r] = dg;
+          x[4 * TT + 4 * t + r] = hk;
         }
       }
+      float* to = s_red + f0 * C + 16 * t0 + 4 * gg;
+      if constexpr (TT == 2) {
+        row_sums(x, mm);   // lane m has sum m: of dG in the first eight lanes
+        to[(mm >> 3) * C + 16 * ((mm >> 2) & 1) + (mm & 3)] = x[0];
+      } else {
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = x[i];
+          y[8 + i] = 0.0f;
+        }
+        row_sums(y, mm);
+        if (mm < 8) to[(mm >> 2) * C + (mm & 3)] = y[0];
+      }
+      ends += from_lane<0x128>(ends);   // row_ror 8, 4, 2, 1
+      ends += from_lane<0x124>(ends);
+      ends += from_lane<0x122>(ends);
+      ends += from_lane<0x121>(ends);
       ends += __shfl_xor(ends, 16);
       ends += __shfl_xor(ends, 32);
-      x[4 * MT - 1] += gg == 3 ? ends : 0.0f;   // to the last token's dG
-      row_sums(x, mm);
-      // lane m has the sums from index m MT/2 on: of dG in the first eight lanes
-      float* to = s_red + (2 * w + (mm >> 3)) * C + 4 * gg;
-      const int i = (mm & 7) * (MT / 2);
-#pragma unroll
-      for (int j = 0; j < MT / 2; ++j) to[16 * (i >> 2) + (i & 3) + j] = x[j];
+      if (l == 0) s_end[w] = ends;
     }
     // dq and dk of the heads that share a key: in LDS until the last one
     f32x4* sum = reinterpret_cast<f32x4*>(smem + Z::oAcc) + w * 2 * MT * 64 + here(l);
     if (at.hh > 0) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        E[t] += sum[t * 64];
-        H[t] += sum[(MT + t) * 64];
-      }
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          E[f][t] += sum[(f * TT + t) * 64];
+          H[f][t] += sum[(MT + f * TT + t) * 64];
+        }
     }
     if (at.hh + 1 < group) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        sum[t * 64] = E[t];
-        sum[(MT + t) * 64] = H[t];
-      }
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          sum[(f * TT + t) * 64] = E[f][t];
+          sum[(MT + f * TT + t) * 64] = H[f][t];
+        }
     } else {
-      const int c = 16 * w + m, ldo = here_s(a.Hk * a.Dk * es);
+      const int ldo = here_s(a.Hk * a.Dk * es);
       const Buf qo = rows_buf(static_cast<char*>(a.dq) + (tok * a.Hk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
       const Buf ko = rows_buf(static_cast<char*>(a.dk) + (tok * a.Hk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
-      const int oo = here(c < a.Dk ? 4 * g * ldo + c * es : kNowhere);
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int f = 0; f < 2; ++f) {
+        const int c = 16 * (f0 + f) + m;
+        const int oo = here(c < a.Dk ? (16 * t0 + 4 * g) * ldo + c * es : kNowhere);
 #pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-          store_el2<BF16>(qo, oo + (16 * t + r) * ldo, ldo, E[t][r], E[t][r + 1]);
-          store_el2<BF16>(ko, oo + (16 * t + r) * ldo, ldo, H[t][r], H[t][r + 1]);
-        }
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            store_el2<BF16>(qo, oo + (16 * t + r) * ldo, ldo, E[f][t][r], E[f][t][r + 1]);
+            store_el2<BF16>(ko, oo + (16 * t + r) * ldo, ldo, H[f][t][r], H[f][t][r + 1]);
+          }
+      }
     }
     __syncthreads();   // the sums are there, the fragments and decays read
     if (w == 1 && more) decays();
     if (w == 0) {
-      float g1 = 0.0f, k1 = 0.0f;
+      float g1 = 0.0f, k1 = 0.0f, last = 0.0f;
       const int i = l < C ? l : 0;
 #pragma unroll
-      for (int x = 0; x < NW; ++x) {
+      for (int x = 0; x < NW / 2; ++x) {
         g1 += s_red[2 * x * C + i];
         k1 += s_red[(2 * x + 1) * C + i];
       }
+#pragma unroll
+      for (int x = 0; x < NW; ++x) last += s_end[x];
+      g1 += l == C - 1 ? last : 0.0f;
       // sums from the end: the lanes the other way round
       const int r = C - 1 - l;
       const double sums = lane_sums(l < C ? __shfl(g1, r & 63) : 0.0f), dg = __shfl(sums, r & 63);
