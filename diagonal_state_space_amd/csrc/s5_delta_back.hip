@@ -19,10 +19,11 @@
 // term of dG is a row of a product that is there anyway.
 //
 // What bounds them (128 x 128 bf16, 64 value heads of 2048 steps): the chain as the
-// forward one, 158 us; the rest, 189 us, by its instructions and phases (one
-// workgroup on a compute unit: vector instructions 34 % of the cycles, matrix
-// instructions 28 %) next to the 540 MB of states, writes and their gradients
-// that it reads (2.9 TB/s).
+// forward one, 158 us; the rest, 181 us, by its phases between barriers, one
+// workgroup on a compute unit (of 47000 cycles for a head's chunk 6000 staging,
+// 20500 products over the value features, of which matrix instructions 12400,
+// 6500 finishing W1 and W2, 4200 the products over tokens, 5000 rows and results),
+// next to the 540 MB of states, writes and their gradients that it reads.
 #include "s5_delta_tile.h"
 
 namespace s5 {
@@ -299,8 +300,9 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
 }
 
 // ---- the gradients without a chain ------------------------------------------------
-// One wave per 32 features of a key and half of the chunk's tokens (16 features
-// and all tokens read more of the LDS, which bounds the products: 185 -> XXX us).
+// A wave has 32 features of a key and half of the chunk's tokens (with 16
+// features and all tokens it reads more of the LDS: 185 us instead of 181 for 64
+// value heads of 2048 steps, 128 x 128 bf16).
 // The products over the value features run in steps of 32: S, D', U, dR and dY
 // are split into parts and put into row fragments in LDS once for the
 // workgroup, the next step's loads on their way meanwhile; each wave has its
