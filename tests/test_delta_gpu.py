@@ -147,6 +147,39 @@ def test_segments_and_lengths(io):
     assert not torch.isfinite(y[7, 1500:2499]).any() and not torch.isfinite(s[7]).any()
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(70, 130, 2, 4, 100, 40), (90, 130, 2, 2, 48, 80), (4, 2100, 2, 4, 128, 64)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_many_heads(shape, io):
+    """More heads than there are compute units for groups of 32 columns (in
+    whole, or in the segments' sums): groups of 64."""
+    lengths = np.random.default_rng(3).integers(0, shape[1] + 1, size=shape[0]).astype(np.int32)
+    x = delta_inputs(*shape, io, seed=sum(shape))
+    y, s = _run(x, io, lengths=torch.from_numpy(lengths).cuda())
+    yr, sr = orc.gated_delta(**x, lengths=lengths)
+    check("y", y, yr, y_bound(shape[1], io), io)
+    check("state", s, sr, delta_bound(shape[1]))
+
+
+def test_offsets_beyond_32_bits():
+    """v and y of 2.3e9 elements: the last tokens as in a call of their own, bit
+    for bit (whole chunks lie before them)."""
+    import diagonal_state_space_amd as s5
+    L, cut, H, Dv = 140000, 139968, 128, 128
+    torch.manual_seed(1)
+    unit = lambda *s: torch.nn.functional.normalize(torch.randn(*s, device="cuda"), dim=-1).bfloat16()   # noqa: E731
+    q, k = unit(1, L, 1, 16), unit(1, L, 1, 16)
+    v = torch.empty(1, L, H, Dv, device="cuda", dtype=torch.bfloat16)
+    for i in range(0, L, 20000):
+        v[:, i:i + 20000].normal_()
+    g, beta = -torch.rand(1, L, H, device="cuda"), torch.rand(1, L, H, device="cuda")
+    y, s = s5.gated_delta(q, k, v, g, beta, final_state=True)
+    _, s1 = s5.gated_delta(q[:, :cut], k[:, :cut], v[:, :cut], g[:, :cut].contiguous(), beta[:, :cut].contiguous(), final_state=True)
+    y2, s2 = s5.gated_delta(q[:, cut:], k[:, cut:], v[:, cut:], g[:, cut:].contiguous(), beta[:, cut:].contiguous(), s1, final_state=True)
+    assert torch.equal(y[:, cut:], y2) and torch.equal(s, s2)
+    assert torch.isfinite(y2).all() and y2.float().abs().mean() > 0.01
+
+
 def test_large_values_stay_relative():
     """v and the state a million times larger: the bound is relative."""
     x = delta_inputs(1, 100, 1, 1, 64, 64, "bf16", seed=4)

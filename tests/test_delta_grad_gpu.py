@@ -92,6 +92,40 @@ def test_lengths_leave_the_rows_behind(io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(70, 130, 2, 4, 100, 40), (140, 130, 2, 2, 48, 80), (4, 1500, 2, 4, 128, 64)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_many_heads(shape, io):
+    """More heads than there are compute units for groups of 32 columns (in
+    whole, or in the segments' sums), and more chunks than workgroups that stay."""
+    lengths = np.random.default_rng(3).integers(0, shape[1] + 1, size=shape[0]).astype(np.int32)
+    x = delta_inputs(*shape, io, seed=sum(shape), grads=True)
+    got = _backward(x, io, lengths=torch.from_numpy(lengths).cuda())
+    _check(got, orc.gated_delta_backward(**x, lengths=lengths), shape[1], io)
+
+
+def test_offsets_beyond_32_bits():
+    """v and its gradient of 2.3e9 elements: the last tokens' gradients as in a
+    call of their own, bit for bit (whole chunks lie before them)."""
+    import diagonal_state_space_amd as s5
+    L, cut, H, Dv = 140000, 139968, 128, 128
+    torch.manual_seed(1)
+    unit = lambda *s: torch.nn.functional.normalize(torch.randn(*s, device="cuda"), dim=-1).bfloat16()   # noqa: E731
+    q, k = unit(1, L, 1, 16), unit(1, L, 1, 16)
+    v, dy = (torch.empty(1, L, H, Dv, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    for i in range(0, L, 20000):
+        v[:, i:i + 20000].normal_()
+        dy[:, i:i + 20000].normal_()
+    g, beta = -torch.rand(1, L, H, device="cuda"), torch.rand(1, L, H, device="cuda")
+    whole = s5.gated_delta_backward(dy, q, k, v, g, beta)
+    head = [a[:, :cut].contiguous() if a is g or a is beta else a[:, :cut] for a in (q, k, v, g, beta)]
+    tail = [a[:, cut:].contiguous() if a is g or a is beta else a[:, cut:] for a in (q, k, v, g, beta)]
+    _, s1 = s5.gated_delta(*head, final_state=True)
+    part = s5.gated_delta_backward(dy[:, cut:].contiguous(), *tail, s1)
+    for a, b in zip(whole[:5], part[:5]):
+        assert torch.equal(a[:, cut:], b) and b.float().abs().mean() > 0.001
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_segments_and_lengths(io):
     L = 2500
     lengths = np.array([0, 1, 700, 1280, 1281, 1279, 2500, 2499], dtype=np.int32)
