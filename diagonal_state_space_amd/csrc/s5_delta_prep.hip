@@ -346,7 +346,7 @@ namespace {
 // 384 us in one piece, 107 in 16.
 int segments_of(int64_t heads, int dvp, int dkp, int chunks, bool bf16) {
   const bool wide = dkp > 64;
-  const double out = bf16 ? (wide ? 2.8 : 2.2) : (wide ? 3.1 : 1.5), sum = bf16 ? (wide ? 2.1 : 1.65) : (wide ? 1.6 : 1.1);
+  const double out = bf16 ? (wide ? 2.8 : 2.2) : (wide ? 2.1 : 1.5), sum = bf16 ? (wide ? 2.1 : 1.65) : (wide ? 1.6 : 1.1);
   const double join = wide ? 2.5 : 0.45;
   constexpr double kStart = 2.0;   // a workgroup's first loads
   if (heads * ((dvp + 63) / 64) >= kUnits / 2 || chunks < 16) return 1;

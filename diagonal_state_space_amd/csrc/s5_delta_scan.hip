@@ -47,12 +47,17 @@ template <bool BF16, int KP, Pass PASS>
 struct Scan : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;
   static constexpr bool kBack = PASS == kKeep || PASS == kSumBack, kY = PASS == kOut;
-  static constexpr int kFrags = (kY ? 3 : 2) * Z::kMat;
   static constexpr int kRecT = tri_frags<Z::C>() * 3 * kFrag;
   static constexpr int kRec = kY ? Record<Z::C>::bytes(false, Z::NO) : kRecT + kFrag;
-  static constexpr int kBuf = kFrags + kRec;
-  static constexpr bool kTwo = 2 * kBuf <= kMaxLds;
-  static constexpr int kLds = (kTwo ? 2 : 1) * kBuf;
+  // q once where two of all do not fit (float32, 128 features): the next one
+  // replaces it when it is read, in the middle of a chunk. With one buffer for
+  // all, 90 heads of up to 4178 steps took 623 us instead of 443.
+  static constexpr bool kOneQ = kY && 2 * (3 * Z::kMat + kRec) > kMaxLds;
+  static constexpr int kFrags = (kY && !kOneQ ? 3 : 2) * Z::kMat;
+  static constexpr int kBuf = kFrags + kRec, kOnce = kOneQ ? Z::kMat : 0;
+  static constexpr bool kTwo = 2 * kBuf + kOnce <= kMaxLds;
+  static constexpr int kLds = (kTwo ? 2 : 1) * kBuf + kOnce;
+  static constexpr int oQ = kOneQ ? (kTwo ? 2 : 1) * kBuf : 2 * Z::kMat;   // in the buffer, if not once
 };
 
 template <bool BF16, int KP, int NW, Pass PASS>
@@ -92,12 +97,12 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
       const unsigned char* rec = a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(Z::kBack, NO);
       if constexpr (BF16) {
         k.store(dst, dst + Z::kMat, id);
-        if constexpr (Y) q.store(dst + 2 * Z::kMat, nullptr, id);
+        if constexpr (Y) q.store(dst + Z::oQ, nullptr, id);
       } else {
         const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack);
         lds_copy<kCopy>(dst, fr + Z::k_rows(Z::kBack), Z::kMat, w - NW);
         lds_copy<kCopy>(dst + Z::kMat, fr, Z::kMat, w - NW);
-        if constexpr (Y) lds_copy<kCopy>(dst + 2 * Z::kMat, fr + Z::q_rows(Z::kBack), Z::kMat, w - NW);
+        if constexpr (Y && !Z::kOneQ) lds_copy<kCopy>(dst + Z::oQ, fr + Z::q_rows(Z::kBack), Z::kMat, w - NW);
       }
       if constexpr (Y) {
         lds_copy<kCopy>(dst + Z::kFrags, rec, Z::kRec, w - NW);
@@ -106,9 +111,15 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
         lds_copy<kCopy>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(Z::kBack, NO), kFrag, w - NW);
       }
     };
+    auto copy_q = [&](int n) {
+      const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack);
+      lds_copy<kCopy>(smem + Z::oQ, fr + Z::q_rows(Z::kBack), Z::kMat, w - NW);
+    };
+    static_assert(!Z::kOneQ || (Z::kTwo && !BF16));
     if (n0 < n1) load(n0);
     if (Z::kTwo && n0 < n1) {
       copy(n0);
+      if constexpr (Z::kOneQ) copy_q(n0);
       if (n0 + 1 < n1) load(n0 + 1);
     }
     for (int n = n0; n < n1; ++n) {
@@ -116,6 +127,10 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
         barrier_copied();
         if (n + 1 < n1) copy(n + 1);
         if (n + 2 < n1) load(n + 2);
+        if constexpr (Z::kOneQ) {
+          barrier_passed();   // q is read; the copies need not be there yet
+          if (n + 1 < n1) copy_q(n + 1);
+        }
       } else {
         barrier_copied();
         copy(n);
@@ -183,10 +198,13 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   for (int n = n0; n < n1; ++n) {
     if constexpr (!Z::kTwo) barrier_read();   // the previous chunk is read
     barrier_read();                           // the chunk is there, the previous one read
-    if (!wave_live) continue;
+    if (!wave_live) {
+      if constexpr (Z::kOneQ) barrier_read();
+      continue;
+    }
 
     const unsigned char* s_k = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
-    const unsigned char *s_kt = s_k + Z::kMat, *s_q = s_k + 2 * Z::kMat, *rec = s_k + Z::kFrags;
+    const unsigned char *s_kt = s_k + Z::kMat, *s_q = Z::kOneQ ? smem + Z::oQ : s_k + Z::oQ, *rec = s_k + Z::kFrags;
     const float* dec = reinterpret_cast<const float*>(rec + Z::kRec - kFrag);
     if constexpr (KEEP) {
       const int o = here(16 * l);
@@ -281,6 +299,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
       stage_end();
     }
     if (n + 1 < n1) fetch(n + 1);
+    if constexpr (Z::kOneQ) barrier_read();   // q is read
     int first = C;   // first row that is not finite, of this lane's column
     // (the last tile's rows have all of R: a zero of T times NaN is NaN)
     if (__any(!(fabsf(U[MT - 1][0]) < INFINITY))) {
