@@ -304,18 +304,6 @@ __device__ __forceinline__ void store_cols(unsigned char* base, const Parts<BF16
 }
 
 // ---- elements of v, y and their gradients in accumulator order --------------------
-template <bool BF16>
-__device__ __forceinline__ float load_el(const void* p, int64_t i) {
-  if constexpr (BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-  else return static_cast<const float*>(p)[i];
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store_el(void* p, int64_t i, float x) {
-  if constexpr (BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16(x);
-  else static_cast<float*>(p)[i] = x;
-}
-
 // an element's bits, and its value (apart: a conversion at the load would wait for it)
 template <bool BF16>
 __device__ __forceinline__ uint32_t load_raw(Buf r, int o) {
