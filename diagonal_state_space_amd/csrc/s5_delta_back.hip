@@ -32,9 +32,9 @@ using namespace delta;
 
 namespace {
 
-// LDS of a chunk: fragments of k (by rows, by columns) and q (by columns) and
-// the decays, two of them where they fit (more waves copy them); the transposed T and P, which the
-// next chunk's replace as soon as they are read.
+// LDS of a chunk: fragments of k (by rows, by columns) and q (by columns), the
+// decays and (bf16) y's gradient, two of them where they fit; the transposed T
+// and P, which the next chunk's replace as soon as they are read.
 template <bool BF16, int KP, int NW>
 struct Back : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
   constexpr int kFirstIo = 2 * MT;   // tile numbers of dY and V
   auto all_kept = [](int j) { return (j + 1) * NW <= kFirstIo; };
   auto all_io = [](int j) { return j * NW >= kFirstIo; };
-  Eight es_, ed, et[Z::kItems];
+  Eight kept_s, kept_d, et[Z::kItems];
   float gn = 0.0f, bn = 0.0f;    // the first two waves': g and beta
   const int lane_kept = g * 256 + (m & 7) * 32, lane_s = lane_kept + (m >> 3) * keep.dkp * 64, lane_r = lane_kept + (m >> 3) * C * 64;
   auto fetch = [&](const Place& p, int v0) {
@@ -502,8 +502,8 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       }
       return x;
     };
-    es_ = load_kept(0, keep.dkp, w, lane_s);
-    ed = load_kept(keep.at_d(), keep.dkp, w, lane_s);
+    kept_s = load_kept(0, keep.dkp, w, lane_s);
+    kept_d = load_kept(keep.at_d(), keep.dkp, w, lane_s);
 #pragma unroll
     for (int j = 0; j < Z::kItems; ++j) {
       const int t = w + j * NW;
@@ -550,8 +550,8 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
 #pragma clang loop unroll(disable)
     while (true) {
       {
-        store_kept(smem + Z::oS + w * 3 * kFrag, here(kept_at), es_.lo, es_.hi);
-        store_kept(smem + Z::oD + w * 3 * kFrag, here(kept_at), ed.lo, ed.hi);
+        store_kept(smem + Z::oS + w * 3 * kFrag, here(kept_at), kept_s.lo, kept_s.hi);
+        store_kept(smem + Z::oD + w * 3 * kFrag, here(kept_at), kept_d.lo, kept_d.hi);
 #pragma unroll
         for (int j = 0; j < Z::kItems; ++j) {
           const int t = w + j * NW;

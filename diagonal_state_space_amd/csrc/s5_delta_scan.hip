@@ -34,15 +34,15 @@ namespace {
 
 constexpr float kNaN = __builtin_nanf("");
 
-// More waves copy the chunks. LDS of a chunk: fragments of k (by rows, by columns) and q, T, P and the
-// decays (KEEP: without q and P); two of them where they fit, the next chunk
-// on its way while one is worked on.
 // What a pass of the chunks is for: y and the last state; the states at the
 // chunks' starts and U for the backward pass; a segment's state from zero and
 // its transition (run on the columns of the identity without values), in the
 // workspace layout of the forward or the backward call.
 enum Pass { kOut, kKeep, kSum, kSumBack };
 
+// LDS of a chunk: fragments of k (by rows, by columns) and q, T, P and the
+// decays (without y: no q and P); two of them where they fit, the next chunk on
+// its way while one is worked on.
 template <bool BF16, int KP, Pass PASS>
 struct Scan : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;

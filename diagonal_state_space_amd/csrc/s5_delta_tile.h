@@ -172,7 +172,6 @@ struct Block {
 typedef __amdgpu_buffer_rsrc_t Buf;
 constexpr int kNowhere = 0x60000000;
 constexpr int kBufferWord3 = 0x00020000;          // raw buffer, 32-bit data format
-constexpr int64_t kMaxStride = int64_t{1} << 22;   // elements between tokens: 64 rows stay below 2^30 bytes
 
 // `rows` rows of `width` bytes, `ld` bytes apart, from p
 __device__ __forceinline__ Buf rows_buf(const void* p, int rows, int ld, int width) {
