@@ -12,7 +12,10 @@
 // lane: in the half layout chunks u and u + R/2V, in the interleaved one chunks
 // 2u and 2u + 1. So the rotation needs no exchange and only the sum of squares
 // crosses lanes. With V features of 16 bytes a wave reads and writes whole
-// lines; odd sizes, strides and bases take V = 1. The angles of a tile of
+// lines; odd sizes, strides and bases take V = 1. A half layout whose R/2 is not
+// a multiple of V takes chunks 2u and 2u + 1 too and finds the other members of
+// its pairs in a row of LDS (15 x 855 tokens of 7 + 6 heads of 96, 54 rotated, the
+// gradients in bf16: 54 us, with V = 1 135). The angles of a tile of
 // tokens are computed once for all heads, into LDS: position * frequency in
 // float64 turns (a float32 product loses the angle of far positions), whole
 // turns dropped, then sine and cosine in float32.
@@ -85,10 +88,15 @@ __device__ __forceinline__ void values(const Raw<BF16, V>& r, float (&x)[V]) {
   }
 }
 
-template <bool BF16, int V, bool GRAD, bool INSIDE>
+// where the members of a pair are: in a unit's two chunks, side by side, or in
+// chunks of any lane of the row
+enum Pairs { kAcross, kInside, kAnywhere };
+
+template <bool BF16, int V, bool GRAD, Pairs PAIRS>
 __global__ void __launch_bounds__(kThreads) k_qk(QkArgs a, int G, int tile) {
   constexpr int U = V == 1 ? 2 : 1;
   extern __shared__ __align__(16) float s_mem[];
+  constexpr bool INSIDE = PAIRS == kInside;
   float2* s_cs = reinterpret_cast<float2*>(s_mem);      // [tile][R/2] cosine, sine
   const int tid = threadIdx.x;
   const int RP = a.R >> 1;                               // rotated pairs
@@ -100,15 +108,16 @@ __global__ void __launch_bounds__(kThreads) k_qk(QkArgs a, int G, int tile) {
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int u = lane + j * G;
-    if (a.interleaved || u >= RP / V) {
-      // interleaved: 2u; the rest of a half layout: from R on, two by two
-      c0[j] = a.interleaved ? 2 * u : 2 * (RP / V) + 2 * (u - RP / V);
+    if (PAIRS != kAcross || a.interleaved || u >= RP / V) {
+      // 2u; the rest of a half layout: from R on, two by two
+      c0[j] = PAIRS != kAcross || a.interleaved ? 2 * u : 2 * (RP / V) + 2 * (u - RP / V);
       c1[j] = c0[j] + 1;
     } else {
       c0[j] = u;
       c1[j] = u + RP / V;
     }
   }
+  float* s_row = s_mem + ((2 * tile * RP + 3) & ~3) + slot * a.D;   // pairs anywhere: the row's values
   float dw[2][U][2][V];   // this lane's sums of the weights' gradients
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -169,6 +178,34 @@ __global__ void __launch_bounds__(kThreads) k_qk(QkArgs a, int G, int tile) {
     }
     // rotates the values of the unit (forward) or turns them back (gradient)
     auto rotate = [&](float (&v)[U][2][V]) {
+      if constexpr (PAIRS == kAnywhere) {
+        // a row's lanes are of one wave, whose LDS accesses stay in order
+        static_assert(U == 1);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = h == 0 ? c0[0] : c1[0];
+          if (c < chunks) {
+#pragma unroll
+            for (int e = 0; e < V; e += 4) *reinterpret_cast<float4*>(s_row + c * V + e) = float4{v[0][h][e], v[0][h][e + 1], v[0][h][e + 2], v[0][h][e + 3]};
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const int f = (h == 0 ? c0[0] : c1[0]) * V + e;
+            if (f < 2 * RP) {
+              const bool second = f >= RP;
+              const int p = second ? f - RP : f;
+              const float2 cs = s_cs[t * RP + p];
+              const float sn = second != GRAD ? cs.y : -cs.y, other = s_row[second ? p : f + RP];
+              v[0][h][e] = v[0][h][e] * cs.x + other * sn;
+            }
+          }
+        return;
+      }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         const int u = lane + j * G;
@@ -332,10 +369,9 @@ __global__ void k_zero(float* p, int n) {
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// whether whole 16-byte chunks of V features can be moved and hold pairs whole
+// whether whole 16-byte chunks of V features can be moved
 bool vectored(const QkArgs& a, bool backward, int V) {
-  return a.D % V == 0 && a.ldq % V == 0 && a.ldk % V == 0 && (a.interleaved || (a.R / 2) % V == 0) && aligned(a.q) &&
-         aligned(a.k) && aligned(a.q_out) && aligned(a.k_out) &&
+  return a.D % V == 0 && a.ldq % V == 0 && a.ldk % V == 0 && aligned(a.q) && aligned(a.k) && aligned(a.q_out) && aligned(a.k_out) &&
          (!backward || (aligned(a.dq_out) && aligned(a.dk_out)));
 }
 
@@ -356,15 +392,15 @@ int tile_of(const QkArgs& a) {
   return tile;
 }
 
-// INSIDE: pairs sit inside a chunk, else across a unit's two chunks
-template <bool BF16, int V, bool GRAD, bool INSIDE>
+template <bool BF16, int V, bool GRAD, Pairs PAIRS>
 hipError_t run(const QkArgs& a, hipStream_t stream) {
   const int G = lanes_of(a, V), tile = tile_of(a);
   int64_t blocks = (a.T + tile - 1) / tile;
   blocks = std::min<int64_t>(blocks, GRAD ? kBackwardBlocks : 1 << 20);
   size_t lds = static_cast<size_t>(tile) * (a.R / 2) * sizeof(float2);
+  if (PAIRS == kAnywhere) lds = (lds + 15) / 16 * 16 + static_cast<size_t>(kThreads / G) * a.D * sizeof(float);
   if (GRAD) lds = std::max(lds, static_cast<size_t>(kThreads / G) * 2 * a.D * sizeof(float));
-  k_qk<BF16, V, GRAD, INSIDE><<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), lds, stream>>>(a, G, tile);
+  k_qk<BF16, V, GRAD, PAIRS><<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), lds, stream>>>(a, G, tile);
   hipError_t e = hipGetLastError();
   if (GRAD && e == hipSuccess && a.partials != nullptr) {
     k_qk_weights<<<dim3(2 * a.D), dim3(kThreads), 0, stream>>>(a.partials, static_cast<int>(blocks), a.D, a.dwq, a.dwk);
@@ -375,8 +411,9 @@ hipError_t run(const QkArgs& a, hipStream_t stream) {
 
 template <bool BF16, int V, bool GRAD>
 hipError_t dispatch(const QkArgs& a, hipStream_t stream) {
-  if (!vectored(a, GRAD, V)) return run<BF16, 1, GRAD, false>(a, stream);
-  return a.interleaved ? run<BF16, V, GRAD, true>(a, stream) : run<BF16, V, GRAD, false>(a, stream);
+  if (!vectored(a, GRAD, V)) return run<BF16, 1, GRAD, kAcross>(a, stream);
+  if (a.interleaved) return run<BF16, V, GRAD, kInside>(a, stream);
+  return (a.R / 2) % V == 0 ? run<BF16, V, GRAD, kAcross>(a, stream) : run<BF16, V, GRAD, kAnywhere>(a, stream);
 }
 
 }  // namespace

@@ -39,6 +39,13 @@ CASES = [
     ((1, 300), 7, 1, 256, 16, "f32", "rms", False, False, False),
     ((4, 1030), 3, 2, 40, 8, "bf16", "rms", True, False, False),
     ((2, 9), 2, 2, 255, 254, "f32", None, False, False, False),
+    # half layouts whose pairs are in any two chunks
+    ((15, 55), 7, 6, 96, 54, "bf16", "rms", True, False, True),
+    ((2, 77), 2, 5, 40, 26, "bf16", "l2", False, False, False),   # five chunks
+    ((3, 40), 3, 1, 256, 254, "bf16", None, False, False, True),
+    ((70,), 9, 2, 8, 6, "bf16", "rms", True, False, False),
+    ((2, 130), 4, 2, 64, 36, "f32", "rms", True, False, True),
+    ((5,), 1, 1, 4, 2, "f32", "l2", True, False, False),
 ]
 
 
