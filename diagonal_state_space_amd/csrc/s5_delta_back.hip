@@ -331,7 +331,12 @@ struct Grad : Shape<BF16, KP> {
   static constexpr int oRV = oRed + NW * Z::C * 4;          // [C] dR.V
   static constexpr int oEnd = oRV + Z::C * 4;               // [NW] the waves' parts of the last token's dG
   static constexpr int oAcc = oEnd + NW * 4;                // [NW][2 MT][64] dq and dk, where heads share a key
-  static constexpr int kAcc = NW * 2 * Z::MT * kFrag, kLds = oAcc + kAcc;
+  static constexpr int kAcc = NW * 2 * Z::MT * kFrag;
+  // 64 features: these sums are in memory, without them two workgroups fit a
+  // compute unit (16 heads on 8 keys, 10 x 1481 tokens, 64 x 128 bf16: 210 us, in the
+  // LDS 285)
+  static constexpr bool kAccLds = KP > 64;
+  static constexpr int kLds = oAcc + (kAccLds ? kAcc : 0), kGroups = kAccLds ? 256 : 512;
 };
 
 // Sums of N values each over the 16 lanes of a row: halves of the values and of
@@ -783,7 +788,9 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       if (l == 0) s_end[w] = ends;
     }
     // dq and dk of the heads that share a key: in LDS until the last one
-    f32x4* sum = reinterpret_cast<f32x4*>(smem + Z::oAcc) + w * 2 * MT * 64 + here(l);
+    f32x4* sum = (Z::kAccLds ? reinterpret_cast<f32x4*>(smem + Z::oAcc)
+                             : reinterpret_cast<f32x4*>(keep.sums) + static_cast<int64_t>(blockIdx.x) * (Z::kAcc / 16)) +
+                 w * 2 * MT * 64 + here(l);
     if (at.hh > 0) {
 #pragma unroll
       for (int f = 0; f < 2; ++f)
@@ -852,7 +859,10 @@ int64_t keep_of(DeltaArgs& a, DeltaSegs& segs, DeltaKeep& k) {
   k.dvp = (a.Dv + 15) & ~15;
   const int64_t head = (delta_work(a, segs, true) + 15) & ~int64_t{15};
   k.p = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + head);
-  return head + chunks * k.size(C) * 4;
+  k.sums = k.p + chunks * k.size(C);
+  const bool sums = a.Dk <= 64 && a.Hv > a.Hk;
+  const int64_t acc = sums ? a.bf16_io ? Grad<true, 64>::kAcc * Grad<true, 64>::kGroups : Grad<false, 64>::kAcc * Grad<false, 64>::kGroups : 0;
+  return head + chunks * k.size(C) * 4 + acc;
 }
 
 // the chain's passes, for all segments or for their sums
@@ -877,9 +887,9 @@ hipError_t grad(const DeltaArgs& a, const DeltaKeep& keep, hipStream_t stream) {
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds);
   if (attr != hipSuccess) return attr;
   const int chunks = (a.L + G::C - 1) / G::C;
-  // one workgroup at a time fits a compute unit (KP = 64: two)
-  const int64_t items = static_cast<int64_t>(a.B) * a.Hk * chunks, most = KP == 64 ? 512 : 256;
-  kern<<<dim3(static_cast<unsigned>(items < most ? items : most)), dim3(G::kThreads), G::kLds - (a.Hv == a.Hk ? G::kAcc : 0), stream>>>(a, chunks, keep);
+  const int64_t items = static_cast<int64_t>(a.B) * a.Hk * chunks;
+  const int lds = G::kLds - (G::kAccLds && a.Hv == a.Hk ? G::kAcc : 0);
+  kern<<<dim3(static_cast<unsigned>(items < G::kGroups ? items : G::kGroups)), dim3(G::kThreads), lds, stream>>>(a, chunks, keep);
   return hipGetLastError();
 }
 
