@@ -504,6 +504,9 @@ __device__ __forceinline__ void lds_copy(unsigned char* dst, const unsigned char
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + o), 16, o + l * 16, 0, 0, 0);
 }
 
+// this wave's copies are there (a barrier by itself does not wait for them)
+__device__ __forceinline__ void lds_copied() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // Barriers of kernels whose last kCopy waves do nothing but copy the next chunk
 // into LDS (the waves that compute then have no such copy in flight, for which
 // the compiler would wait before each of their LDS reads): they arrive when
