@@ -97,7 +97,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_delta_prep(DeltaArgs a, int chu
     const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(BACK);
     lds_copy<kWaves>(s_k, fr + Z::k_rows(BACK), Z::kMat, w);
     lds_copy<kWaves>(s_q, fr + Z::q_rows(BACK), Z::kMat, w);
-    lds_copied();   // before the barrier: the other waves read what this one copied
   }
   // sums of g (a wave's 64 lanes hold the chunk)
   if (w == 0) {
@@ -113,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_delta_prep(DeltaArgs a, int chu
     }
     if (l == 0) *s_bad = mask != 0 ? static_cast<int>(__ffsll(static_cast<unsigned long long>(mask))) - 1 : C;
   }
+  if constexpr (!BF16) lds_copied();   // the other waves read what this one copied
   __syncthreads();
 
   unsigned char* rec = a.recs + static_cast<int64_t>(blockIdx.x) * Record<C>::bytes(BACK, NO);
