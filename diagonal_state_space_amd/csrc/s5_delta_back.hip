@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     const bool vec = vectored(a, BF16), vecy = a.Dv % 8 == 0;
     Stage<BF16, KP, 64 * kCopy> k, q;
     ValueStage<NW> y;
-    auto record = [&](int n) { return a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true, 3); };
+    auto record = [&](int n) { return a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(true); };
     auto load = [&](int n) {
       const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
       if constexpr (BF16) {
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
         lds_copy<kCopy>(dst, fr + Z::k_rows(true), Z::kMat, w - NW);
         lds_copy<kCopy>(dst + Z::kMat, fr, 2 * Z::kMat, w - NW);
       }
-      lds_copy<kCopy>(dst + 3 * Z::kMat, record(n) + Record<C>::decays(true, 3), kFrag, w - NW);
+      lds_copy<kCopy>(dst + 3 * Z::kMat, record(n) + Record<C>::decays(true), kFrag, w - NW);
     };
     if (n0 < n1) {
       load(n1 - 1);

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_frags(DeltaArgs a, int chunk
 template <bool BF16, int KP, bool BACK>
 __global__ void __launch_bounds__(kThreads, 4) k_delta_prep(DeltaArgs a, int chunks) {
   using Z = Shape<BF16, KP>;
-  constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT;
+  constexpr int C = Z::C, NI = Z::NI, KS = Z::KS, MT = Z::MT;
   constexpr int LD = C + 4;
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* s_k = smem;
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_delta_prep(DeltaArgs a, int chu
   if constexpr (!BF16) lds_copied();   // the other waves read what this one copied
   __syncthreads();
 
-  unsigned char* rec = a.recs + static_cast<int64_t>(blockIdx.x) * Record<C>::bytes(BACK, NO);
+  unsigned char* rec = a.recs + static_cast<int64_t>(blockIdx.x) * Record<C>::bytes(BACK);
   // A: wave w the row tile w, in registers until k and q are read (in the same
   // LDS four workgroups fit a compute unit, not three: 62 -> 50 us for 8 ragged
   // sequences of 2048 steps, 16 heads)
@@ -173,11 +173,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_delta_prep(DeltaArgs a, int chu
         x[4 * half + r] = (BACK ? q <= p : p <= q) ? v : 0.0f;
       }
     }
-    constexpr int NPP = BACK ? 3 : NO;
-    const Frag<NPP> fr = to_frag<NPP>(x);
-    unsigned char* dst = rec + (BACK ? Record<C>::PT : Record<C>::P) + f * NPP * kFrag + l * 16;
+    const Frag<3> fr = to_frag<3>(x);
+    unsigned char* dst = rec + (BACK ? Record<C>::PT : Record<C>::P) + f * 3 * kFrag + l * 16;
 #pragma unroll
-    for (int p = 0; p < NPP; ++p) *reinterpret_cast<bf16x8*>(dst + p * kFrag) = fr.p[p];
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(dst + p * kFrag) = fr.p[p];
   }
   __syncthreads();
   const int bad = *s_bad;   // rows from a token that is not finite on are those of I
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_delta_prep(DeltaArgs a, int chu
     }
   }
   if (tid < C) {
-    float* dec = reinterpret_cast<float*>(rec + Record<C>::decays(BACK, NO));
+    float* dec = reinterpret_cast<float*>(rec + Record<C>::decays(BACK));
     const float from = expf(static_cast<float>(s_g[tid]));
     dec[tid] = from;
     dec[C + tid] = expf(static_cast<float>(s_g[C - 1] - s_g[tid]));
@@ -376,7 +375,7 @@ int64_t work(DeltaArgs& a, DeltaSegs& segs, bool backward) {
   const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
   const int chunks = (a.L + Z::C - 1) / Z::C;
   const int64_t frags = static_cast<int64_t>(a.B) * a.Hk * chunks * Z::frags(backward);
-  const int64_t recs = heads * chunks * Record<Z::C>::bytes(backward, Z::NO);
+  const int64_t recs = heads * chunks * Record<Z::C>::bytes(backward);
   a.frags = static_cast<unsigned char*>(a.ws);
   a.recs = a.frags + frags;
   segs.dkp = (a.Dk + 15) & ~15;

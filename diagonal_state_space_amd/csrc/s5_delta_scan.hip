@@ -11,8 +11,11 @@
 // without an exchange or a barrier. What the waves share - k, its transpose,
 // q, T and P of the chunk - is staged in LDS once for the workgroup, by waves
 // that do nothing else, a chunk ahead.
-// The state's chain is exact to float32 (three bf16 parts); what only reaches
-// y of bf16 io takes two parts.
+// All products are exact to float32 (three bf16 parts), those that lead to a y of
+// bf16 io alone too: its terms scale from Q S and P U can be far larger than y
+// (where a key is written over, y is what is left of them), and with two parts
+// a y 4096 times smaller than its terms had two digits. The third part costs 7 %
+// of 8 ragged sequences of 2048 steps, 16 heads of 128 x 128 (172 -> 183 us).
 //
 // What bounds it: the chain itself, with one wave on a SIMD (the LDS has room for
 // one workgroup on a compute unit). Of 7550 cycles for a chunk of 64 steps (128 x
@@ -48,10 +51,10 @@ struct Scan : Shape<BF16, KP> {
   using Z = Shape<BF16, KP>;
   static constexpr bool kBack = PASS == kKeep || PASS == kSumBack, kY = PASS == kOut;
   static constexpr int kRecT = tri_frags<Z::C>() * 3 * kFrag;
-  static constexpr int kRec = kY ? Record<Z::C>::bytes(false, Z::NO) : kRecT + kFrag;
-  // q once where two of all do not fit (float32, 128 features): the next one
-  // replaces it when it is read, in the middle of a chunk. With one buffer for
-  // all, 90 heads of up to 4178 steps took 623 us instead of 443.
+  static constexpr int kRec = kY ? Record<Z::C>::bytes(false) : kRecT + kFrag;
+  // q once where two of all do not fit (128 features): the next one replaces it
+  // when it is read, in the middle of a chunk. With one buffer for all, 90 heads of
+  // up to 4178 steps in float32 took 623 us instead of 443.
   static constexpr bool kOneQ = kY && 2 * (3 * Z::kMat + kRec) > kMaxLds;
   static constexpr int kFrags = (kY && !kOneQ ? 3 : 2) * Z::kMat;
   static constexpr int kBuf = kFrags + kRec, kOnce = kOneQ ? Z::kMat : 0;
@@ -63,7 +66,7 @@ struct Scan : Shape<BF16, KP> {
 template <bool BF16, int KP, int NW, Pass PASS>
 __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, int chunks, int groups, DeltaSegs segs, DeltaKeep keep) {
   using Z = Scan<BF16, KP, PASS>;
-  constexpr int C = Z::C, NI = Z::NI, NO = Z::NO, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
+  constexpr int C = Z::C, NI = Z::NI, KS = Z::KS, MT = Z::MT, CS = Z::CS, KT = Z::KT, es = Z::es;
   constexpr bool SUM = PASS == kSum || PASS == kSumBack, KEEP = PASS == kKeep, Y = PASS == kOut;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, m = l & 15;
@@ -90,52 +93,70 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
     auto load = [&](int n) {
       const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
       if constexpr (BF16) k.load(a, a.k, a.ldk, tok, min(len - n * C, C), hk, id, vec);
+    };
+    auto load_q = [&](int n) {
+      const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
       if constexpr (BF16 && Y) q.load(a, a.q, a.ldq, tok, min(len - n * C, C), hk, id, vec);
     };
     auto copy = [&](int n) {
       unsigned char* dst = smem + (Z::kTwo ? (n & 1) * Z::kBuf : 0);
-      const unsigned char* rec = a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(Z::kBack, NO);
+      const unsigned char* rec = a.recs + (static_cast<int64_t>(bh) * chunks + n) * Record<C>::bytes(Z::kBack);
       if constexpr (BF16) {
         k.store(dst, dst + Z::kMat, id);
-        if constexpr (Y) q.store(dst + Z::oQ, nullptr, id);
       } else {
         const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack);
         lds_copy<kCopy>(dst, fr + Z::k_rows(Z::kBack), Z::kMat, w - NW);
         lds_copy<kCopy>(dst + Z::kMat, fr, Z::kMat, w - NW);
-        if constexpr (Y && !Z::kOneQ) lds_copy<kCopy>(dst + Z::oQ, fr + Z::q_rows(Z::kBack), Z::kMat, w - NW);
       }
       if constexpr (Y) {
         lds_copy<kCopy>(dst + Z::kFrags, rec, Z::kRec, w - NW);
       } else {
         lds_copy<kCopy>(dst + Z::kFrags, rec + Record<C>::T, Z::kRecT, w - NW);
-        lds_copy<kCopy>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(Z::kBack, NO), kFrag, w - NW);
+        lds_copy<kCopy>(dst + Z::kFrags + Z::kRecT, rec + Record<C>::decays(Z::kBack), kFrag, w - NW);
       }
     };
     auto copy_q = [&](int n) {
-      const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack);
-      lds_copy<kCopy>(smem + Z::oQ, fr + Z::q_rows(Z::kBack), Z::kMat, w - NW);
+      unsigned char* dst = smem + (Z::kTwo && !Z::kOneQ ? (n & 1) * Z::kBuf : 0) + Z::oQ;
+      if constexpr (BF16 && Y) {
+        q.store(dst, nullptr, id);
+      } else if constexpr (Y) {
+        const unsigned char* fr = a.frags + (static_cast<int64_t>(b * a.Hk + hk) * chunks + n) * Z::frags(Z::kBack);
+        lds_copy<kCopy>(dst, fr + Z::q_rows(Z::kBack), Z::kMat, w - NW);
+      }
     };
-    static_assert(!Z::kOneQ || (Z::kTwo && !BF16));
-    if (n0 < n1) load(n0);
+    static_assert(!Z::kOneQ || Z::kTwo);
+    if (n0 < n1) {
+      load(n0);
+      load_q(n0);
+    }
     if (Z::kTwo && n0 < n1) {
       copy(n0);
-      if constexpr (Z::kOneQ) copy_q(n0);
-      if (n0 + 1 < n1) load(n0 + 1);
+      copy_q(n0);
+      if (n0 + 1 < n1) {
+        load(n0 + 1);
+        load_q(n0 + 1);
+      }
     }
     for (int n = n0; n < n1; ++n) {
       if constexpr (Z::kTwo) {
         barrier_copied();
         if (n + 1 < n1) copy(n + 1);
+        if (!Z::kOneQ && n + 1 < n1) copy_q(n + 1);
         if (n + 2 < n1) load(n + 2);
         if constexpr (Z::kOneQ) {
           barrier_passed();   // q is read; the copies need not be there yet
           if (n + 1 < n1) copy_q(n + 1);
         }
+        if (n + 2 < n1) load_q(n + 2);
       } else {
         barrier_copied();
         copy(n);
+        copy_q(n);
         barrier_copied();
-        if (n + 1 < n1) load(n + 1);
+        if (n + 1 < n1) {
+          load(n + 1);
+          load_q(n + 1);
+        }
       }
     }
     return;
@@ -219,7 +240,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
     for (int t = 0; t < MT; ++t) X[t] = O[t] = U[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     Frag<NI> kx[2][MT], qx[KS / 2][MT];
     Frag<3> tf[CS][MT], sf[2];
-    Frag<NO> so[KS / 2];
+    Frag<3> so[KS / 2];
     auto read_k = [&](int ks) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) kx[ks & 1][t] = read_rows<NI, KS>(s_k, t, ks);
@@ -257,7 +278,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
       stage_end();
       mma(X, kx[ks & 1], sf[ks & 1]);
       if (ks + 1 < KS) sf[(ks + 1) & 1] = to_frag<3>(S[2 * ks + 2], S[2 * ks + 3]);
-      if (Y && ks < KS / 2) so[ks] = to_frag<NO>(S[2 * ks], S[2 * ks + 1]);
+      if (Y && ks < KS / 2) so[ks] = sf[ks & 1];
       stage_end();
     }
     read_tri<false, C>(tf[0], rec + Record<C>::T, 0);
@@ -288,7 +309,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
       if (ks + 1 < CS) xf[ks + 1] = to_frag<3>(X[2 * ks + 2], X[2 * ks + 3]);
       if (Y && ks == 0) {
 #pragma unroll
-        for (int i = 0; i < KS / 2; ++i) so[i] = to_frag<NO>(S[KS + 2 * i], S[KS + 2 * i + 1]);
+        for (int i = 0; i < KS / 2; ++i) so[i] = to_frag<3>(S[KS + 2 * i], S[KS + 2 * i + 1]);
       }
       if (ks == CS - 1) {
 #pragma unroll
@@ -338,8 +359,22 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
       for (int t = 0; t < MT; ++t) store16(p, o + t * 1024, U[t]);
     }
     // S <- whole S + K^T (to U), and O <- scale from O + P U beside it
+    constexpr int kGroups = CS * KT / 4;
+    // the 32-steps of P: read in one of these groups (-1: before them), multiplied
+    // in the next one (float32 with 64 features: the only one)
+    auto read_at = [](int ks) { return CS == 1 ? 0 : kGroups >= 4 ? ks : ks - 1; };
+    auto mma_at = [&](int ks) { return kGroups > 1 ? read_at(ks) + 1 : 0; };
     Frag<NI> cf[2][4];
+    Frag<3> pf[CS][MT], ub[CS];
+    auto read_p = [&](int i) {
+      if constexpr (Y) {
+#pragma unroll
+        for (int ks = 0; ks < CS; ++ks)
+          if (i == read_at(ks)) read_tri<false, C>(pf[ks], rec + Record<C>::P, ks);
+      }
+    };
     read_cols4<NI, C>(cf[0], s_kt, 0, 0);
+    read_p(-1);
     stage_end();
     mma_q(1);
     Frag<3> uf[CS];
@@ -354,14 +389,11 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
       uf[ks] = to_frag<3>(x);
     }
     stage_end();
-    constexpr int kGroups = CS * KT / 4;
-    Frag<NO> pf[CS][MT], ub[CS];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       if (i + 1 < kGroups) read_cols4<NI, C>(cf[(i + 1) & 1], s_kt, 4 * ((i + 1) % (KT / 4)), (i + 1) / (KT / 4));
+      read_p(i);
       if (Y && i == 0) {
-#pragma unroll
-        for (int ks = 0; ks < CS; ++ks) read_tri<false, C>(pf[ks], rec + Record<C>::P, ks);
 #pragma unroll
         for (int t = 0; t < MT; ++t) from[t] = *reinterpret_cast<const float4*>(dec + 3 * C + 16 * t + 4 * g);
       }
@@ -376,12 +408,11 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
             for (int r = 0; r < 4; ++r) O[t][r] *= ff[r];
           }
 #pragma unroll
-          for (int ks = 0; ks < CS; ++ks) ub[ks] = to_frag<NO>(U[2 * ks], U[2 * ks + 1]);
+          for (int ks = 0; ks < CS; ++ks) ub[ks] = to_frag<3>(U[2 * ks], U[2 * ks + 1]);
         }
-        if (i == (kGroups > 1 ? 1 : 0)) {
 #pragma unroll
-          for (int ks = 0; ks < CS; ++ks) mma_tri<false, C>(O, pf[ks], ks, ub[ks]);
-        }
+        for (int ks = 0; ks < CS; ++ks)
+          if (i == mma_at(ks)) mma_tri<false, C>(O, pf[ks], ks, ub[ks]);
         if (i == kGroups - 1) {
           if (first < C) {
 #pragma unroll

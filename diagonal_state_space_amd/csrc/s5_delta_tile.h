@@ -138,16 +138,35 @@ __device__ __forceinline__ Frag<NP> read_cols(const unsigned char* base, int mt,
   return read_frag<NP>(base, mt * (C / 32) + ks, mt);
 }
 
+// the same offset, of which the compiler makes no table for a loop: sums with it
+// are formed where they are used instead of kept in registers throughout
+__device__ __forceinline__ int here(int o) {
+  asm volatile("" : "+v"(o));
+  return o;
+}
+
+__device__ __forceinline__ int here_s(int o) {
+  asm volatile("" : "+s"(o));
+  return o;
+}
+
 // The chains' products run in stages whose fragments are read one stage ahead
 // (left to itself the compiler reads a fragment right before its use, and the
 // wave, alone on its SIMD, waits for the LDS each time). A stage ends here.
 __device__ __forceinline__ void stage_end() { __builtin_amdgcn_sched_barrier(0); }
 
-// four of the state's tiles by the fragments of 32 tokens
+// four of the state's tiles by the fragments of 32 tokens. bf16's exchanged slots
+// are formed where they are used: kept throughout they do not all find a register
+// in its y pass, and what is spilled is waited for with v.
 template <int NP, int C>
 __device__ __forceinline__ void read_cols4(Frag<NP> (&f)[4], const unsigned char* a, int t0, int ks) {
+  const int slot = 16 * (threadIdx.x & 63), l16 = NP == 1 ? here(slot) : slot;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) f[t] = read_cols<NP, C>(a, t0 + t, ks);
+  for (int t = 0; t < 4; ++t) {
+    const unsigned char* p = a + ((t0 + t) * (C / 32) + ks) * NP * kFrag + (l16 ^ 16 * (t0 + t));
+#pragma unroll
+    for (int i = 0; i < NP; ++i) f[t].p[i] = *reinterpret_cast<const bf16x8*>(p + i * kFrag);
+  }
 }
 template <int NP, int KT>
 __device__ __forceinline__ void mma_cols4(f32x4 (&s)[KT], int t0, const Frag<NP> (&f)[4], const Frag<3>& x) {
@@ -185,18 +204,6 @@ __device__ __forceinline__ uint4 load16(Buf r, int o) {
 
 __device__ __forceinline__ void store16(Buf r, int o, f32x4 x) {
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned, x), r, o, 0, 0);
-}
-
-// the same offset, of which the compiler makes no table for a loop: sums with it
-// are formed where they are used instead of kept in registers throughout
-__device__ __forceinline__ int here(int o) {
-  asm volatile("" : "+v"(o));
-  return o;
-}
-
-__device__ __forceinline__ int here_s(int o) {
-  asm volatile("" : "+s"(o));
-  return o;
 }
 
 // four tokens `ld` bytes apart, the first at byte `o` (kNowhere: a block of
@@ -354,9 +361,16 @@ template <bool UP, int C>
 __device__ __forceinline__ bool tri_has(int t, int ks) { return UP ? t <= 2 * ks + 1 : t >= 2 * ks; }
 template <bool UP, int C, int NP>
 __device__ __forceinline__ void read_tri(Frag<NP> (&f)[C / 16], const unsigned char* a, int ks) {
+  // rows are not exchanged here: slot l; formed where it is used (bf16's y pass has
+  // no register to keep it in)
+  const unsigned char* p = a + here(16 * (threadIdx.x & 63));
 #pragma unroll
   for (int t = 0; t < C / 16; ++t)
-    if (tri_has<UP, C>(t, ks)) f[t] = read_frag<NP>(a, UP ? tri_frag_t<C>(t, ks) : tri_frag<C>(t, ks), 0);
+    if (tri_has<UP, C>(t, ks)) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        f[t].p[i] = *reinterpret_cast<const bf16x8*>(p + ((UP ? tri_frag_t<C>(t, ks) : tri_frag<C>(t, ks)) * NP + i) * kFrag);
+    }
 }
 template <bool UP, int C, int NP, int NB>
 __device__ __forceinline__ void mma_tri(f32x4 (&c)[C / 16], const Frag<NP> (&f)[C / 16], int ks, const Frag<NB>& b) {
@@ -379,18 +393,17 @@ struct Record {
   static constexpr int T = 0;
   static constexpr int P = tri_frags<C>() * 3 * kFrag;           // backward: T transposed
   static constexpr int PT = 2 * P;                               // backward only
-  static constexpr int decays(bool backward, int np) { return backward ? 3 * P : P + tri_frags<C>() * np * kFrag; }
-  static constexpr int bytes(bool backward, int np) { return decays(backward, np) + kFrag; }
+  static constexpr int decays(bool backward) { return (backward ? 3 : 2) * P; }
+  static constexpr int bytes(bool backward) { return decays(backward) + kFrag; }
 };
 
 // What the kernels share for an io type and padded features of a key (KP = 64
-// or 128): parts of k and q (NI) and of what leads to y only (NO), tiles of 16
-// and steps of 32 tokens (MT, CS) and features (KT, KS), bytes of the fragments
-// of k or q of a chunk.
+// or 128): parts of k and q (NI), tiles of 16 and steps of 32 tokens (MT, CS) and
+// features (KT, KS), bytes of the fragments of k or q of a chunk.
 template <bool BF16, int KP>
 struct Shape {
   static constexpr int C = chunk_of<BF16>();
-  static constexpr int NI = BF16 ? 1 : 3, NO = BF16 ? 2 : 3;
+  static constexpr int NI = BF16 ? 1 : 3;
   static constexpr int KS = KP / 32, KT = KP / 16, MT = C / 16, CS = C / 32;
   static constexpr int kMat = MT * KS * NI * kFrag;
   static constexpr int es = BF16 ? 2 : 4;

@@ -391,7 +391,7 @@ s5_status s5_glu(int64_t T, int64_t H, s5_dtype io, int variant, const void* y, 
  * Precision: the state and sums are float32 (the sums of g float64), products
  * with float32 values as exact as float32 products (on the matrix cores as
  * three bf16 parts), so for bf16 io only the outputs of type io are rounded to
- * bf16; what leads to y of bf16 io and nowhere else takes two parts (2^-16).
+ * bf16.
  * A chunk's writes are solved for at once, with sums in the order of a
  * triangular system's inverse: keys close to one another with beta near 2
  * amplify roundings as they do token by token, by up to the chunk's length.
