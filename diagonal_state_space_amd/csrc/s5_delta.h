@@ -33,7 +33,9 @@ int qk_partial_blocks(const QkArgs& a);
 hipError_t launch_qk(const QkArgs& a, bool backward, hipStream_t stream);
 hipError_t launch_zero(float* p, int n, hipStream_t stream);
 
-// Gated delta rule over B sequences of up to L tokens.
+// Gated delta rule over B sequences of up to L tokens. Strides are at most
+// kMostStride elements where a sequence has several tokens.
+constexpr int64_t kMostStride = int64_t{1} << 22;
 struct DeltaArgs {
   int B, L, Hk, Hv, Dk, Dv;
   int64_t ldq, ldk, ldv;   // elements between the tokens of q, k and v

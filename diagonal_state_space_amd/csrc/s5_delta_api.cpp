@@ -42,6 +42,9 @@ int64_t span(int64_t rows, int64_t stride, int64_t width, int64_t es) {
   return rows > 0 ? ((rows - 1) * stride + width) * es : 0;
 }
 
+// whether `rows` rows, `stride` elements apart, are farther apart than offsets reach
+bool far(int64_t stride, int64_t rows) { return rows > 0 && stride > (int64_t{1} << 55) / rows; }
+
 s5_status delta_sizes(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, s5_dtype io,
                       int64_t ldq, int64_t ldk, int64_t ldv, float scale) {
   if (B < 0 || L < 0 || Hk < 1 || Hv < 1 || Dk < 1 || Dv < 1) return S5_ERR_INVALID_ARGUMENT;
@@ -50,9 +53,13 @@ s5_status delta_sizes(int64_t B, int64_t L, int64_t Hk, int64_t Hv, int64_t Dk, 
   if (Hv % Hk != 0 || !std::isfinite(scale)) return S5_ERR_INVALID_ARGUMENT;
   if (Hv > INT32_MAX / Dv || Hk > INT32_MAX / Dk) return S5_ERR_UNSUPPORTED;
   if (ldq < Hk * Dk || ldk < Hk * Dk || ldv < Hv * Dv) return S5_ERR_INVALID_ARGUMENT;
-  constexpr int64_t kMost = int64_t{1} << 22;   // a chunk's rows stay below 2^30 bytes
-  if (ldq > kMost || ldk > kMost || ldv > kMost || Hv * Dv > kMost || Hk * Dk > kMost) return S5_ERR_UNSUPPORTED;
+  constexpr int64_t kMost = s5::kMostStride;   // a chunk's rows stay below 2^30 bytes
+  if (Hv * Dv > kMost || Hk * Dk > kMost) return S5_ERR_UNSUPPORTED;
+  // the tokens of several steps; one step of each sequence is a row of its own, any
+  // distance from the next one's
+  if (L > 1 && (ldq > kMost || ldk > kMost || ldv > kMost)) return S5_ERR_UNSUPPORTED;
   if (B > 0 && (L > INT32_MAX / B || Hv * Dv > INT32_MAX / B)) return S5_ERR_UNSUPPORTED;
+  if (far(ldq, B * L) || far(ldk, B * L) || far(ldv, B * L)) return S5_ERR_UNSUPPORTED;
   // A launch has fewer than 2^32 threads: 256 for each chunk of 32 or 64 steps and
   // head, and for each head up to 8 column groups of 512 (the chains) or 16 of 256
   // (the single step)

@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     auto load_io = [&](bool second, int t) {
       const int64_t ld = second ? a.ldv : a.Hv * a.Dv;
       const char* src = static_cast<const char*>(second ? a.v : a.dy) + ((tok + 16 * t) * ld + static_cast<int64_t>(h) * a.Dv) * es;
-      const int ldb = static_cast<int>(ld) * es, v = v0 + 8 * (l & 3), o = (l >> 2) * ldb + v * es;
+      const int ldb = row_bytes(ld, es), v = v0 + 8 * (l & 3), o = (l >> 2) * ldb + v * es;
       const Buf r = rows_buf(src, min(p.left, C) - 16 * t, ldb, a.Dv * es);
       Eight x{};
       if constexpr (VEC) {

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   }
 
   uint32_t vb[MT][4];
-  const int ldv = static_cast<int>(a.ldv) * es, ldy = a.Hv * a.Dv * es;
+  const int ldv = row_bytes(a.ldv, es), ldy = a.Hv * a.Dv * es;
   // byte of the first of this lane's elements in rows of `ld` bytes: bf16's y pass
   // has no register to keep it in, and one that is spilled is waited for with the
   // stores

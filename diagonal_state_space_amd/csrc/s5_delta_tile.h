@@ -206,6 +206,12 @@ __device__ __forceinline__ void store16(Buf r, int o, f32x4 x) {
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) unsigned, x), r, o, 0, 0);
 }
 
+// bytes between a chunk's tokens. A longer stride than kMostStride is that of
+// chunks of one token: only its row is in the buffer, whatever the distance.
+__device__ __forceinline__ int row_bytes(int64_t stride, int es) {
+  return static_cast<int>(stride < kMostStride ? stride : kMostStride) * es;
+}
+
 // four tokens `ld` bytes apart, the first at byte `o` (kNowhere: a block of
 // features that do not exist); nd of the eight features exist
 template <bool BF16>
@@ -428,7 +434,7 @@ struct Stage {
 
   // tokens [tok, tok + rows) of head `hk`
   __device__ __forceinline__ void load(const DeltaArgs& a, const void* p, int64_t stride, int64_t tok, int rows, int hk, int id, bool vec) {
-    const int ld = static_cast<int>(stride) * Z::es;
+    const int ld = row_bytes(stride, Z::es);
     const Buf buf = rows_buf(static_cast<const char*>(p) + (tok * stride + static_cast<int64_t>(hk) * a.Dk) * Z::es, rows, ld, a.Dk * Z::es);
 #pragma unroll
     for (int j = 0; j < kJobs; ++j) {

@@ -407,9 +407,11 @@ s5_status s5_glu(int64_t T, int64_t H, s5_dtype io, int variant, const void* y, 
  * B or L, heads or features < 1, Hv not a multiple of Hk, a token stride below
  * the row, a scale that is not finite, workspace too small, an output
  * overlapping an input or another output), S5_ERR_UNSUPPORTED (io, feature
- * limits, a token stride, Hk*Dk or Hv*Dv above 2^22 elements, B*L or B*Hv*Dv
- * above INT32_MAX, B*Hv above 2^19 - 1 or, times the 32-step chunks of L, above
- * 2^24 - 1, misalignment), S5_ERR_HIP.
+ * limits, Hk*Dk or Hv*Dv above 2^22 elements, with L > 1 a token stride above
+ * that (one step of each sequence may be a slice of a buffer of whole prompts),
+ * B*L strides above 2^55 elements, B*L or B*Hv*Dv above INT32_MAX, B*Hv above
+ * 2^19 - 1 or, times the 32-step chunks of L, above 2^24 - 1, misalignment),
+ * S5_ERR_HIP.
  */
 #define S5_DELTA_MAX_DK 128
 #define S5_DELTA_MAX_DV 512
@@ -452,7 +454,7 @@ s5_status s5_gated_delta_backward(const s5_delta_desc* desc, hipStream_t stream)
  * q, k [B,Hk,Dk], v [B,Hv,Dv] (row strides as above), g, beta [B,Hv], s
  * [B,Hv,Dk,Dv] float32 read and overwritten in place, y [B,Hv,Dv] out. Equal,
  * up to rounding, to s5_gated_delta with L = 1 and s0 = s_last = s. The sums
- * run on the vector units in float32. Errors as s5_gated_delta.
+ * run on the vector units in float32. Errors as s5_gated_delta with L = 1.
  */
 s5_status s5_gated_delta_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, s5_dtype io,
                               int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
