@@ -171,8 +171,7 @@ s5_status qk_args(const s5_qk_desc* x, s5::QkArgs& a) {
   if (x->D > S5_QK_MAX_D || (x->io != S5_F32 && x->io != S5_BF16)) return S5_ERR_UNSUPPORTED;
   if (x->Hq > INT32_MAX / 512 || x->Hk > INT32_MAX / 512 || x->T > INT32_MAX / (x->Hq + x->Hk)) return S5_ERR_UNSUPPORTED;
   if (x->q_stride < x->Hq * x->D || x->k_stride < x->Hk * x->D) return S5_ERR_INVALID_ARGUMENT;
-  constexpr int64_t kMost = int64_t{1} << 28;
-  if (x->q_stride > kMost || x->k_stride > kMost) return S5_ERR_UNSUPPORTED;
+  if (far(x->q_stride, x->T) || far(x->k_stride, x->T)) return S5_ERR_UNSUPPORTED;
   if (!std::isfinite(x->rope_scale)) return S5_ERR_INVALID_ARGUMENT;
   if (norms ? !(std::isfinite(x->eps) && x->eps > 0.0f) : (x->q_weight || x->k_weight)) return S5_ERR_INVALID_ARGUMENT;
   a = s5::QkArgs{};

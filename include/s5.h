@@ -508,7 +508,8 @@ s5_status s5_gated_delta_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int
  * L, Hq, Hk or D < 1, R odd or outside 0..D, a stride below the row, eps not
  * finite or not > 0 with a norm, rope_scale not finite, workspace too small,
  * overlaps), S5_ERR_UNSUPPORTED (io, D above the limit, T*(Hq+Hk) above
- * INT32_MAX, misalignment), S5_ERR_HIP.
+ * INT32_MAX, Hq or Hk above INT32_MAX/512, T strides above 2^55 elements,
+ * misalignment), S5_ERR_HIP.
  */
 #define S5_QK_MAX_D 256
 enum { S5_QK_RMS = 1u << 0, S5_QK_L2 = 1u << 1, S5_QK_INTERLEAVED = 1u << 2 };

@@ -55,6 +55,19 @@ def test_limits_of_the_step(which):
     assert call(1 << 61) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("which", ["q_stride", "k_stride"])
+def test_limits_of_the_query_key_pass(which):
+    def call(**kw):
+        x = dict(size=ctypes.sizeof(s5.QkDesc), flags=1, io=1, T=10, L=5, Hq=2, Hk=2, D=32, R=0, q_stride=64, k_stride=64, eps=1e-6,
+                 rope_scale=1.0)
+        n = ctypes.c_int64()
+        return s5.lib().s5_qk_workspace(ctypes.byref(s5.QkDesc(**{**x, **kw})), ctypes.byref(n))
+
+    for stride in (1 << 28, (1 << 28) + 1, 1 << 40):
+        assert call(**{which: stride}) == OK
+    assert call(**{which: 1 << 61}) == UNSUPPORTED
+
+
 # ---- results ----------------------------------------------------------------------
 
 
@@ -94,3 +107,31 @@ def test_one_token_of_a_prompt(shape, T, row, io):
     check("state", s, sr, delta_bound(1))
     for name, a, r in zip(("dq", "dk", "dv", "dg", "dbeta", "ds0"), s5.gated_delta_backward(**d), gr):
         check(name, a, r, delta_bound(1, grad=True) * (8 if name == "dg" else 1), io if name in ("dq", "dk", "dv") else "f32")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,row,D,io", [(33000, 8200, 64, "bf16"), (33000, 8201, 33, "bf16"), (2000, 8192, 96, "f32")])
+def test_one_token_of_a_prompt_normalised_and_rotated(T, row, D, io):
+    """Two sequences' tokens 270 million elements apart."""
+    _gpu()
+    rng = np.random.default_rng(D)
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    x = torch.from_numpy(rng.normal(size=(2, 1, 7, D))).cuda().to(dt)
+    dy = torch.from_numpy(rng.normal(size=(2, 1, 7, D))).cuda().to(dt)
+    buf = torch.full((2, T, row), float("nan"), device="cuda", dtype=dt)
+    buf[:, T - 2, 8:8 + 7 * D] = x.reshape(2, -1)
+    part = buf[:, T - 2:T - 1, 8:8 + 7 * D].unflatten(-1, (7, D))
+    f = s5.rope_frequencies(D // 2 // 2 * 2)
+    pos = torch.tensor([[T - 2], [17]], device="cuda", dtype=torch.int32)
+    opt = dict(norm="l2", freqs=f, positions=pos)
+    got = s5.qk_norm_rope(part[:, :, :4], part[:, :, 4:], **opt)
+    grads = s5.qk_norm_rope_backward(dy[:, :, :4].contiguous(), dy[:, :, 4:].contiguous(), part[:, :, :4], part[:, :, 4:], **opt)
+    x, dy = x.double().cpu().numpy(), dy.double().cpu().numpy()
+    ref = dict(norm="l2", eps=float(np.float32(1e-6)), freqs=f.cpu().numpy(), positions=pos.cpu().numpy())
+    rel = 8 * 2.0 ** -24
+    for i, part in enumerate((slice(0, 4), slice(4, 7))):
+        check("qk"[i], got[i], orc.norm_rope(x[:, :, part], **ref), rel, io, element=4 * np.sqrt(D))
+        dx = orc.norm_rope_backward(dy[:, :, part], x[:, :, part], **ref)[0]
+        # the difference of two terms of the size of dy / |x|, each off by rel
+        terms = np.linalg.norm(dy[:, :, part] / np.linalg.norm(x[:, :, part], axis=-1, keepdims=True)) / np.linalg.norm(dx)
+        check("dq dk".split()[i], grads[i], dx, 2 * rel * max(1.0, terms), io, element=8 * np.sqrt(D))
