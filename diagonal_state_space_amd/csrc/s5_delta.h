@@ -67,7 +67,7 @@ hipError_t launch_delta_step(const DeltaArgs& a, hipStream_t stream);
 // of 16 columns one after the other: four rows of a column in 16 bytes.
 struct DeltaKeep {
   float* p;
-  float* sums;   // gradients' workgroups' sums of dq and dk over the heads of a key (64 features)
+  float* sums;   // gradients' workgroups' sums of dq and dk over the heads of a key (bf16, 64 features)
   int dkp, dvp;
   __host__ __device__ int at_d() const { return dkp * dvp; }
   __host__ __device__ int at_u() const { return 2 * dkp * dvp; }

@@ -332,11 +332,12 @@ struct Grad : Shape<BF16, KP> {
   static constexpr int oEnd = oRV + Z::C * 4;               // [NW] the waves' parts of the last token's dG
   static constexpr int oAcc = oEnd + NW * 4;                // [NW][2 MT][64] dq and dk, where heads share a key
   static constexpr int kAcc = NW * 2 * Z::MT * kFrag;
-  // 64 features: these sums are in memory, without them two workgroups fit a
-  // compute unit (16 heads on 8 keys, 10 x 1481 tokens, 64 x 128 bf16: 210 us, in the
-  // LDS 285)
-  static constexpr bool kAccLds = KP > 64;
-  static constexpr int kLds = oAcc + (kAccLds ? kAcc : 0), kGroups = kAccLds ? 256 : 512;
+  // Up to 64 features two workgroups fit a compute unit; with these sums in the LDS
+  // not of bf16, whose sums are in memory then (16 heads on 8 keys, 10 x 1481
+  // tokens, 64 x 128: 210 us, in the LDS 285). Those of float32 fit too (16 heads on
+  // 4 keys, 10 x 1481 tokens, 64 x 64, forward and gradients: 636 us, in memory 646).
+  static constexpr bool kAccLds = KP > 64 || 2 * (oAcc + kAcc) <= kMaxLds;
+  static constexpr int kLds = oAcc + (kAccLds ? kAcc : 0), kGroups = KP > 64 ? 256 : 512;
 };
 
 // Sums of N values each over the 16 lanes of a row: halves of the values and of
@@ -860,8 +861,9 @@ int64_t keep_of(DeltaArgs& a, DeltaSegs& segs, DeltaKeep& k) {
   const int64_t head = (delta_work(a, segs, true) + 15) & ~int64_t{15};
   k.p = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + head);
   k.sums = k.p + chunks * k.size(C);
-  const bool sums = a.Dk <= 64 && a.Hv > a.Hk;
-  const int64_t acc = sums ? a.bf16_io ? Grad<true, 64>::kAcc * Grad<true, 64>::kGroups : Grad<false, 64>::kAcc * Grad<false, 64>::kGroups : 0;
+  using G = Grad<true, 64>;
+  static_assert(!G::kAccLds && Grad<false, 64>::kAccLds);
+  const int64_t acc = a.bf16_io && a.Dk <= 64 && a.Hv > a.Hk ? G::kAcc * G::kGroups : 0;
   return head + chunks * k.size(C) * 4 + acc;
 }
 
