@@ -186,13 +186,13 @@ def _dev_tensor(t, name, dtype, shape):
     return t
 
 
-def _io_code(dtype) -> int:
+def _io_code(dtype, name="u/y") -> int:
     import torch
     if dtype == torch.float32:
         return S5_F32
     if dtype == torch.bfloat16:
         return S5_BF16
-    raise TypeError(f"u/y must be float32 or bfloat16, got {dtype}")
+    raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
 
 
 def discretize(lam, b_tilde, log_delta, lam_bar=None, b_bar=None, stream=None):
@@ -439,12 +439,16 @@ def set_profiling_events(events) -> None:
 # property, and the words for what is wrong only after that.
 
 
-def _on(t, stream):
+def _on(t, stream, name="the first tensor"):
     """None where t's device is the current one and no stream is given; else a
     context that makes both torch's, so that outputs and workspaces are
     allocated for the stream that the kernels run on."""
     import torch
-    if t.device.type != "cuda":
+    try:
+        on_gpu = t.device.type == "cuda"
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if not on_gpu:
         raise ValueError(f"the tensors must be on a GPU device, got {t.device}")
     if stream is None and t.device.index == torch.cuda.current_device():
         return None
@@ -550,7 +554,7 @@ def _delta_desc(q, k, v, g, beta, s0, scale, lengths):
     if v.dim() != 4:
         raise ValueError("v must be [B, L, Hv, Dv]")
     B, L, Hv, Dv = v.shape
-    dev, io = v.device, _io_code(v.dtype)
+    dev, io = v.device, _io_code(v.dtype, "v")
     ldv = _heads(v, "v", v.dtype, (B, L), dev)
     ldk = _heads(k, "k", v.dtype, (B, L), dev)
     ldq = _heads(q, "q", v.dtype, (B, L), dev)
@@ -582,7 +586,7 @@ def gated_delta(q, k, v, g, beta, s0=None, *, scale=None, lengths=None, final_st
     Returns (y, s_last), s_last None unless final_state is set or a buffer is
     given (which may be s0)."""
     import torch
-    on = _on(v, stream)
+    on = _on(v, stream, "v")
     if on is not None:
         with on:
             return gated_delta(q, k, v, g, beta, s0, scale=scale, lengths=lengths, final_state=final_state, y=y, s_last=s_last)
@@ -606,7 +610,7 @@ def gated_delta_backward(dy, q, k, v, g, beta, s0=None, ds_last=None, *, scale=N
     ds0), ds0 None unless s0 or a buffer for it is given. With lengths the
     rows behind are zero in gradients made here and left in given ones."""
     import torch
-    on = _on(v, stream)
+    on = _on(v, stream, "v")
     if on is not None:
         with on:
             return gated_delta_backward(dy, q, k, v, g, beta, s0, ds_last, scale=scale, lengths=lengths, dq=dq, dk=dk, dv=dv,
@@ -635,15 +639,15 @@ def gated_delta_step(q, k, v, g, beta, s, *, scale=None, y=None, stream=None):
     q, k [B, Hk, Dk], v [B, Hv, Dv], g, beta [B, Hv]; s [B, Hv, Dk, Dv] float32
     is updated in place. Returns y [B, Hv, Dv]."""
     import torch
-    if v.dim() != 3:
-        raise ValueError("v must be [B, Hv, Dv]")
-    on = _on(v, stream)
+    on = _on(v, stream, "v")
     if on is not None:
         with on:
             return gated_delta_step(q, k, v, g, beta, s, scale=scale, y=y)
+    if v.dim() != 3:
+        raise ValueError("v must be [B, Hv, Dv]")
     B, Hv, Dv = v.shape
     dev, dtype = v.device, v.dtype
-    io = _io_code(dtype)
+    io = _io_code(dtype, "v")
     ldv = _heads(v, "v", dtype, (B,), dev)
     ldk = _heads(k, "k", dtype, (B,), dev)
     ldq = _heads(q, "q", dtype, (B,), dev)
@@ -667,7 +671,7 @@ def _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, 
     import torch
     if q.dim() not in (3, 4):
         raise ValueError("q must be [T, Hq, D] or [B, L, Hq, D]")
-    lead, dev, io = q.shape[:-2], q.device, _io_code(q.dtype)
+    lead, dev, io = q.shape[:-2], q.device, _io_code(q.dtype, "q")
     ldq = _heads(q, "q", q.dtype, lead, dev)
     ldk = _heads(k, "k", q.dtype, lead, dev)
     (Hq, D), Hk = q.shape[-2:], k.shape[-2]
@@ -680,6 +684,8 @@ def _qk_desc(q, k, norm, q_weight, k_weight, eps, freqs, positions, rope_scale, 
         raise ValueError("weights need a norm")
     R = 0
     if freqs is not None:
+        if not isinstance(freqs, torch.Tensor):
+            raise TypeError("freqs must be a torch.Tensor")
         R = 2 * freqs.numel()
         if freqs.dim() != 1 or R > D:
             raise ValueError(f"freqs must be [R/2] with R <= {D}, got {tuple(freqs.shape)}")
@@ -708,7 +714,7 @@ def qk_norm_rope(q, k, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, fr
     (j, j + R/2), or (2j, 2j + 1) if interleaved. positions int32, shaped as
     the tokens; None counts 0, 1, ... along L (T). Returns contiguous
     (q_out, k_out); a contiguous input may be its own output."""
-    on = _on(q, stream)
+    on = _on(q, stream, "q")
     if on is not None:
         with on:
             return qk_norm_rope(q, k, norm=norm, q_weight=q_weight, k_weight=k_weight, eps=eps, freqs=freqs, positions=positions,
@@ -729,7 +735,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, *, norm="rms", q_weight=None, k_
     (dq, dk, dq_weight, dk_weight), a weight's gradient None without the
     weight."""
     import torch
-    on = _on(q, stream)
+    on = _on(q, stream, "q")
     if on is not None:
         with on:
             return qk_norm_rope_backward(dq_out, dk_out, q, k, norm=norm, q_weight=q_weight, k_weight=k_weight, eps=eps,
