@@ -38,6 +38,7 @@ hipError_t launch_zero(float* p, int n, hipStream_t stream);
 constexpr int64_t kMostStride = int64_t{1} << 22;
 struct DeltaArgs {
   int B, L, Hk, Hv, Dk, Dv;
+  int Nk, Nv;              // heads in a token's row of the contiguous arrays: Hk, Hv, or more in a slice of the heads
   int64_t ldq, ldk, ldv;   // elements between the tokens of q, k and v
   bool bf16_io;
   float scale;

@@ -74,6 +74,8 @@ s5::DeltaArgs delta_args(const s5_delta_desc& x) {
   a.L = static_cast<int>(x.L);
   a.Hk = static_cast<int>(x.Hk);
   a.Hv = static_cast<int>(x.Hv);
+  a.Nk = a.Hk;
+  a.Nv = a.Hv;
   a.Dk = static_cast<int>(x.Dk);
   a.Dv = static_cast<int>(x.Dv);
   a.ldq = x.q_stride;

@@ -24,6 +24,8 @@
 // 20500 products over the value features, of which matrix instructions 12400,
 // 6500 finishing W1 and W2, 4200 the products over tokens, 5000 rows and results),
 // next to the 540 MB of states, writes and their gradients that it reads.
+#include <algorithm>
+
 #include "s5_delta_tile.h"
 
 namespace s5 {
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     auto load = [&](int n) {
       const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
       if constexpr (BF16) {
-        y.load(static_cast<const char*>(a.dy) + ((tok * a.Hv + h) * a.Dv + cg * 16 * NW) * es, a.Hv * a.Dv * es, min(len - n * C, C),
+        y.load(static_cast<const char*>(a.dy) + ((tok * a.Nv + h) * a.Dv + cg * 16 * NW) * es, a.Nv * a.Dv * es, min(len - n * C, C),
                a.Dv - cg * 16 * NW, id, vecy);
         k.load(a, a.k, a.ldk, tok, min(len - n * C, C), hk, id, vec);
         q.load(a, a.q, a.ldq, tok, min(len - n * C, C), hk, id, vec);
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
     for (int t = 0; t < KT; ++t) asm volatile("" : "+v"(D[t]));   // waited for here, not in every chunk
   }
 
-  const int ldy = a.Hv * a.Dv * es;
+  const int ldy = a.Nv * a.Dv * es;
   const int yo = live ? 4 * g * ldy + col * es : kNowhere;
   // whole 16-byte groups of bf16: lane l/2's row, its columns from 8 (l%2) on
   const bool vecy = BF16 && a.Dv % 8 == 0;
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
   auto fetch = [&](int n) {
     const int64_t tok = static_cast<int64_t>(b) * a.L + n * C;
     const int o = here(yo);
-    const Buf yr = rows_buf(static_cast<const char*>(a.dy) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
+    const Buf yr = rows_buf(static_cast<const char*>(a.dy) + (tok * a.Nv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_back_scan(DeltaArgs
       for (int r = 0; r < 4; ++r) dR[t][r] *= bb[r];
     }
     if constexpr (!SUM) {
-      const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
+      const Buf vr = rows_buf(static_cast<char*>(a.dv) + (tok * a.Nv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
       if (vecy) {
         store_values(s_k + Z::oV + w * ValueStage<NW>::kWave, vr, here(vo), ldy, dR);
       } else {
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       return Eight{load16(b, o), load16(b, o + 16)};
     };
     auto load_io = [&](bool second, int t) {
-      const int64_t ld = second ? a.ldv : a.Hv * a.Dv;
+      const int64_t ld = second ? a.ldv : a.Nv * a.Dv;
       const char* src = static_cast<const char*>(second ? a.v : a.dy) + ((tok + 16 * t) * ld + static_cast<int64_t>(h) * a.Dv) * es;
       const int ldb = row_bytes(ld, es), v = v0 + 8 * (l & 3), o = (l >> 2) * ldb + v * es;
       const Buf r = rows_buf(src, min(p.left, C) - 16 * t, ldb, a.Dv * es);
@@ -518,8 +520,8 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
     }
     if (v0 == 0 && w < 2) {
       const bool in = l < C && l < p.left;
-      gn = in ? a.g[(tok + l) * a.Hv + h] : 0.0f;
-      bn = in ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
+      gn = in ? a.g[(tok + l) * a.Nv + h] : 0.0f;
+      bn = in ? a.beta[(tok + l) * a.Nv + h] : 0.0f;
     }
   };
   const int kept_at = kept_place(l), row_at = row_place(l);
@@ -810,9 +812,9 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
           sum[(MT + f * TT + t) * 64] = H[f][t];
         }
     } else {
-      const int ldo = here_s(a.Hk * a.Dk * es);
-      const Buf qo = rows_buf(static_cast<char*>(a.dq) + (tok * a.Hk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
-      const Buf ko = rows_buf(static_cast<char*>(a.dk) + (tok * a.Hk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
+      const int ldo = here_s(a.Nk * a.Dk * es);
+      const Buf qo = rows_buf(static_cast<char*>(a.dq) + (tok * a.Nk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
+      const Buf ko = rows_buf(static_cast<char*>(a.dk) + (tok * a.Nk + at.hk) * a.Dk * es, rows, ldo, a.Dk * es);
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         const int c = 16 * (f0 + f) + m;
@@ -844,15 +846,15 @@ __global__ void __launch_bounds__(4 * KP, 2) k_delta_grad(DeltaArgs a, int chunk
       const double sums = lane_sums(l < C ? __shfl(g1, r & 63) : 0.0f), dg = __shfl(sums, r & 63);
       if (l < C && l < left) {
         // a decay that clears the state hides what it multiplied
-        a.dg[(tok + l) * a.Hv + h] = gi < kLeastDecay ? 0.0f : static_cast<float>(dg);
-        a.dbeta[(tok + l) * a.Hv + h] = s_rv[l] + k1;
+        a.dg[(tok + l) * a.Nv + h] = gi < kLeastDecay ? 0.0f : static_cast<float>(dg);
+        a.dbeta[(tok + l) * a.Nv + h] = s_rv[l] + k1;
       }
     }
     at = next;
   }
 }
 
-// finds the workspace's parts; bytes of all of them
+// finds the workspace's parts (of a slice); bytes of all of them
 int64_t keep_of(DeltaArgs& a, DeltaSegs& segs, DeltaKeep& k) {
   const int C = a.bf16_io ? 64 : 32;
   const int64_t chunks = static_cast<int64_t>(a.B) * a.Hv * ((a.L + C - 1) / C);
@@ -896,7 +898,7 @@ hipError_t grad(const DeltaArgs& a, const DeltaKeep& keep, hipStream_t stream) {
 }
 
 template <bool BF16, int KP>
-hipError_t run(DeltaArgs a, hipStream_t stream) {
+hipError_t run(DeltaArgs a, hipStream_t stream) {   // a slice
   DeltaKeep keep{};
   DeltaSegs segs{};
   keep_of(a, segs, keep);
@@ -918,18 +920,107 @@ hipError_t run(DeltaArgs a, hipStream_t stream) {
   return vec ? grad<BF16, KP, true>(a, keep, stream) : grad<BF16, KP, false>(a, keep, stream);
 }
 
+// What the chains leave for the gradients is far more than the call's arrays (4.5
+// KB for a token and head of 128 x 128 bf16, whose v, y and their gradients are 1
+// KB), so a call that would leave more than kKeepMost is cut into slices that
+// follow each other in one workspace: some sequences each, or some key heads (with
+// their value heads) of one sequence. Slices of this size still fill the chip: forward
+// and gradients of 9 x 8192 steps of 16 heads, 128 x 128 bf16, take 5.36 ms in one
+// piece and 5.37 in two.
+constexpr int64_t kKeepMost = int64_t{4} << 30;
+
+struct Slices {
+  int seqs, heads;   // sequences and key heads of a slice
+  int64_t bytes;     // of workspace
+};
+
+int64_t bytes_of(const DeltaArgs& a, int seqs, int heads) {
+  DeltaArgs s = a;
+  s.B = seqs;
+  s.Hv = a.Hv / a.Hk * heads;
+  s.Hk = heads;
+  DeltaSegs segs{};
+  DeltaKeep k{};
+  return keep_of(s, segs, k);
+}
+
+// the fewest equal parts of n that need at most kKeepMost each (parts of one may need more)
+template <class F>
+int part_of(int n, F bytes) {
+  const int64_t all = bytes(n);
+  if (bytes(1) > kKeepMost) return 1;
+  for (int64_t parts = (all + kKeepMost - 1) / kKeepMost; parts < n; ++parts) {
+    const int part = static_cast<int>((n + parts - 1) / parts);
+    if (bytes(part) <= kKeepMost) return part;
+  }
+  return 1;
+}
+
+Slices slices_of(const DeltaArgs& a) {
+  Slices s{a.B, a.Hk, bytes_of(a, a.B, a.Hk)};
+  if (s.bytes <= kKeepMost) return s;
+  s.seqs = part_of(a.B, [&](int n) { return bytes_of(a, n, a.Hk); });
+  if (s.seqs == 1) s.heads = part_of(a.Hk, [&](int n) { return bytes_of(a, 1, n); });
+  // the last slice is smaller, but may have segments where the others have none
+  s.bytes = bytes_of(a, s.seqs, s.heads);
+  if (const int rest = a.B % s.seqs; rest > 0) s.bytes = std::max(s.bytes, bytes_of(a, rest, a.Hk));
+  if (const int rest = a.Hk % s.heads; rest > 0) s.bytes = std::max(s.bytes, bytes_of(a, 1, rest));
+  return s;
+}
+
+// sequences from b on and key heads from hk on (one sequence, if not all of them)
+DeltaArgs slice(const DeltaArgs& a, const Slices& n, int b, int hk) {
+  DeltaArgs s = a;
+  const int group = a.Hv / a.Hk, h = hk * group;
+  s.B = std::min(n.seqs, a.B - b);
+  s.Hk = std::min(n.heads, a.Hk - hk);
+  s.Hv = s.Hk * group;
+  const int64_t tok = static_cast<int64_t>(b) * a.L, es = a.bf16_io ? 2 : 4;
+  const int64_t vy = (tok * a.Nv + h) * a.Dv, qk = (tok * a.Nk + hk) * a.Dk, gb = tok * a.Nv + h;
+  const int64_t state = (static_cast<int64_t>(b) * a.Hv + h) * a.Dk * a.Dv;
+  auto at = [](auto* p, int64_t bytes) {
+    using T = decltype(p);
+    return p == nullptr ? p : reinterpret_cast<T>(reinterpret_cast<uintptr_t>(p) + bytes);
+  };
+  s.q = at(a.q, (tok * a.ldq + static_cast<int64_t>(hk) * a.Dk) * es);
+  s.k = at(a.k, (tok * a.ldk + static_cast<int64_t>(hk) * a.Dk) * es);
+  s.v = at(a.v, (tok * a.ldv + static_cast<int64_t>(h) * a.Dv) * es);
+  s.g = at(a.g, gb * 4);
+  s.beta = at(a.beta, gb * 4);
+  s.s0 = at(a.s0, state * 4);
+  s.lengths = at(a.lengths, b * 4);
+  s.dy = at(a.dy, vy * es);
+  s.ds_last = at(a.ds_last, state * 4);
+  s.dq = at(a.dq, qk * es);
+  s.dk = at(a.dk, qk * es);
+  s.dv = at(a.dv, vy * es);
+  s.dg = at(a.dg, gb * 4);
+  s.dbeta = at(a.dbeta, gb * 4);
+  s.ds0 = at(a.ds0, state * 4);
+  return s;
+}
+
+hipError_t run(const DeltaArgs& a, hipStream_t stream) {
+  if (a.bf16_io) return a.Dk > 64 ? run<true, 128>(a, stream) : run<true, 64>(a, stream);
+  return a.Dk > 64 ? run<false, 128>(a, stream) : run<false, 64>(a, stream);
+}
+
 }  // namespace
 
 int64_t delta_workspace(const DeltaArgs& args, bool backward) {
   DeltaArgs a = args;
   DeltaSegs segs{};
-  DeltaKeep k{};
-  return backward ? keep_of(a, segs, k) : delta_work(a, segs, false);
+  return backward ? slices_of(a).bytes : delta_work(a, segs, false);
 }
 
 hipError_t launch_delta_backward(const DeltaArgs& a, hipStream_t stream) {
-  if (a.bf16_io) return a.Dk > 64 ? run<true, 128>(a, stream) : run<true, 64>(a, stream);
-  return a.Dk > 64 ? run<false, 128>(a, stream) : run<false, 64>(a, stream);
+  const Slices n = slices_of(a);
+  for (int b = 0; b < a.B; b += n.seqs)
+    for (int hk = 0; hk < a.Hk; hk += n.heads) {
+      const hipError_t e = run(slice(a, n, b, hk), stream);
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
 }
 
 }  // namespace s5

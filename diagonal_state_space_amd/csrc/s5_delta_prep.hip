@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_delta_prep(DeltaArgs a, int chu
   // sums of g (a wave's 64 lanes hold the chunk)
   if (w == 0) {
     const bool live = l < C && l < left;
-    const float gi = live ? a.g[(tok + l) * a.Hv + h] : 0.0f;
-    const float be = live ? a.beta[(tok + l) * a.Hv + h] : 0.0f;
+    const float gi = live ? a.g[(tok + l) * a.Nv + h] : 0.0f;
+    const float be = live ? a.beta[(tok + l) * a.Nv + h] : 0.0f;
     const double s = chunk_sums(gi);
     const bool bad = !(gi < INFINITY) || !(fabsf(be) < INFINITY);
     const uint64_t mask = __ballot(bad);

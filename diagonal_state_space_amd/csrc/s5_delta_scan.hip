@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
   }
 
   uint32_t vb[MT][4];
-  const int ldv = row_bytes(a.ldv, es), ldy = a.Hv * a.Dv * es;
+  const int ldv = row_bytes(a.ldv, es), ldy = a.Nv * a.Dv * es;
   // byte of the first of this lane's elements in rows of `ld` bytes: bf16's y pass
   // has no register to keep it in, and one that is spilled is waited for with the
   // stores
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(64 * (NW + kCopy)) k_delta_scan(DeltaArgs a, i
                 if (16 * t + 4 * g + r >= first) O[t][r] = kNaN;
           }
           const int o = place(yo, ldy);
-          const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Hv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
+          const Buf yr = rows_buf(static_cast<char*>(a.y) + (tok * a.Nv + h) * a.Dv * es, min(len - n * C, C), ldy, a.Dv * es);
 #pragma unroll
           for (int t = 0; t < MT; ++t)
 #pragma unroll
