@@ -1,5 +1,5 @@
-"""The gated delta rule with write strengths between 1 and 2, up to a
-reflection at every step, for random, close and equal keys.
+"""The gated delta rule with write strengths near 1 and between 1 and 2, up to
+a reflection at every step, for random, close and equal keys.
 
 Bound. The chunked form solves (I + A) U = R for the writes U of a chunk, A_ij =
 beta_i e^{G_i - G_j} k_i.k_j. The products k_i.k_j are sums of up to 128 terms, off
@@ -27,7 +27,7 @@ torch = pytest.importorskip("torch")
 
 ETA = 2.0 ** -24 * np.sqrt(128)
 NAMES = ("y", "state", "dq", "dk", "dv", "dg", "dbeta", "ds0")
-STRENGTHS = {"two": (2.0, 2.0), "near_two": (1.9, 2.0), "one_to_two": (1.0, 2.0)}
+STRENGTHS = {"two": (2.0, 2.0), "near_two": (1.9, 2.0), "one_to_two": (1.0, 2.0), "near_one": (0.9, 1.0)}
 KEYS = {"random": None, "close": 0.1, "very_close": 1e-3, "equal": 0.0}
 
 
