@@ -873,10 +873,8 @@ int64_t keep_of(DeltaArgs& a, DeltaSegs& segs, DeltaKeep& k) {
 template <bool BF16, int KP, int NW, bool SUM>
 hipError_t chain(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep, hipStream_t stream) {
   using Z = Back<BF16, KP, NW>;
-  auto* kern = k_delta_back_scan<BF16, KP, NW, SUM>;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
-  if (attr != hipSuccess) return attr;
+  constexpr auto* kern = k_delta_back_scan<BF16, KP, NW, SUM>;
+  if (const hipError_t e = allow_lds<kern>(Z::kLds); e != hipSuccess) return e;
   const int chunks = (a.L + Z::C - 1) / Z::C, groups = (a.Dv + 16 * NW - 1) / (16 * NW);
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv * (SUM ? segs.count - 1 : segs.count) + 7) / 8 * 8 * groups;
   kern<<<dim3(static_cast<unsigned>(blocks)), dim3(64 * (NW + kCopy)), Z::kLds, stream>>>(a, chunks, groups, segs, keep);
@@ -886,10 +884,8 @@ hipError_t chain(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& kee
 template <bool BF16, int KP, bool VEC>
 hipError_t grad(const DeltaArgs& a, const DeltaKeep& keep, hipStream_t stream) {
   using G = Grad<BF16, KP>;
-  auto* kern = k_delta_grad<BF16, KP, VEC>;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds);
-  if (attr != hipSuccess) return attr;
+  constexpr auto* kern = k_delta_grad<BF16, KP, VEC>;
+  if (const hipError_t e = allow_lds<kern>(G::kLds); e != hipSuccess) return e;
   const int chunks = (a.L + G::C - 1) / G::C;
   const int64_t items = static_cast<int64_t>(a.B) * a.Hk * chunks;
   const int lds = G::kLds - (G::kAccLds && a.Hv == a.Hk ? G::kAcc : 0);

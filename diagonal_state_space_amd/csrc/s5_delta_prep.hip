@@ -303,16 +303,12 @@ hipError_t run(const DeltaArgs& a, hipStream_t stream) {
   constexpr int C = Z::C;
   constexpr int square = C * (C + 4) * 4, stage = 2 * Z::kMat;
   constexpr int lds = (stage > 2 * square ? stage : 2 * square) + C * 8 + C * 4 + 16;
-  auto* prep = k_delta_prep<BF16, KP, BACK>;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(prep), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (attr != hipSuccess) return attr;
+  constexpr auto* prep = k_delta_prep<BF16, KP, BACK>;
+  if (const hipError_t e = allow_lds<prep>(lds); e != hipSuccess) return e;
   const int chunks = (a.L + C - 1) / C;
   if constexpr (!BF16) {
-    auto* frags = k_delta_frags<KP, BACK>;
-    static const hipError_t frags_attr =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(frags), hipFuncAttributeMaxDynamicSharedMemorySize, Z::frags(BACK));
-    if (frags_attr != hipSuccess) return frags_attr;
+    constexpr auto* frags = k_delta_frags<KP, BACK>;
+    if (const hipError_t e = allow_lds<frags>(Z::frags(BACK)); e != hipSuccess) return e;
     frags<<<dim3(static_cast<unsigned>(a.B * a.Hk * chunks)), dim3(kThreads), Z::frags(BACK), stream>>>(a, chunks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

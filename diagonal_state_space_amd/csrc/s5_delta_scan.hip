@@ -567,10 +567,8 @@ template <bool BF16, int KP, int NW, Pass PASS>
 hipError_t run(const DeltaArgs& a, const DeltaSegs& segs, const DeltaKeep& keep, hipStream_t stream) {
   using Z = Scan<BF16, KP, PASS>;
   constexpr bool SUM = PASS == kSum || PASS == kSumBack;
-  auto* kern = k_delta_scan<BF16, KP, NW, PASS>;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, Z::kLds);
-  if (attr != hipSuccess) return attr;
+  constexpr auto* kern = k_delta_scan<BF16, KP, NW, PASS>;
+  if (const hipError_t e = allow_lds<kern>(Z::kLds); e != hipSuccess) return e;
   const int chunks = (a.L + Z::C - 1) / Z::C;
   const int groups = ((SUM ? segs.ld() : a.Dv) + 16 * NW - 1) / (16 * NW);
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.Hv * (SUM ? segs.count - 1 : segs.count) + 7) / 8 * 8 * groups;

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "s5_common.h"
 #include "s5_delta.h"
 
@@ -111,6 +113,21 @@ __device__ __forceinline__ void mma(f32x4 (&c)[N], const Frag<NA> (&a)[N], const
 
 constexpr int kFrag = 1024;   // bytes of one part of a fragment
 constexpr int kMaxLds = 160 * 1024;
+
+// Asks once for each device (a kernel's attributes are those of one) that it may
+// be launched with so much LDS.
+template <auto* KERNEL>
+hipError_t allow_lds(int bytes) {
+  static std::atomic<uint64_t> allowed{0};
+  int device = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (allowed.load(std::memory_order_acquire) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) allowed.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 __device__ __forceinline__ int slot_of(int g, int m, int mix) { return (g * 16 + (m ^ (mix & 15))) * 16; }
 
