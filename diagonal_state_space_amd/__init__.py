@@ -584,7 +584,8 @@ def gated_delta(q, k, v, g, beta, s0=None, *, scale=None, lengths=None, final_st
     Dk ** -0.5. lengths [B] int32: the valid steps of each sequence; rows of y
     behind them are zero in a y made here and left as they were in a given one.
     Returns (y, s_last), s_last None unless final_state is set or a buffer is
-    given (which may be s0)."""
+    given (which may be s0). Inputs that require gradients are taken, but the
+    results carry no autograd graph: gated_delta_backward gives the gradients."""
     import torch
     on = _on(v, stream, "v")
     if on is not None:
@@ -608,7 +609,9 @@ def gated_delta_backward(dy, q, k, v, g, beta, s0=None, ds_last=None, *, scale=N
     of y, and ds_last, that of the last state (None: zero); the forward pass is
     computed again, nothing is kept from it. Returns (dq, dk, dv, dg, dbeta,
     ds0), ds0 None unless s0 or a buffer for it is given. With lengths the
-    rows behind are zero in gradients made here and left in given ones."""
+    rows behind are zero in gradients made here and left in given ones. It
+    allocates 4.5 KB (float32: 8.8) for each step and head of 128 x 128 while it
+    runs, up to 4 GiB (s5_gated_delta_workspace)."""
     import torch
     on = _on(v, stream, "v")
     if on is not None:
@@ -637,7 +640,7 @@ def gated_delta_backward(dy, q, k, v, g, beta, s0=None, ds_last=None, *, scale=N
 def gated_delta_step(q, k, v, g, beta, s, *, scale=None, y=None, stream=None):
     """One token of gated_delta for each of B sequences (s5_gated_delta_step):
     q, k [B, Hk, Dk], v [B, Hv, Dv], g, beta [B, Hv]; s [B, Hv, Dk, Dv] float32
-    is updated in place. Returns y [B, Hv, Dv]."""
+    is updated in place. Returns y [B, Hv, Dv], without an autograd graph."""
     import torch
     on = _on(v, stream, "v")
     if on is not None:
@@ -713,7 +716,8 @@ def qk_norm_rope(q, k, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, fr
     radians per position (rope_frequencies), None: no rotation; pairs are
     (j, j + R/2), or (2j, 2j + 1) if interleaved. positions int32, shaped as
     the tokens; None counts 0, 1, ... along L (T). Returns contiguous
-    (q_out, k_out); a contiguous input may be its own output."""
+    (q_out, k_out); a contiguous input may be its own output. The results carry
+    no autograd graph: qk_norm_rope_backward gives the gradients."""
     on = _on(q, stream, "q")
     if on is not None:
         with on:

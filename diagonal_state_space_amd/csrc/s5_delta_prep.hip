@@ -336,10 +336,10 @@ namespace {
 // many as the estimate below favours, in microseconds as measured (128 or 64
 // features of a key): a chunk's pass for outputs and for a segment's sums with a
 // workgroup on few units (with one on each they take 1.35 times as long), a
-// segment's join. Over 160 calls (1 to 48 heads of 1024 to 8192 steps, 64 and 128
-// features, both types) its choice took 0.6 % longer than the best of eleven
-// numbers on average and 13 % at most; one head of 8192 steps, 128 x 128, bf16:
-// 384 us in one piece, 107 in 16.
+// segment's join. Over 148 calls (1 to 48 heads of 1024 to 8192 steps, 64 and 128
+// features, both types, both directions) its choice took 0.7 % longer than the best
+// of eleven numbers on average and 10 % at most; one head of 8192 steps, 128 x 128,
+// bf16: 429 us in one piece, 108 in 16.
 int segments_of(int64_t heads, int dvp, int dkp, int chunks, bool bf16) {
   const bool wide = dkp > 64;
   const double out = bf16 ? (wide ? 2.8 : 2.2) : (wide ? 2.1 : 1.5), sum = bf16 ? (wide ? 2.1 : 1.65) : (wide ? 1.6 : 1.1);
