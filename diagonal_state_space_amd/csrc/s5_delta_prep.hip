@@ -20,8 +20,8 @@
 //
 // What bounds it: each workgroup's chain of loads, products, substitution and
 // stores, of which four are on a compute unit; 128 x 128 bf16, 1 x 8192 steps of
-// 16 heads: 28 us for 2048 chunks (31 KB of record each, 3.3 TB/s in and out),
-// with the gradients' records (55 KB) and fragments 48 us (3.8 TB/s).
+// 16 heads: 27 us for 2048 chunks (37 KB of record each, 4.2 TB/s in and out),
+// with the gradients' records (55 KB) and fragments 47 us (4 TB/s).
 #include "s5_delta_tile.h"
 
 namespace s5 {
@@ -333,7 +333,7 @@ namespace {
 
 // Segments of a call: none where the chain's workgroups (64 columns of a head
 // each) fill half of the compute units or the sequence is short; otherwise as
-// many as the estimate below favours, in microseconds as measured (128 or 64
+// many as the estimate below favours, in microseconds fitted to calls (128 or 64
 // features of a key): a chunk's pass for outputs and for a segment's sums with a
 // workgroup on few units (with one on each they take 1.35 times as long), a
 // segment's join. Over 148 calls (1 to 48 heads of 1024 to 8192 steps, 64 and 128

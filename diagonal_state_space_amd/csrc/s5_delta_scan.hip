@@ -18,11 +18,11 @@
 // of 8 ragged sequences of 2048 steps, 16 heads of 128 x 128 (172 -> 183 us).
 //
 // What bounds it: the chain itself, with one wave on a SIMD (the LDS has room for
-// one workgroup on a compute unit). Of 7550 cycles for a chunk of 64 steps (128 x
-// 128 bf16, outputs) matrix instructions take 3500 and vector instructions, four
-// cycles each and most of them splits into parts, 2900; neither can start
-// before the other's results. 64 heads of 2048 steps: outputs 110 us, states and
-// U for the gradients 91; 128 heads: 117.
+// one workgroup on a compute unit). Of 7900 cycles for a chunk of 64 steps (128 x
+// 128 bf16, outputs) matrix instructions take 4000, and vector instructions, four
+// cycles each and most of them splits into parts, 3000; neither can start
+// before the other's results. 64 heads of 2048 steps: outputs 119 us, states and
+// U for the gradients 91; 128 heads (ragged): 131.
 //
 // A value that is not finite must not reach earlier steps through a zero of T
 // or P: rows from the first such one on are taken out of R for this column and

@@ -16,10 +16,11 @@ namespace delta {
 // ---- float32 values as bf16 parts ----------------------------------------------
 // A float32 is the sum of three bf16 values exactly (three times 8 of its 24
 // bits, each cut off the rest), so products of float32 operands run on the
-// bf16 matrix instructions: the six part products above 2^-24 of the result
-// for two float32 operands, three for one with a bf16 operand. Measured
-// alternatives: two parts leave 3e-6 in the float32 state, the float32 matrix
-// instruction takes 8 x 32 cycles where six bf16 ones take 6 x 16.
+// bf16 matrix instructions: three part products for one with a bf16 operand
+// (exact), six for two float32 operands. The two that would come next are left
+// out, 2^-24.5 of a product on average (2^-21 at most): less than its rounding.
+// Measured alternatives: two parts leave 3e-6 in the float32 state, the float32
+// matrix instruction takes 8 x 32 cycles where six bf16 ones take 6 x 16.
 
 __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
